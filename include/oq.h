@@ -498,6 +498,134 @@ int oq_gemm_w4a4_asym(int afmt, const uint8_t *qa, const float *a_scale, const u
 int oq_kron_plan(int32_t n, int32_t *m, int32_t *block, int32_t *n_pad);
 
 /*
+ * 8-bit weights: layers that do not tolerate 4 bits keep int8 codes with one
+ * scale per output row, behind the same rotation, centering and activation
+ * codes (oq_quant_act OQ_A8 or OQ_A6) as the INT4 layers.
+ */
+
+/*
+ * oq_quant_weight_w8 -- offline: rotate each row as oq_quant_weight does, then
+ * symmetric absmax INT8 per row: scale[o] = RN32(a / 127) with a = max(max_j
+ * |v_oj|, RN32(1e-10)), codes clamp(RNE(RN32(v RN32(127 / a))), -127, 127).
+ * codes int8 [N][ldc_bytes], rows of the rotated width (padded for the
+ * Kronecker rotation), 16-byte aligned; scales float32 [N]; w1 (nullable) as
+ * oq_quant_weight.  rot: RPBH, Kronecker or NULL.  K % 16 == 0.
+ */
+int oq_quant_weight_w8(const float *w, int32_t N, int32_t K, int64_t ldw, const oq_rot *rot, int8_t *codes,
+                       int64_t ldc_bytes, float *scales, float *w1, hipStream_t stream);
+
+/*
+ * oq_gemm_w8a8 -- int8 activations times int8 weights:
+ *   y[t][o] = bf16_RNE( a_scale[t] * w_scale[o] * acc[t][o] + mean[t] * w1[o] + bias[o] )
+ *   acc = exact int32 sum over K, converted to float32 with one rounding.
+ * qa int8 [M][lda]; a_scale float32 [M]; w int8 [N][ldw]; w_scale float32 [N];
+ * mean and w1 both NULL or both set; bias nullable; y bf16 [M][ldy].
+ * Any M, N >= 0 (zero enqueues nothing); K a multiple of 16, 16 <= K <=
+ * 131056 (the int32 sum cannot overflow, codes of -128 included); lda, ldw
+ * multiples of 16; qa and w 16-byte aligned.  No scratch.  The result does
+ * not depend on the tile that the library picks from M, N, K and the CU count.
+ */
+int oq_gemm_w8a8(const int8_t *qa, int64_t lda, const float *a_scale, int64_t M, int32_t K, const int8_t *w,
+                 int64_t ldw, const float *w_scale, int32_t N, const float *mean, const float *w1, const float *bias,
+                 uint16_t *y, int64_t ldy, hipStream_t stream);
+
+/*
+ * Between the projections of an attention layer: per-head norm and rotary
+ * embedding of queries and keys, a paged cache of keys and values, and
+ * attention over it.  Heads are bfloat16 vectors of d consecutive elements;
+ * element (token t, head h) of a tensor starts at base + t ld + h hs
+ * (elements; every start 16-byte aligned, so ld, hs and d multiples of 8).
+ */
+
+/*
+ * Rotary embedding (host struct, device arrays): the pair (a, b) of a head at
+ * position p becomes (a cos[p][i] - b sin[p][i], b cos[p][i] + a sin[p][i]),
+ * i = 0 .. dim/2 - 1, on elements (i, i + dim/2), or (2i, 2i + 1) with
+ * interleaved != 0; elements dim .. d - 1 stay.  cos, sin: float32
+ * [rows][dim/2], 4-byte aligned.  dim even, 2 <= dim <= d.
+ */
+typedef struct {
+  const float *cos;
+  const float *sin;
+  int64_t rows;
+  int32_t dim;
+  int32_t interleaved;
+} oq_rope;
+
+/*
+ * Paged cache (host struct, device arrays): page p of k and of v starts at
+ * base + p page_stride (elements, a multiple of 8, >= heads * page * d) and
+ * holds [heads][page][d].  page: a power of two in [8, 1024].  k and v may be
+ * parts of one allocation (pages of both interleaved); a cache may pass 4 GiB.
+ */
+typedef struct {
+  uint16_t *k;
+  uint16_t *v;
+  int64_t page_stride;
+  int32_t pages;
+  int32_t page;
+  int32_t heads;
+  int32_t d;
+} oq_kv;
+
+/*
+ * oq_qk_norm_rope -- for every head x of every token, query and key heads in
+ * one launch:  n = x / sqrt(mean(x^2) + eps) * w  (w float32 [d]; NULL: n = x),
+ * then the rotary embedding at position pos[t] (pos int32 [T]; NULL: t; rope
+ * NULL: none), rounded once to bfloat16 (float32 inside).
+ * q: heads_q heads of T tokens (heads_q 0: none, q NULL); k the same.  Outputs
+ * have their own strides; out == in with the same strides works in place.
+ * A position outside [0, rope->rows) gives NaN in that token's rows.
+ * d a multiple of 8, 8 <= d <= 512.  eps >= 0, finite.
+ */
+int oq_qk_norm_rope(const uint16_t *q, int64_t q_ld, int64_t q_hs, int32_t heads_q, const uint16_t *k, int64_t k_ld,
+                    int64_t k_hs, int32_t heads_k, int64_t T, int32_t d, const float *w_q, const float *w_k, float eps,
+                    const oq_rope *rope, const int32_t *pos, uint16_t *q_out, int64_t qo_ld, int64_t qo_hs,
+                    uint16_t *k_out, int64_t ko_ld, int64_t ko_hs, hipStream_t stream);
+
+/*
+ * oq_kv_append -- token t's keys, through the norm (w_k NULL: none) and rotary
+ * embedding (rope NULL: none) of oq_qk_norm_rope, and its values as they are,
+ * go to slot[t] of the cache: page slot / page, place slot % page, all
+ * kv->heads heads of kv->d.  slot int64 [T]; a slot outside [0, pages * page)
+ * writes nothing (padding tokens carry -1).  Two tokens of one call must not
+ * share a slot.  kv->d <= 512.
+ */
+int oq_kv_append(const uint16_t *k, int64_t k_ld, int64_t k_hs, const uint16_t *v, int64_t v_ld, int64_t v_hs,
+                 int64_t T, const float *w_k, float eps, const oq_rope *rope, const int32_t *pos, const int64_t *slot,
+                 const oq_kv *kv, hipStream_t stream);
+
+/*
+ * oq_attn_prefix -- attention of B sequences that share prefix_len cached
+ * tokens, each followed by a suffix of its own.  Sequence b has n_q query
+ * tokens t = b n_q + i (decode: n_q = 1), the last tokens of its suffix:
+ * token i sees the whole prefix and the suffix places j < lens[b] - n_q + 1 + i.
+ *   o[t][h] = sum_j p_j v_j,  p = softmax_j(scale q[t][h] . k_j)
+ * over the seen keys of key head h / (heads_q / kv->heads); a row that sees
+ * no key gives zeros and lse -inf.  lse (nullable) float32 [B n_q][heads_q]:
+ * log sum_j exp(scale q . k_j).
+ * prefix_table int32 [ceil(prefix_len / page)], tables int32 [B][table_ld]:
+ * page numbers in order; lens int32 [B], at most table_ld * page places are
+ * read.  Keys on a page number outside [0, pages) are left out.  Cache places
+ * that a row does not see may hold anything, NaN included.
+ * The prefix is read once for all rows of a tile; scores, statistics and sums
+ * are float32; softmax numerators enter the value product as bfloat16 (their
+ * sum is of the float32 values).
+ * d (kv->d) 64 or 128; heads_q a multiple of kv->heads; scale finite.
+ * ws: device scratch of oq_attn_prefix_ws_bytes(B, n_q, heads_q, kv,
+ * prefix_len, table_ld) bytes, 16-byte aligned (may be 0).
+ */
+int oq_attn_prefix(const uint16_t *q, int64_t q_ld, int64_t q_hs, int32_t B, int32_t n_q, int32_t heads_q,
+                   const oq_kv *kv, const int32_t *prefix_table, int32_t prefix_len, const int32_t *tables,
+                   int32_t table_ld, const int32_t *lens, float scale, uint16_t *o, int64_t o_ld, int64_t o_hs,
+                   float *lse, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* Scratch bytes of oq_attn_prefix (0 for arguments it refuses).  Pure host
+ * function of the sizes and the device's CU count. */
+size_t oq_attn_prefix_ws_bytes(int32_t B, int32_t n_q, int32_t heads_q, const oq_kv *kv, int32_t prefix_len,
+                               int32_t table_ld);
+
+/*
  * oq_probe_mfma -- measurement helper, not part of the layer: the rate one
  * matrix-core instruction sustains on the calling device at its current clock
  * (a roofline denominator beside the published dense peak, which assumes the

@@ -50,6 +50,7 @@ def _load():
         raise ImportError(f"liboq.so is not built ({LIB_PATH}); run __graft_entry__.build()")
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    f32 = ctypes.c_float
     sig = {
         "oq_last_error": ([], ctypes.c_char_p),
         "oq_center": ([vp, i64, i32, i64, vp, i64, vp, vp], ctypes.c_int),
@@ -82,6 +83,14 @@ def _load():
         "oq_gemm_w4a4_asym": ([ctypes.c_int, vp, vp, vp, i64, i32, vp, vp, vp, i32, vp, vp, vp, vp, i64, vp],
                               ctypes.c_int),
         "oq_kron_plan": ([i32, vp, vp, vp], ctypes.c_int),
+        "oq_quant_weight_w8": ([vp, i32, i32, i64, vp, vp, i64, vp, vp, vp], ctypes.c_int),
+        "oq_gemm_w8a8": ([vp, i64, vp, i64, i32, vp, i64, vp, i32, vp, vp, vp, vp, i64, vp], ctypes.c_int),
+        "oq_qk_norm_rope": ([vp, i64, i64, i32, vp, i64, i64, i32, i64, i32, vp, vp, f32, vp, vp, vp, i64, i64, vp, i64,
+                             i64, vp], ctypes.c_int),
+        "oq_kv_append": ([vp, i64, i64, vp, i64, i64, i64, vp, f32, vp, vp, vp, vp, vp], ctypes.c_int),
+        "oq_attn_prefix": ([vp, i64, i64, i32, i32, i32, vp, vp, i32, vp, i32, vp, f32, vp, i64, i64, vp, vp, sz, vp],
+                           ctypes.c_int),
+        "oq_attn_prefix_ws_bytes": ([i32, i32, i32, vp, i32, i32], sz),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -96,7 +105,8 @@ EXPORTED = ("oq_last_error", "oq_center", "oq_rotate", "oq_quant_act", "oq_quant
             "oq_prepack_w4", "oq_tiled_mx_bytes", "oq_prepack_mx", "oq_lloyd_max_levels", "oq_lloyd_max_tables",
             "oq_tiled_f16_bytes", "oq_quant_act_lm", "oq_prepack_w16", "oq_gemm_lm", "oq_quant_weight_asym",
             "oq_prepack_w4_asym", "oq_quant_act_gsum", "oq_gemm_w4a4_asym", "oq_kron_plan",
-            "oq_linear_fused_noalloc", "oq_probe_mfma", "oq_probe_sink_elems")
+            "oq_linear_fused_noalloc", "oq_probe_mfma", "oq_probe_sink_elems", "oq_quant_weight_w8", "oq_gemm_w8a8",
+            "oq_qk_norm_rope", "oq_kv_append", "oq_attn_prefix", "oq_attn_prefix_ws_bytes")
 
 
 def lib():
@@ -581,3 +591,189 @@ def oq_kron_plan(n: int):
     m, b, p = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32()
     _check(_lib.oq_kron_plan(n, ctypes.byref(m), ctypes.byref(b), ctypes.byref(p)))
     return m.value, b.value, p.value
+
+
+# ---------------------------------------------------------------- 8-bit weights
+def oq_quant_weight_w8(w, rot: Optional[Rotation] = None, codes=None, scales=None, w1=None, want_w1: bool = False):
+    if w.dim() != 2 or w.dtype != torch.float32 or w.stride(1) != 1:
+        raise OQError(OQ_ERR_INVALID_ARG, "w must be a float32 matrix with unit column stride")
+    N, K = w.shape
+    dev = _dev(w)
+    Kq = rot.width if rot is not None else K
+    if codes is None:
+        codes = torch.empty((N, Kq), dtype=torch.int8, device=dev)
+    elif not codes.is_cuda or codes.dtype != torch.int8 or codes.dim() != 2 or codes.shape[0] < N \
+            or codes.shape[1] < Kq or codes.stride(1) != 1:
+        raise OQError(OQ_ERR_INVALID_ARG, f"codes must be a GPU int8 matrix of at least {N} x {Kq}")
+    if scales is None:
+        scales = torch.empty(N, dtype=torch.float32, device=dev)
+    if want_w1 and w1 is None:
+        w1 = torch.empty(N, dtype=torch.float32, device=dev)
+    _need(scales, 4 * N, "scales", _F32)
+    _need(w1, 4 * N, "w1", _F32, optional=True)
+    _check(_lib.oq_quant_weight_w8(_p(w), N, K, w.stride(0), _rref(rot), _p(codes), codes.stride(0), _p(scales),
+                                   _p(w1), _stream()))
+    return {"codes": codes, "scales": scales, "w1": w1}
+
+
+def oq_gemm_w8a8(qa, a_scale, w, w_scale, mean=None, w1=None, bias=None, y=None):
+    """qa int8 [M][K] (oq_quant_act OQ_A8 or OQ_A6 codes), w int8 [N][K] (oq_quant_weight_w8)."""
+    if qa.dim() != 2 or w.dim() != 2 or qa.dtype != torch.int8 or w.dtype != torch.int8:
+        raise OQError(OQ_ERR_INVALID_ARG, "qa and w must be int8 matrices")
+    (M, K), (N, Kw) = qa.shape, w.shape
+    (lda, ca), (ldw, cw) = qa.stride(), w.stride()
+    if K != Kw or ca != 1 or cw != 1:
+        raise OQError(OQ_ERR_INVALID_ARG, f"qa [M][K] and w [N][K] with unit column strides, got {qa.shape} and {w.shape}")
+    if not (qa.is_cuda and w.is_cuda):
+        raise OQError(OQ_ERR_INVALID_ARG, "tensors must live on the GPU")
+    _need(a_scale, 4 * M, "a_scale", _F32)
+    _need(w_scale, 4 * N, "w_scale", _F32)
+    if mean is not None or w1 is not None or bias is not None:
+        _epilogue_args(M, N, mean, w1, bias)
+    y = _out_y(y, M, N, qa.device)
+    # a matrix of one row has no row stride to speak of
+    _check(_lib.oq_gemm_w8a8(qa.data_ptr(), lda if M > 1 else (K + 15) // 16 * 16, a_scale.data_ptr(), M, K, w.data_ptr(),
+                             ldw if N > 1 else (K + 15) // 16 * 16, w_scale.data_ptr(), N, _p(mean), _p(w1), _p(bias),
+                             y.data_ptr(), y.stride(0) if y.shape[0] > 1 else N, _stream()))
+    return y
+
+
+# ---------------------------------------------------------------- heads, cache, attention
+class oq_rope(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("rows", ctypes.c_int64), ("dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
+class oq_kv(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("pages", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("heads", ctypes.c_int32), ("d", ctypes.c_int32)]
+
+
+class Rope:
+    """Rotary tables cos, sin (float32 [rows][dim / 2], kept alive here) and the order of the pairs."""
+
+    def __init__(self, cos: torch.Tensor, sin: torch.Tensor, interleaved: bool = False):
+        if cos.dim() != 2 or cos.shape != sin.shape:
+            raise OQError(OQ_ERR_INVALID_ARG, "cos and sin must be matrices of one shape")
+        for t, what in ((cos, "cos"), (sin, "sin")):
+            _need(t, 0, what, _F32)
+        self.cos, self.sin, self.interleaved = cos, sin, interleaved
+        self.c = oq_rope(cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1], int(interleaved))
+        self.ref = ctypes.byref(self.c)
+
+
+class PagedKV:
+    """A paged cache: k and v bfloat16 [pages][heads][page][d] (kept alive
+    here), contiguous but for one stride from page to page shared by both."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        for t, what in ((k, "k"), (v, "v")):
+            if not t.is_cuda or t.dtype not in _BF16 or t.dim() != 4:
+                raise OQError(OQ_ERR_INVALID_ARG, f"{what} must be a GPU bfloat16 tensor [pages][heads][page][d]")
+            if t.stride()[1:] != (t.shape[2] * t.shape[3], t.shape[3], 1):
+                raise OQError(OQ_ERR_INVALID_ARG, f"the pages of {what} must be contiguous")
+        if k.shape != v.shape or k.stride() != v.stride() or k.device != v.device:
+            raise OQError(OQ_ERR_INVALID_ARG, "k and v must have one shape, stride and device")
+        self.k, self.v = k, v
+        self.pages, self.heads, self.page, self.d = k.shape
+        self.c = oq_kv(k.data_ptr(), v.data_ptr(), k.stride(0), self.pages, self.page, self.heads, self.d)
+        self.ref = ctypes.byref(self.c)
+
+
+def _heads(t: torch.Tensor, what: str):
+    """(address, token stride, head stride) of a GPU bfloat16 tensor [T][heads][d]."""
+    if t.dim() != 3 or not t.is_cuda or t.dtype not in _BF16:
+        raise OQError(OQ_ERR_INVALID_ARG, f"{what} must be a GPU bfloat16 tensor [T][heads][d]")
+    ld, hs, es = t.stride()
+    if es != 1 and t.shape[2] > 1:
+        raise OQError(OQ_ERR_INVALID_ARG, f"{what} must have unit stride within a head")
+    T, H, d = t.shape
+    # the stride over a single token or head is never used
+    return t.data_ptr(), ld if T > 1 else 0, hs if H > 1 else 0
+
+
+def _same(t: torch.Tensor, shape, what: str):
+    if tuple(t.shape) != tuple(shape):
+        raise OQError(OQ_ERR_INVALID_ARG, f"{what} has shape {tuple(t.shape)}, {tuple(shape)} needed")
+
+
+_I32, _I64 = (torch.int32,), (torch.int64,)
+
+
+def oq_qk_norm_rope(q, k, w_q=None, w_k=None, eps: float = 1e-6, rope: Optional[Rope] = None, pos=None, q_out=None,
+                    k_out=None):
+    """q [T][heads_q][d], k [T][heads_k][d] (either may be None), any token and
+    head strides; returns (q_out, k_out).  Passing q as q_out works in place."""
+    x = q if q is not None else k
+    if x is None:
+        raise OQError(OQ_ERR_INVALID_ARG, "q or k is required")
+    T, _, d = x.shape
+    args = [None, 0, 0, 0, None, 0, 0, 0]
+    outs = [None, 0, 0, None, 0, 0]
+    if q is not None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        _same(q_out, q.shape, "q_out")
+        args[0:4] = *_heads(q, "q"), q.shape[1]
+        outs[0:3] = _heads(q_out, "q_out")
+    if k is not None:
+        if q is not None and (k.shape[0] != T or k.shape[2] != d):
+            raise OQError(OQ_ERR_INVALID_ARG, f"q and k differ: {tuple(q.shape)}, {tuple(k.shape)}")
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
+        _same(k_out, k.shape, "k_out")
+        args[4:8] = *_heads(k, "k"), k.shape[1]
+        outs[3:6] = _heads(k_out, "k_out")
+    _need(w_q, 4 * d, "w_q", _F32, optional=True)
+    _need(w_k, 4 * d, "w_k", _F32, optional=True)
+    _need(pos, 4 * T, "pos", _I32, optional=True)
+    _check(_lib.oq_qk_norm_rope(*args, T, d, _p(w_q), _p(w_k), eps, None if rope is None else rope.ref, _p(pos), *outs,
+                                _stream()))
+    return q_out, k_out
+
+
+def oq_kv_append(k, v, slot, kv: PagedKV, w_k=None, eps: float = 1e-6, rope: Optional[Rope] = None, pos=None):
+    """k, v [T][heads][d] into the places slot (int64 [T], negative: skipped) of the cache."""
+    T = k.shape[0]
+    _same(k, (T, kv.heads, kv.d), "k")
+    _same(v, (T, kv.heads, kv.d), "v")
+    _need(slot, 8 * T, "slot", _I64)
+    _need(w_k, 4 * kv.d, "w_k", _F32, optional=True)
+    _need(pos, 4 * T, "pos", _I32, optional=True)
+    _check(_lib.oq_kv_append(*_heads(k, "k"), *_heads(v, "v"), T, _p(w_k), eps, None if rope is None else rope.ref, _p(pos),
+                             slot.data_ptr(), kv.ref, _stream()))
+
+
+def oq_attn_prefix_ws_bytes(B: int, n_q: int, heads_q: int, kv: PagedKV, prefix_len: int, table_ld: int) -> int:
+    return int(_lib.oq_attn_prefix_ws_bytes(B, n_q, heads_q, kv.ref, prefix_len, table_ld))
+
+
+def oq_attn_prefix(q, n_q: int, kv: PagedKV, prefix_table, prefix_len: int, tables, lens, scale: float, o=None, lse=None,
+                   ws=None, want_lse: bool = False):
+    """q [B n_q][heads_q][d]; prefix_table int32 [>= ceil(prefix_len / page)] (None
+    without a prefix); tables int32 [B][table_ld] and lens int32 [B] (both None
+    without suffixes); returns (o, lse)."""
+    T, heads_q, d = q.shape
+    if n_q < 1 or T % n_q or d != kv.d:
+        raise OQError(OQ_ERR_INVALID_ARG, f"q of shape {tuple(q.shape)} for n_q={n_q} and heads of {kv.d}")
+    B = T // n_q
+    _need(prefix_table, 4 * (-(-prefix_len // kv.page)), "prefix_table", _I32, optional=prefix_len <= 0)
+    table_ld = 0
+    if tables is not None:
+        if tables.dim() != 2 or tables.shape[0] != B:
+            raise OQError(OQ_ERR_INVALID_ARG, f"tables must be a matrix of {B} rows")
+        table_ld = tables.shape[1]
+        _need(tables, 0, "tables", _I32)
+        _need(lens, 4 * B, "lens", _I32)
+    if o is None:
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _same(o, q.shape, "o")
+    if lse is None and want_lse:
+        lse = torch.empty((T, heads_q), dtype=torch.float32, device=q.device)
+    _need(lse, 4 * T * heads_q, "lse", _F32, optional=True)
+    if ws is None:
+        ws = torch.empty(oq_attn_prefix_ws_bytes(B, n_q, heads_q, kv, prefix_len, table_ld), dtype=torch.uint8, device=q.device)
+    elif not ws.is_cuda or not ws.is_contiguous():
+        raise OQError(OQ_ERR_INVALID_ARG, "ws must be a contiguous GPU tensor")
+    _check(_lib.oq_attn_prefix(*_heads(q, "q"), B, n_q, heads_q, kv.ref, _p(prefix_table), prefix_len, _p(tables), table_ld,
+                               _p(lens), scale, *_heads(o, "o"), _p(lse), ws.data_ptr(), ws.numel() * ws.element_size(),
+                               _stream()))
+    return o, lse

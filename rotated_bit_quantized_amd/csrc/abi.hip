@@ -32,14 +32,14 @@ int fail(int code, const char *fmt, ...) {
   return code;
 }
 
-namespace {
-
-inline bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 int hip_status(hipError_t e, const char *what) {
   if (e == hipSuccess) return OQ_OK;
   return fail(OQ_ERR_HIP, "%s: HIP error %d (%s)", what, (int)e, hipGetErrorString(e));
 }
+
+namespace {
+
+inline bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool is_pow2(int v) { return v > 0 && (v & (v - 1)) == 0; }
 
@@ -53,6 +53,8 @@ int check_x(const char *fn, const uint16_t *x, int64_t M, int d, int64_t ldx) {
   if (!al16(x) || (ldx * 2) % 16) return fail(OQ_ERR_ALIGNMENT, "%s: x rows must be 16-byte aligned", fn);
   return OQ_OK;
 }
+
+}  // namespace
 
 // Fills RotArgs from an RPBH descriptor (or identity when rot == NULL).
 int rot_args(const char *fn, const oq_rot *rot, int d, RotArgs *ra) {
@@ -91,6 +93,8 @@ int rot_args(const char *fn, const oq_rot *rot, int d, RotArgs *ra) {
   ra->c_h = (float)(1.0 / std::sqrt((double)rot->block));
   return OQ_OK;
 }
+
+namespace {
 
 int check_dense(const char *fn, const oq_rot *rot, int d) {
   if (rot->d != d) return fail(OQ_ERR_INVALID_ARG, "%s: rot->d=%d differs from d=%d", fn, rot->d, d);

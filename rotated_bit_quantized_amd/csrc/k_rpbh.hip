@@ -131,7 +131,7 @@ rpbh_quant_kernel(const void *__restrict__ xin, int64_t M, int d, int64_t ldx,
       for (int j = 0; j < E; ++j) v[j] = 0.f;
     }
 
-    if (MODE == OUT_W4G || MODE == OUT_W4A) {
+    if (MODE == OUT_W4G || MODE == OUT_W4A || (MODE == OUT_I8 && IN_F32)) {
       if (mean_out) {  // w1 = row sum of the unrotated weight, float64 then RN32
         double s = 0.0;
 #pragma unroll
@@ -452,6 +452,20 @@ hipError_t launch_weight_rpbh_asym(const float *w, int N, int K, int64_t ldw, co
     case 0: return launch_t<0, OUT_W4A, true>(w, N, K, ldw, rot, 0, w1, 0, codes, K / 2, sg, group, stream, zero);
     case 1: return launch_t<1, OUT_W4A, true>(w, N, K, ldw, rot, 0, w1, 0, codes, K / 2, sg, group, stream, zero);
     case 2: return launch_t<2, OUT_W4A, true>(w, N, K, ldw, rot, 0, w1, 0, codes, K / 2, sg, group, stream, zero);
+  }
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_weight_rpbh_w8(const float *w, int N, int K, int64_t ldw, const RotArgs &rot, int8_t *codes,
+                                 int64_t ldc_bytes, float *scales, float *w1, hipStream_t stream) {
+  if (N == 0) return hipSuccess;
+  if (rot.kron_m)
+    return launch_t<1, OUT_I8, true, true>(w, N, rot_out_width(rot, K), ldw, rot, 0, w1, 127, codes, ldc_bytes, scales,
+                                           0, stream, nullptr, K);
+  switch (rot.rounds) {
+    case 0: return launch_t<0, OUT_I8, true>(w, N, K, ldw, rot, 0, w1, 127, codes, ldc_bytes, scales, 0, stream);
+    case 1: return launch_t<1, OUT_I8, true>(w, N, K, ldw, rot, 0, w1, 127, codes, ldc_bytes, scales, 0, stream);
+    case 2: return launch_t<2, OUT_I8, true>(w, N, K, ldw, rot, 0, w1, 127, codes, ldc_bytes, scales, 0, stream);
   }
   return hipErrorInvalidValue;
 }

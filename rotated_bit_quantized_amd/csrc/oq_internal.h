@@ -30,6 +30,7 @@ inline hipError_t lds_limit_once(const void *kern, int bytes, std::atomic<bool> 
 // ------------------------------------------------------------------ errors --
 void set_error(const char *fmt, ...);
 int fail(int code, const char *fmt, ...);
+int hip_status(hipError_t e, const char *what);  // OQ_OK, or OQ_ERR_HIP with a message
 
 // ------------------------------------------------------- numeric helpers --
 __device__ __forceinline__ float bf16_lo(uint32_t pair) { return __uint_as_float(pair << 16); }
@@ -157,6 +158,10 @@ struct RotArgs {
   float c_h;             // RN32(1/sqrt h); for the Kronecker rotation RN32(1/sqrt(m h))
   int kron_m = 0;        // 0: RPBH rounds; else the order m of the Paley factor of (H_m (x) H_h)
 };
+
+// Fills RotArgs from an RPBH or Kronecker descriptor of width d (identity when
+// rot is NULL); an OQ_ERR_* code, with its message set, where it does not fit.
+int rot_args(const char *fn, const oq_rot *rot, int d, RotArgs *ra);
 
 // width of the rotated (and quantized) row: the padded m h for the Kronecker rotation
 inline int rot_out_width(const RotArgs &ra, int d) { return ra.kron_m ? ra.kron_m * ra.block : d; }
@@ -305,8 +310,59 @@ hipError_t launch_weight_rpbh(const float *w, int N, int K, int64_t ldw, const R
 // [N][K/2], bfloat16 scale and shift [N][K/group] each
 hipError_t launch_weight_rpbh_asym(const float *w, int N, int K, int64_t ldw, const RotArgs &rot, int group,
                                    uint8_t *codes, uint16_t *sigma, uint16_t *zero, float *w1, hipStream_t stream);
+// symmetric INT8 per row: codes [N][ldc_bytes], one float32 scale per row
+hipError_t launch_weight_rpbh_w8(const float *w, int N, int K, int64_t ldw, const RotArgs &rot, int8_t *codes,
+                                 int64_t ldc_bytes, float *scales, float *w1, hipStream_t stream);
 hipError_t launch_weight_dense32(const float *w, int N, int K, int64_t ldw, const uint16_t *mats,
                                  uint8_t *codes, uint8_t *e8m0, float *w1, hipStream_t stream);
+
+// int8 activations x int8 weights, one scale per row of each (K % 16 == 0).
+hipError_t launch_gemm_w8a8(const int8_t *qa, int64_t lda, const float *a_scale, int64_t M, int K, const int8_t *w,
+                            int64_t ldw, const float *w_scale, int N, const float *mean, const float *w1,
+                            const float *bias, uint16_t *y, int64_t ldy, hipStream_t stream);
+
+// Heads of T tokens through norm and rotary embedding, into dense rows or the
+// slots of a paged cache: what one launch does with one group of heads.
+struct HeadPart {
+  const uint16_t *x = nullptr;  // head h of token t at x + t ld + h hs
+  int64_t ld = 0, hs = 0;
+  int heads = 0;
+  const float *w = nullptr;  // norm weights [d], or NULL for no norm
+  bool rope = false;
+  uint16_t *out = nullptr;   // dense: out + t out_ld + h out_hs; cache: the k or v base
+  int64_t out_ld = 0, out_hs = 0;
+};
+struct HeadArgs {
+  HeadPart part[2];
+  int64_t T = 0;
+  int d = 0;
+  float eps = 0.f;
+  oq_rope rope = {nullptr, nullptr, 0, 0, 0};
+  const int32_t *pos = nullptr;
+  const int64_t *slot = nullptr;  // set: outputs go to the slots of a cache of these dimensions
+  int64_t page_stride = 0, slots = 0;
+  int page_log2 = 0, cache_heads = 0;
+};
+hipError_t launch_heads(const HeadArgs &a, hipStream_t stream);
+
+// Shared-prefix attention (arguments as oq_attn_prefix, already validated).
+struct AttnArgs {
+  const uint16_t *q;
+  int64_t q_ld, q_hs;
+  int B, n_q, heads_q;
+  oq_kv kv;
+  const int32_t *prefix_table;
+  int prefix_len;
+  const int32_t *tables;
+  int table_ld;
+  const int32_t *lens;
+  float scale;
+  uint16_t *o;
+  int64_t o_ld, o_hs;
+  float *lse;
+};
+size_t attn_prefix_ws(const AttnArgs &a);
+hipError_t launch_attn_prefix(const AttnArgs &a, void *ws, hipStream_t stream);
 
 // Compute units of the current device (cached per device).
 int device_cus();

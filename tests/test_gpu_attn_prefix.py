@@ -1,0 +1,263 @@
+"""Shared-prefix attention over a paged cache (oq_attn_prefix) against a
+64-bit softmax.
+
+Bound on one output: with S_j = |scale| sum_e |q_e k_je| a score is within
+(d + 4) 2^-24 S_j of the exact one (float32 sums of exact products, the
+scale), so every softmax weight within twice the largest such error, plus
+2^-8 for its rounding to bfloat16 and 2^-18 for the exponential, the running
+sums and the join; the result is rounded once more to bfloat16.  With A =
+sum_j p_j |v_j|:  |o - exact| <= 2^-8 |exact| + A (1.01 2^-8 + 2 (d + 4)
+2^-24 max S + 2^-18).  lse is within (d + 4) 2^-24 max S + 2^-20 (1 + |lse|)."""
+import math
+
+import pytest
+import torch
+
+import rotated_bit_quantized_amd as oq
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF = torch.bfloat16
+
+
+class Case:
+    def __init__(self, B, n_q, Hk, G, D, page, prefix, lens, seed=0, width=None, q_scale=1.0, spare=3):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        self.B, self.n_q, self.Hk, self.G, self.D, self.page, self.prefix = B, n_q, Hk, G, D, page, prefix
+        self.P, self.S = -(-prefix // page), -(-max(list(lens) + [0]) // page) if width is None else width
+        self.pages = self.P + B * self.S + spare
+        self.k = torch.randn(self.pages, Hk, page, D, generator=g, device=DEV).to(BF)
+        self.v = torch.randn(self.pages, Hk, page, D, generator=g, device=DEV).to(BF)
+        order = torch.randperm(self.pages, generator=g, device=DEV).int()
+        self.prefix_table = order[: self.P].contiguous()
+        self.tables = order[self.P : self.P + B * self.S].view(B, self.S).contiguous()
+        self.lens = torch.tensor(list(lens), dtype=torch.int32, device=DEV)
+        self.q = (torch.randn(B * n_q, Hk * G, D, generator=g, device=DEV) * q_scale).to(BF)
+        self.scale = 1 / math.sqrt(D)
+
+    def run(self, **kw):
+        kv = oq.PagedKV(self.k, self.v)
+        return oq.oq_attn_prefix(self.q, self.n_q, kv, self.prefix_table, self.prefix, self.tables if self.S else None,
+                                 self.lens if self.S else None, self.scale, want_lse=True, **kw)
+
+    def places(self, b, i):
+        """(page, offset) of the keys that query token i of sequence b sees."""
+        t = self.prefix_table.tolist()
+        seen = [(t[j // self.page], j % self.page) for j in range(self.prefix)]
+        t = self.tables[b].tolist()
+        n = min(int(self.lens[b]) - self.n_q + 1 + i, self.S * self.page)
+        seen += [(t[j // self.page], j % self.page) for j in range(max(0, n))]
+        return [(p, o) for p, o in seen if 0 <= p < self.pages]
+
+    def check(self, o, lse):
+        for b in range(self.B):
+            for i in range(self.n_q):
+                at = self.places(b, i)
+                t = b * self.n_q + i
+                if not at:
+                    assert (o[t] == 0).all() and (lse[t] == -math.inf).all()
+                    continue
+                idx = torch.tensor(at, device=DEV)
+                k, v = (c[idx[:, 0], :, idx[:, 1]].double().transpose(0, 1) for c in (self.k, self.v))  # [Hk][n][D]
+                q = self.q[t].double().view(self.Hk, self.G, self.D)
+                s = torch.matmul(q, k.transpose(1, 2).contiguous()) * self.scale
+                mag = (torch.matmul(q.abs(), k.abs().transpose(1, 2).contiguous()) * abs(self.scale)).amax(-1)
+                z = torch.logsumexp(s, -1)
+                p = torch.exp(s - z[..., None])
+                y, A = torch.matmul(p, v), torch.matmul(p, v.abs())
+                ds = (self.D + 4) * 2.0 ** -24 * mag
+                tol = 2.0 ** -8 * y.abs() + A * (1.01 * 2.0 ** -8 + 2 * ds[..., None] + 2.0 ** -18)
+                got = o[t].double().view(self.Hk, self.G, self.D)
+                off = (got - y).abs()
+                assert torch.isfinite(got).all(), (b, i)
+                assert (off <= tol).all(), f"sequence {b}, token {i}: {float((off / tol).max()):.2f} of the bound"
+                got = lse[t].double().view(self.Hk, self.G)
+                assert ((got - z).abs() <= ds + 2.0 ** -20 * (1 + z.abs())).all(), (b, i, float((got - z).abs().max()))
+
+
+CASES = [
+    # one sequence, one token, one key
+    dict(B=1, n_q=1, Hk=1, G=1, D=64, page=8, prefix=1, lens=[0]),
+    dict(B=1, n_q=1, Hk=1, G=1, D=128, page=16, prefix=0, lens=[1]),
+    dict(B=1, n_q=1, Hk=2, G=3, D=128, page=16, prefix=17, lens=[5]),
+    # rows with a prefix alone, a suffix alone, nothing at all
+    dict(B=3, n_q=1, Hk=2, G=4, D=128, page=16, prefix=100, lens=[0, 33, 7]),
+    dict(B=4, n_q=1, Hk=2, G=4, D=64, page=32, prefix=0, lens=[0, 1, 31, 95]),
+    dict(B=5, n_q=1, Hk=1, G=8, D=128, page=64, prefix=63, lens=[0, 0, 0, 0, 0]),
+    # lengths around the tiles and pages
+    dict(B=6, n_q=1, Hk=1, G=4, D=128, page=16, prefix=127, lens=[15, 16, 17, 31, 32, 33]),
+    dict(B=6, n_q=1, Hk=1, G=4, D=128, page=64, prefix=128, lens=[63, 64, 65, 127, 128, 129]),
+    dict(B=6, n_q=1, Hk=2, G=2, D=64, page=8, prefix=129, lens=[7, 8, 9, 255, 256, 257]),
+    dict(B=2, n_q=1, Hk=1, G=1, D=64, page=1024, prefix=1025, lens=[1500, 3]),
+    # several query tokens: causal at the end, some before the suffix begins
+    dict(B=3, n_q=2, Hk=2, G=4, D=128, page=16, prefix=50, lens=[2, 40, 1]),
+    dict(B=4, n_q=5, Hk=1, G=3, D=64, page=32, prefix=0, lens=[5, 77, 3, 0]),
+    dict(B=2, n_q=37, Hk=2, G=1, D=128, page=16, prefix=65, lens=[37, 200]),
+    dict(B=2, n_q=100, Hk=1, G=5, D=64, page=64, prefix=333, lens=[100, 150]),
+    # head layouts: many query heads a key head, none shared
+    dict(B=7, n_q=1, Hk=1, G=32, D=128, page=16, prefix=300, lens=[20, 1, 9, 64, 130, 11, 5]),
+    dict(B=9, n_q=1, Hk=16, G=1, D=64, page=16, prefix=200, lens=[3] * 9),
+    dict(B=3, n_q=1, Hk=3, G=5, D=128, page=128, prefix=511, lens=[100, 200, 128]),
+    # tiles of rows full and ragged, splits of the prefix
+    dict(B=64, n_q=1, Hk=2, G=4, D=128, page=64, prefix=2000, lens=[1 + 3 * b for b in range(64)]),
+    dict(B=65, n_q=1, Hk=1, G=2, D=64, page=32, prefix=4097, lens=[b % 7 for b in range(65)]),
+    dict(B=33, n_q=4, Hk=2, G=5, D=64, page=32, prefix=3000, lens=[4 + b for b in range(33)]),
+    dict(B=130, n_q=1, Hk=2, G=8, D=128, page=16, prefix=700, lens=[5 + b % 40 for b in range(130)]),
+    dict(B=2, n_q=1, Hk=2, G=4, D=128, page=64, prefix=20000, lens=[4000, 17]),
+    dict(B=1, n_q=1, Hk=8, G=4, D=64, page=16, prefix=9001, lens=[9001]),
+    dict(B=20, n_q=1, Hk=1, G=1, D=128, page=16, prefix=0, lens=[50 * b for b in range(20)]),
+]
+
+
+@pytest.mark.parametrize("n", range(len(CASES)))
+def test_against_float64(n):
+    c = Case(seed=n, **CASES[n])
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("D,B", [(64, 3), (128, 40)])
+@pytest.mark.parametrize("q_scale", [0.0, 8.0, 60.0])
+def test_flat_and_peaked_scores(D, B, q_scale):
+    """All scores equal; scores far apart, so that nearly one key takes all."""
+    c = Case(B, 1, 2, 4, D, 32, 1500, [40] * B, seed=1, q_scale=q_scale)
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("order", ["rising", "falling"])
+@pytest.mark.parametrize("B", [2, 40])
+def test_running_maximum(order, B):
+    """Scores that rise (fall) along the prefix by some 200 in all."""
+    c = Case(B, 1, 1, 4, 128, 16, 2048, [64] * B, seed=2)
+    c.q[:] = 1.0
+    ramp = torch.linspace(-1, 1, 2048, device=DEV) * (1 if order == "rising" else -1) * 8.8
+    for j in range(2048):
+        c.k[int(c.prefix_table[j // 16]), :, j % 16] = ramp[j].to(BF)
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
+def test_scales(scale):
+    c = Case(5, 1, 2, 4, 128, 16, 300, [10, 0, 33, 5, 100], seed=3)
+    c.scale = scale
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("fill", [float("nan"), float("inf"), -3e38])
+@pytest.mark.parametrize("B,n_q,D", [(3, 1, 128), (3, 4, 64), (50, 1, 64)])
+def test_unseen_places_may_hold_anything(fill, B, n_q, D):
+    """Places past each length, unused pages and the rest of the prefix's last page."""
+    lens = [(7 * b) % 60 + n_q - 1 for b in range(B)]
+    c = Case(B, n_q, 2, 4, D, 16, 211, lens, seed=4, width=6)
+    want = c.run()
+    seen = torch.zeros(c.pages, c.page, dtype=torch.bool, device=DEV)
+    for b in range(B):
+        for p, o in c.places(b, n_q - 1):
+            seen[p, o] = True
+    mask = ~seen[:, None, :, None]
+    c.k.masked_fill_(mask, fill)
+    c.v.masked_fill_(mask, fill)
+    o, lse = c.run()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    c.check(o, lse)
+
+
+def test_pages_outside_the_cache_are_left_out():
+    c = Case(4, 1, 2, 4, 128, 16, 200, [70, 33, 5, 0], seed=5)
+    c.prefix_table[3], c.prefix_table[12] = -1, c.pages
+    c.tables[0, 1], c.tables[2, 0] = 2 ** 31 - 1, -(2 ** 31)
+    c.check(*c.run())
+    c.prefix_table[:] = -5  # nothing of the prefix, and one sequence without any key
+    c.check(*c.run())
+
+
+def test_lengths_past_the_table_read_the_table_only():
+    c = Case(3, 1, 1, 4, 64, 16, 40, [10, 20, 30], seed=6, width=2)
+    c.lens = torch.tensor([1000, 2 ** 31 - 1, -7], dtype=torch.int32, device=DEV)
+    c.check(*c.run())
+
+
+def test_scores_of_minus_infinity():
+    """A seen key whose score is -inf has weight zero; a row of such keys alone counts as empty."""
+    c = Case(2, 1, 1, 2, 64, 16, 20, [3, 0], seed=7)
+    c.q.abs_().add_(0.1)
+    for j in range(20):
+        c.k[int(c.prefix_table[j // 16]), :, j % 16, 0] = float("-inf")
+    o, lse = c.run()
+    assert (o[1] == 0).all() and (lse[1] == -math.inf).all()
+    c.prefix, c.B = 0, 1  # the first sequence: its suffix alone
+    c.check(o[:1], lse[:1])
+
+
+@pytest.mark.parametrize("B,n_q", [(3, 1), (40, 2)])
+def test_strides_and_guard(B, n_q):
+    """Queries inside wider rows, head-major outputs in a larger buffer, no lse."""
+    c = Case(B, n_q, 2, 4, 128, 16, 500, [9 + n_q] * B, seed=8)
+    want, _ = c.run()
+    T, H, D = c.q.shape
+    wide = torch.randn(T, (H + 3) * D, device=DEV).to(BF)
+    wide[:, D : D + H * D] = c.q.flatten(1)
+    out = torch.full((H + 1, T, D + 8), 3.0, dtype=BF, device=DEV)
+    o = out[:H, :, :D].transpose(0, 1)
+    kv = oq.PagedKV(c.k, c.v)
+    got, lse = oq.oq_attn_prefix(wide[:, D : D + H * D].unflatten(1, (H, D)), n_q, kv, c.prefix_table, c.prefix, c.tables,
+                                 c.lens, c.scale, o=o)
+    assert lse is None and torch.equal(o, want)
+    out[:H, :, :D] = 3.0
+    assert (out == 3.0).all()
+
+
+def test_interleaved_cache_and_deterministic():
+    c = Case(30, 1, 2, 4, 128, 16, 3000, [50] * 30, seed=9)
+    want = c.run()
+    both = torch.stack((c.k, c.v), 1)
+    c.k, c.v = both[:, 0], both[:, 1]
+    for _ in range(3):
+        o, lse = c.run()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_cache_past_4_gib():
+    """Pages more than 2^32 bytes (and 2^31 elements) from the base."""
+    c = Case(3, 1, 1, 4, 64, 16, 40, [5, 20, 16], seed=10)
+    want = c.run()
+    # pages of the same contents, page p at place p * stride
+    n, stride = c.pages, 1 << 29
+    k = torch.as_strided(torch.empty((n - 1) * stride + 16 * 64, dtype=BF, device=DEV), (n, 1, 16, 64), (stride, 1024, 64, 1))
+    v = torch.as_strided(torch.empty((n - 1) * stride + 16 * 64, dtype=BF, device=DEV), (n, 1, 16, 64), (stride, 1024, 64, 1))
+    for p in range(n):
+        k[p], v[p] = c.k[p], c.v[p]
+    assert (n - 1) * stride > 1 << 32
+    o, lse = oq.oq_attn_prefix(c.q, 1, oq.PagedKV(k, v), c.prefix_table, c.prefix, c.tables, c.lens, c.scale, want_lse=True)
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_empty_batch():
+    c = Case(2, 1, 1, 4, 64, 16, 40, [5, 20], seed=11)
+    o, _ = oq.oq_attn_prefix(c.q[:0], 1, oq.PagedKV(c.k, c.v), c.prefix_table, c.prefix, c.tables[:0], c.lens[:0], c.scale)
+    assert o.shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("B,prefix", [(2, 100), (40, 3000)])
+def test_streams_and_graph(B, prefix):
+    c = Case(B, 1, 2, 4, 128, 16, prefix, [50] * B, seed=12)
+    want = c.run()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        o, lse = c.run()
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(o, want[0])
+    kv = oq.PagedKV(c.k, c.v)
+    ws = torch.empty(oq.oq_attn_prefix_ws_bytes(B, 1, 8, kv, prefix, c.S), dtype=torch.uint8, device=DEV)
+    ws.fill_(255)  # scratch needs no particular contents
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        oq.oq_attn_prefix(c.q, 1, kv, c.prefix_table, prefix, c.tables, c.lens, c.scale, o=o, lse=lse, ws=ws)
+    for i in range(3):
+        c.q.mul_(-1.25)
+        c.lens.sub_(9)
+        g.replay()
+        torch.cuda.synchronize()
+        want = c.run()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    c.check(o, lse)
