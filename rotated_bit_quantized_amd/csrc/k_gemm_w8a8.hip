@@ -9,8 +9,8 @@
 // gemm_w8a8_tile: a workgroup of WM x WN wavefronts, each TI x TJ tiles of
 // 32 x 32 on v_mfma_i32_32x32x32_i8, accumulated in place (nothing happens
 // between k steps, so the accumulators stay where the MFMA wants them).  k
-// advances in stages of 64 through a ring of NSLOT LDS slots, filled global ->
-// LDS with 16 rows x 64 bytes per instruction; the 16-byte pieces of a row are
+// advances in stages of 128 through a ring of NSLOT LDS slots, filled global ->
+// LDS with 8 rows x 128 bytes per instruction; the 16-byte pieces of a row are
 // permuted by the row (on the source side, LDS destinations being linear) so
 // that the fragment reads of 16 consecutive rows fall into different banks.
 // One barrier per stage; the fragments of the next 32 k are read under the
@@ -54,17 +54,18 @@ template <int TI_, int TJ_, int WM_, int WN_, int NSLOT_>
 struct Tile {
   static constexpr int TI = TI_, TJ = TJ_, WM = WM_, WN = WN_, NSLOT = NSLOT_;
   static constexpr int NW = WM * WN, BM = 32 * TI * WM, BN = 32 * TJ * WN;
-  static constexpr int STAGE = (BM + BN) * 64;
+  static constexpr int STAGE = (BM + BN) * 128;
   static constexpr int PER = STAGE / 1024 / NW;  // copies per wavefront and stage
   static constexpr int SROW = 64 * TJ + 16;      // bytes of a staged output row of 32 TJ bf16, padded
-  static constexpr int LDS = NSLOT * STAGE > NW * 32 * SROW ? NSLOT * STAGE : NW * 32 * SROW;
+  static constexpr int VEC = NSLOT * STAGE > NW * 32 * SROW ? NSLOT * STAGE : NW * 32 * SROW;
+  static constexpr int LDS = VEC + 2 * BM * 4;   // the ring or the staged slabs, row scales and means
   static_assert(PER * NW * 1024 == STAGE, "every wavefront copies the same share");
-  static_assert(NSLOT == 4, "the waits count for four slots");
+  static_assert(NSLOT >= 2 && (NSLOT - 2) * PER <= 63, "vmcnt range");
   static_assert(LDS <= 160 * 1024, "LDS");
 };
 
 template <class C>
-__global__ void __launch_bounds__(64 * C::NW, 1) gemm_w8a8_tile(const GemmArgs g) {
+__global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 ? 2 : 1) gemm_w8a8_tile(const GemmArgs g) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   constexpr int TI = C::TI, TJ = C::TJ;
   const uint32_t lds0 = lds_addr_of(smem);
@@ -84,15 +85,15 @@ __global__ void __launch_bounds__(64 * C::NW, 1) gemm_w8a8_tile(const GemmArgs g
   const int64_t m0 = (int64_t)(8 * band + id % bm) * C::BM;
   const int n0 = id / bm * C::BN;
 
-  // this wavefront's copies: unit u = wave + NW q covers rows 16 u + lane / 4
+  // this wavefront's copies: unit u = wave + NW q covers rows 8 u + lane / 8
   // of the stage (the tile's BM activation rows, then its BN weight rows),
   // 1 KiB at 1024 u of the slot; rows past the end re-read the last one
   const int8_t *src[C::PER];
   int koff[C::PER];
 #pragma unroll
   for (int q = 0; q < C::PER; ++q) {
-    const int row = 16 * (wave + C::NW * q) + (lane >> 2);
-    koff[q] = 16 * ((lane & 3) ^ ((row >> 2) & 3));
+    const int row = 8 * (wave + C::NW * q) + (lane >> 3);
+    koff[q] = 16 * ((lane & 7) ^ ((row >> 1) & 7));
     if (row < C::BM) {
       const int64_t m = m0 + row < g.M ? m0 + row : g.M - 1;
       src[q] = g.qa + m * g.lda + koff[q];
@@ -101,19 +102,36 @@ __global__ void __launch_bounds__(64 * C::NW, 1) gemm_w8a8_tile(const GemmArgs g
       src[q] = g.w + n * g.ldw + koff[q];
     }
   }
-  const int S = (g.K + 63) / 64;
-  auto issue = [&](int st) {
-    const uint32_t base = lds0 + (st & 3) * C::STAGE + 1024 * wave;
-    if (64 * st + 64 <= g.K) {
+  const int S = (g.K + 127) / 128;
+  // src[] always points at stage `next`: its copies past K (the last stage of
+  // a K that is no multiple of 128) and past the last stage come from zeros, so
+  // that the loop below has no special stages
+  int next = 0, fill = 0;  // that stage and its slot
+  auto zero_past = [&](int k) {
 #pragma unroll
-      for (int q = 0; q < C::PER; ++q) dma_lds16(src[q] + (int64_t)64 * st, base + 1024 * C::NW * q);
-    } else {
+    for (int q = 0; q < C::PER; ++q)
+      if (koff[q] >= k) src[q] = reinterpret_cast<const int8_t *>(&g_zero16);
+  };
+  if (S == 1) zero_past(g.K);
+  auto issue = [&](int q) { dma_lds16(src[q], lds0 + fill * C::STAGE + 1024 * wave + 1024 * C::NW * q); };
+  auto advance = [&]() {
+    ++next;
+    fill = fill == C::NSLOT - 1 ? 0 : fill + 1;
+    if (next < S) {
 #pragma unroll
-      for (int q = 0; q < C::PER; ++q)
-        dma_lds16(64 * st + koff[q] < g.K ? (const void *)(src[q] + (int64_t)64 * st) : (const void *)&g_zero16,
-                  base + 1024 * C::NW * q);
+      for (int q = 0; q < C::PER; ++q) src[q] += 128;
+      if (next == S - 1) zero_past(g.K - 128 * next);
+    } else if (next == S) {
+      zero_past(0);
     }
   };
+
+  float *s_scale = reinterpret_cast<float *>(smem + C::VEC), *s_mean = s_scale + C::BM;
+  for (int t = threadIdx.x; t < C::BM; t += 64 * C::NW) {
+    const int64_t row = m0 + t < g.M ? m0 + t : g.M - 1;
+    s_scale[t] = g.a_scale[row];
+    s_mean[t] = g.mean ? g.mean[row] : 0.f;
+  }
 
   const int wm = wave / C::WN, wn = wave % C::WN;
   v16i acc[TI][TJ];
@@ -124,52 +142,65 @@ __global__ void __launch_bounds__(64 * C::NW, 1) gemm_w8a8_tile(const GemmArgs g
 
   // fragment of 32 rows, k 32 kc + 16 half of the stage: row r of the block,
   // piece 2 kc + half in the row's order
-  const uint8_t *fa = smem + (wm * 32 * TI + r) * 64, *fb = smem + (C::BM + wn * 32 * TJ + r) * 64;
-  const int sw = (r >> 2) & 3;  // (row >> 2) & 3 of every row that is r modulo 32
-  auto load = [&](v4i (&a)[TI], v4i (&b)[TJ], int slot, int kc) {
+  const uint8_t *fa = smem + (wm * 32 * TI + r) * 128, *fb = smem + (C::BM + wn * 32 * TJ + r) * 128;
+  const int sw = (r >> 1) & 7;  // (row >> 1) & 7 of every row that is r modulo 32
+
+  // One chunk of 32 k: the MFMAs of each row block under the reads of the next
+  // chunk's fragments and this wavefront's share of the next copies, spread
+  // over the first half of a stage's MFMAs so that neither holds them up.
+  constexpr int GROUPS = 2 * TI;
+  auto chunk = [&](const v4i (&a)[TI], const v4i (&b)[TJ], v4i (&an)[TI], v4i (&bn)[TJ], int slot, int kc, int part) {
     const int at = slot * C::STAGE + 16 * ((2 * kc + half) ^ sw);
 #pragma unroll
-    for (int i = 0; i < TI; ++i) a[i] = *reinterpret_cast<const v4i *>(fa + at + i * 2048);
+    for (int i = 0; i < TI; ++i) {
+      an[i] = *reinterpret_cast<const v4i *>(fa + at + i * 4096);
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) b[j] = *reinterpret_cast<const v4i *>(fb + at + j * 2048);
-  };
-  auto mma = [&](const v4i (&a)[TI], const v4i (&b)[TJ]) {
+      for (int j = i * TJ / TI; j < (i + 1) * TJ / TI; ++j) bn[j] = *reinterpret_cast<const v4i *>(fb + at + j * 4096);
+      if (part < 2) {
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
+        for (int q = (part * TI + i) * C::PER / GROUPS; q < (part * TI + i + 1) * C::PER / GROUPS; ++q) issue(q);
+      }
 #pragma unroll
       for (int j = 0; j < TJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[i], b[j], acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
 
-  // Stage s starts with its first fragments in registers.  It waits for this
-  // wavefront's copies of stage s + 1 and for its LDS reads; after the barrier
-  // stage s + 1 is visible everywhere and nobody reads the slot of stage s - 1
-  // any more, which stage s + 3 then fills.
-#pragma unroll
-  for (int p = 0; p < 3; ++p)
-    if (p < S) issue(p);
-  if (S > 2) wait_vm<2 * C::PER>();
-  else if (S > 1) wait_vm<C::PER>();
-  else wait_vm<0>();
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
+  // The loop is turned by one chunk: when the last chunk of stage s - 1 is in
+  // registers, nobody needs its slot any more.  So there the wavefronts wait
+  // for their copies of stage s, meet, run that chunk while the fragments of
+  // stage s come in, and send the copies of stage s + NSLOT - 1 to the slot.
   v4i a[2][TI], b[2][TJ];
-  load(a[0], b[0], 0, 0);
+#pragma unroll
+  for (int i = 0; i < TI; ++i) a[0][i] = (v4i){};  // the chunk before stage 0
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) b[0][j] = (v4i){};
+#pragma unroll
+  for (int p = 0; p < C::NSLOT - 1; ++p) {
+#pragma unroll
+    for (int q = 0; q < C::PER; ++q) issue(q);
+    advance();
+  }
+  int slot = 0;
   for (int s = 0; s < S; ++s) {
-    if (s + 2 < S) wait_vm<C::PER>();
-    else wait_vm<0>();
+    wait_vm<(C::NSLOT - 2) * C::PER>();
     wait_lgkm0();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (s + 3 < S) issue(s + 3);
     __builtin_amdgcn_sched_barrier(0);
-    load(a[1], b[1], s & 3, 1);
-    mma(a[0], b[0]);
-    // after the last stage this reads a slot whose contents are never used
-    load(a[0], b[0], (s + 1) & 3, 0);
-    mma(a[1], b[1]);
+    chunk(a[0], b[0], a[1], b[1], slot, 0, 0);
+    chunk(a[1], b[1], a[0], b[0], slot, 1, 1);
+    advance();
+    chunk(a[0], b[0], a[1], b[1], slot, 2, 2);
+    chunk(a[1], b[1], a[0], b[0], slot, 3, 3);
+    slot = slot == C::NSLOT - 1 ? 0 : slot + 1;
   }
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[0][i], b[0][j], acc[i][j], 0, 0, 0);
+  wait_vm<0>();  // the slots are reused
 
   // Epilogue: 32-row slabs staged in this wavefront's own part of LDS (free
   // once everybody has passed the barrier) for 16-byte stores.
@@ -192,17 +223,20 @@ __global__ void __launch_bounds__(64 * C::NW, 1) gemm_w8a8_tile(const GemmArgs g
     const int64_t mrow = m0 + 32 * (wm * TI + i);
     if (mrow >= g.M) break;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int rr = 8 * (e >> 2) + 4 * half + (e & 3);
-      const int64_t row = mrow + rr < g.M ? mrow + rr : g.M - 1;
-      const float al = g.a_scale[row], mu = g.mean ? g.mean[row] : 0.f;
+    for (int e4 = 0; e4 < 4; ++e4) {
+      const int r4 = 8 * e4 + 4 * half;  // rows r4 .. r4 + 3 of the slab
+      const float4 al4 = *reinterpret_cast<const float4 *>(s_scale + 32 * (wm * TI + i) + r4);
+      const float4 mu4 = *reinterpret_cast<const float4 *>(s_mean + 32 * (wm * TI + i) + r4);
+      const float al[4] = {al4.x, al4.y, al4.z, al4.w}, mu[4] = {mu4.x, mu4.y, mu4.z, mu4.w};
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        float v = al * ws[j] * (float)acc[i][j][e];
-        if (g.mean) v = __builtin_fmaf(mu, w1v[j], v);
-        if (g.bias) v = v + bv[j];
-        *reinterpret_cast<uint16_t *>(stg + rr * C::SROW + (32 * j + r) * 2) = f32_to_bf16_rne(v);
-      }
+      for (int e1 = 0; e1 < 4; ++e1)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) {
+          float v = al[e1] * ws[j] * (float)acc[i][j][4 * e4 + e1];
+          if (g.mean) v = __builtin_fmaf(mu[e1], w1v[j], v);
+          if (g.bias) v = v + bv[j];
+          *reinterpret_cast<uint16_t *>(stg + (r4 + e1) * C::SROW + (32 * j + r) * 2) = f32_to_bf16_rne(v);
+        }
     }
     constexpr int CPR = 4 * TJ;  // 16-byte pieces of a slab row
 #pragma unroll
@@ -328,9 +362,12 @@ hipError_t launch_gemm_w8a8(const int8_t *qa, int64_t lda, const float *a_scale,
   if (f == 1 && M <= 16) return launch_rows<1, 1, 4, 8>(g, stream);
   if (f == 2 && M <= 32) return launch_rows<2, 1, 4, 8>(g, stream);
   if (f == 3) return launch_tile<Tile<1, 1, 2, 2, 4>>(g, stream);
-  if (f == 4) return launch_tile<Tile<2, 2, 2, 2, 4>>(g, stream);
-  if (f == 5) return launch_tile<Tile<4, 4, 2, 2, 4>>(g, stream);
-  if (f == 6) return launch_tile<Tile<4, 2, 2, 4, 4>>(g, stream);
+  if (f == 4) return launch_tile<Tile<2, 2, 2, 2, 2>>(g, stream);
+  if (f == 5) return launch_tile<Tile<4, 4, 2, 2, 2>>(g, stream);
+  if (f == 6) return launch_tile<Tile<4, 2, 2, 4, 2>>(g, stream);
+  if (f == 12) return launch_tile<Tile<2, 2, 2, 2, 3>>(g, stream);
+  if (f == 13) return launch_tile<Tile<2, 2, 2, 2, 4>>(g, stream);
+  if (f == 14) return launch_tile<Tile<2, 4, 4, 2, 2>>(g, stream);
   if (f == 7 && M <= 16) return launch_rows<1, 1, 8, 8>(g, stream);
   if (f == 8 && M <= 16) return launch_rows<1, 1, 8, 4>(g, stream);
   if (f == 9 && M <= 16) return launch_rows<1, 1, 16, 4>(g, stream);
@@ -338,7 +375,7 @@ hipError_t launch_gemm_w8a8(const int8_t *qa, int64_t lda, const float *a_scale,
   if (f == 11 && M <= 16) return launch_rows<1, 2, 4, 8>(g, stream);
   if (M <= 16) return launch_rows<1, 1, 4, 8>(g, stream);
   if (M <= 32) return launch_rows<2, 1, 4, 8>(g, stream);
-  if (((M + 255) / 256) * ((N + 255) / 256) >= 128) return launch_tile<Tile<4, 4, 2, 2, 4>>(g, stream);
+  if (((M + 255) / 256) * ((N + 255) / 256) >= 128) return launch_tile<Tile<4, 2, 2, 4, 2>>(g, stream);
   if (((M + 127) / 128) * ((N + 127) / 128) >= 128) return launch_tile<Tile<2, 2, 2, 2, 4>>(g, stream);
   return launch_tile<Tile<1, 1, 2, 2, 4>>(g, stream);
 }
