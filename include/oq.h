@@ -522,7 +522,7 @@ int oq_quant_weight_w8(const float *w, int32_t N, int32_t K, int64_t ldw, const 
  * mean and w1 both NULL or both set; bias nullable; y bf16 [M][ldy].
  * Any M, N >= 0 (zero enqueues nothing); K a multiple of 16, 16 <= K <=
  * 131056 (the int32 sum cannot overflow, codes of -128 included); lda, ldw
- * multiples of 16; qa and w 16-byte aligned.  No scratch.  The result does
+ * multiples of 16, at most 2^23; qa and w 16-byte aligned.  No scratch.  The result does
  * not depend on the tile that the library picks from M, N, K and the CU count.
  */
 int oq_gemm_w8a8(const int8_t *qa, int64_t lda, const float *a_scale, int64_t M, int32_t K, const int8_t *w,

@@ -113,6 +113,8 @@ int oq_gemm_w8a8(const int8_t *qa, int64_t lda, const float *a_scale, int64_t M,
   if (M > ((int64_t)1 << 30)) return fail(OQ_ERR_UNSUPPORTED, "%s: M=%lld exceeds 2^30", fn, (long long)M);
   if (!qa || !a_scale || !w || !w_scale || !y) return fail(OQ_ERR_INVALID_ARG, "%s: NULL operand", fn);
   if (lda < K || ldw < K) return fail(OQ_ERR_INVALID_ARG, "%s: lda=%lld or ldw=%lld < K=%d", fn, (long long)lda, (long long)ldw, K);
+  if (lda > (1 << 23) || ldw > (1 << 23))
+    return fail(OQ_ERR_UNSUPPORTED, "%s: lda=%lld or ldw=%lld exceeds 2^23", fn, (long long)lda, (long long)ldw);
   if (ldy < N) return fail(OQ_ERR_INVALID_ARG, "%s: ldy=%lld < N=%d", fn, (long long)ldy, N);
   if (!al(qa, 16) || !al(w, 16) || lda % 16 || ldw % 16)
     return fail(OQ_ERR_ALIGNMENT, "%s: rows of qa and w must start 16-byte aligned", fn);

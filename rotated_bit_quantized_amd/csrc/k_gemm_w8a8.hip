@@ -26,8 +26,14 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v16i __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-// what k past the end of the rows is copied from
-__device__ const uint4 g_zero16 = {0u, 0u, 0u, 0u};
+// dma_lds16 with a scalar base and a 32-bit offset per lane
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void dma_lds16_s(const void *base, uint32_t off, uint32_t lds_addr) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds_addr)
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
 
 template <int C>
 __device__ __forceinline__ void wait_vm() {
@@ -50,104 +56,154 @@ struct GemmArgs {
   int64_t ldy;
 };
 
+// x / d for a divisor whose reciprocal r = floor(2^32 / d) + 1 the host has
+// formed: the high product is the quotient or one more.
+struct Div {
+  uint32_t d, r;
+};
+__host__ inline Div div_by(uint32_t d) { return {d, d == 1 ? 0u : (uint32_t)((1ull << 32) / d + 1)}; }
+__device__ __forceinline__ uint32_t div_of(uint32_t x, Div v) {
+  if (v.d == 1) return x;
+  const uint32_t q = __umulhi(x, v.r);
+  return q * v.d > x ? q - 1 : q;
+}
+
+// How workgroups map to tiles.
+struct TileMap {
+  int mt, nt;      // tile rows and columns
+  int run, rem;    // tiles / 8, tiles % 8
+  Div band, full, last;  // 8 nt; tile rows of a full band; of the last band
+};
+
 template <int TI_, int TJ_, int WM_, int WN_, int NSLOT_>
 struct Tile {
   static constexpr int TI = TI_, TJ = TJ_, WM = WM_, WN = WN_, NSLOT = NSLOT_;
   static constexpr int NW = WM * WN, BM = 32 * TI * WM, BN = 32 * TJ * WN;
   static constexpr int STAGE = (BM + BN) * 128;
   static constexpr int PER = STAGE / 1024 / NW;  // copies per wavefront and stage
-  static constexpr int SROW = 64 * TJ + 16;      // bytes of a staged output row of 32 TJ bf16, padded
-  static constexpr int VEC = NSLOT * STAGE > NW * 32 * SROW ? NSLOT * STAGE : NW * 32 * SROW;
-  static constexpr int LDS = VEC + 2 * BM * 4;   // the ring or the staged slabs, row scales and means
+  // copies NW q .. NW q + NW - 1 are activation rows (weight rows follow them)
+  static constexpr bool A_UNIT(int q) { return 8 * NW * q < BM; }
+  static constexpr int SROW = 80;                // bytes of a staged row of 32 bf16, padded
+  static constexpr int STG = NW * TJ * 32 * SROW, RING = NSLOT * STAGE;
+  static constexpr int VEC = RING > STG ? RING : STG, LDS = VEC + 3 * BN * 4;
+  static constexpr int RESIDENT = 160 * 1024 / LDS < 4 ? 160 * 1024 / LDS : 4;  // workgroups a CU
   static_assert(PER * NW * 1024 == STAGE, "every wavefront copies the same share");
+  static_assert(BM % (8 * NW) == 0 && NW % 2 == 0, "a round of copies is all activations or all weights");
   static_assert(NSLOT >= 2 && (NSLOT - 2) * PER <= 63, "vmcnt range");
+  static_assert(BN <= 64 * NW, "one thread per column");
   static_assert(LDS <= 160 * 1024, "LDS");
 };
 
 template <class C>
-__global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 ? 2 : 1) gemm_w8a8_tile(const GemmArgs g) {
+__global__ void __launch_bounds__(64 * C::NW, C::NW / 4 * C::RESIDENT) gemm_w8a8_tile(const GemmArgs g, const TileMap t) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   constexpr int TI = C::TI, TJ = C::TJ;
   const uint32_t lds0 = lds_addr_of(smem);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 31, half = lane >> 5;
 
-  // Tile order: workgroups go to the 8 XCDs in turn, each XCD takes a run of
+  // Tile order: workgroups go to the 8 XCDs in turn; each XCD takes a run of
   // tiles, and a run walks column by column through bands of 8 tile rows, so
-  // that the 32 tiles an XCD has in flight share rows and columns in its L2.
-  const int mt = (int)((g.M + C::BM - 1) / C::BM), nt = (g.N + C::BN - 1) / C::BN;
-  const int tiles = mt * nt, xcd = blockIdx.x & 7;
-  const int run = tiles >> 3, rem = tiles & 7;
-  int id = xcd * run + (xcd < rem ? xcd : rem) + (blockIdx.x >> 3);
-  const int band = id / (8 * nt);
-  const int bm = mt - 8 * band < 8 ? mt - 8 * band : 8;
-  id -= band * 8 * nt;
-  const int64_t m0 = (int64_t)(8 * band + id % bm) * C::BM;
-  const int n0 = id / bm * C::BN;
+  // that the tiles that an XCD has in flight share rows and columns in its L2.
+  const int xcd = blockIdx.x & 7;
+  const int id = xcd * t.run + (xcd < t.rem ? xcd : t.rem) + (blockIdx.x >> 3);
+  const int band = div_of(id, t.band), in_band = id - band * t.band.d;
+  const Div rows = 8 * band + 8 <= t.mt ? t.full : t.last;
+  const int tn = div_of(in_band, rows);
+  const int64_t m0 = (int64_t)(8 * band + in_band - tn * rows.d) * C::BM;
+  const int n0 = tn * C::BN;
 
-  // this wavefront's copies: unit u = wave + NW q covers rows 8 u + lane / 8
+  // This wavefront's copies: unit u = wave + NW q covers rows 8 u + lane / 8
   // of the stage (the tile's BM activation rows, then its BN weight rows),
-  // 1 KiB at 1024 u of the slot; rows past the end re-read the last one
-  const int8_t *src[C::PER];
-  int koff[C::PER];
+  // 1 KiB at 1024 u of the slot; rows past the end re-read the last one.
+  // base_a, base_w (scalar) point at stage `next`, voff[] is each lane's place
+  // below them, slot `fill` takes the stage.
+  const int S = (g.K + 127) / 128, last_k = g.K - 128 * (S - 1);  // k of the last stage
+  int next = 0, fill = 0;
+  uint32_t voff[C::PER];
+  const int piece = 16 * ((lane & 7) ^ ((lane >> 4) | (wave & 1) << 2));  // of its row: every row of a lane has this (row >> 1) & 7
+  const int8_t *base_a = g.qa + m0 * g.lda, *base_w = g.w + (int64_t)n0 * g.ldw;
+  {
+    const int ma = g.M - m0 < C::BM ? (int)(g.M - m0) - 1 : C::BM - 1, na = g.N - n0 < C::BN ? g.N - n0 - 1 : C::BN - 1;
 #pragma unroll
-  for (int q = 0; q < C::PER; ++q) {
-    const int row = 8 * (wave + C::NW * q) + (lane >> 3);
-    koff[q] = 16 * ((lane & 7) ^ ((row >> 1) & 7));
-    if (row < C::BM) {
-      const int64_t m = m0 + row < g.M ? m0 + row : g.M - 1;
-      src[q] = g.qa + m * g.lda + koff[q];
-    } else {
-      const int64_t n = n0 + row - C::BM < g.N ? n0 + row - C::BM : g.N - 1;
-      src[q] = g.w + n * g.ldw + koff[q];
+    for (int q = 0; q < C::PER; ++q) {
+      const int row = 8 * (wave + C::NW * q) + (lane >> 3);
+      if (C::A_UNIT(q)) voff[q] = (uint32_t)(row < ma ? row : ma) * (uint32_t)g.lda + piece;
+      else voff[q] = (uint32_t)(row - C::BM < na ? row - C::BM : na) * (uint32_t)g.ldw + piece;
     }
   }
-  const int S = (g.K + 127) / 128;
-  // src[] always points at stage `next`: its copies past K (the last stage of
-  // a K that is no multiple of 128) and past the last stage come from zeros, so
-  // that the loop below has no special stages
-  int next = 0, fill = 0;  // that stage and its slot
-  auto zero_past = [&](int k) {
-#pragma unroll
-    for (int q = 0; q < C::PER; ++q)
-      if (koff[q] >= k) src[q] = reinterpret_cast<const int8_t *>(&g_zero16);
+  auto issue = [&](int q) {
+    dma_lds16_s(C::A_UNIT(q) ? base_a : base_w, voff[q], lds0 + fill * C::STAGE + 1024 * wave + 1024 * C::NW * q);
   };
-  if (S == 1) zero_past(g.K);
-  auto issue = [&](int q) { dma_lds16(src[q], lds0 + fill * C::STAGE + 1024 * wave + 1024 * C::NW * q); };
+  // what lies past K in the last stage is copied from the row's first piece of
+  // the stage and cleared in LDS (clear_tail)
+  auto tail_offsets = [&]() {
+    if (piece < last_k) return;
+#pragma unroll
+    for (int q = 0; q < C::PER; ++q) voff[q] -= piece;
+  };
+  if (S == 1) tail_offsets();
+  // After the last stage the loop goes on copying 16 bytes of it all over slots
+  // that nobody reads, so that it has no special stages.
   auto advance = [&]() {
     ++next;
     fill = fill == C::NSLOT - 1 ? 0 : fill + 1;
     if (next < S) {
-#pragma unroll
-      for (int q = 0; q < C::PER; ++q) src[q] += 128;
-      if (next == S - 1) zero_past(g.K - 128 * next);
+      base_a += 128;
+      base_w += 128;
+      if (next == S - 1) tail_offsets();
     } else if (next == S) {
-      zero_past(0);
+#pragma unroll
+      for (int q = 0; q < C::PER; ++q) voff[q] = 0;
     }
   };
-
-  float *s_scale = reinterpret_cast<float *>(smem + C::VEC), *s_mean = s_scale + C::BM;
-  for (int t = threadIdx.x; t < C::BM; t += 64 * C::NW) {
-    const int64_t row = m0 + t < g.M ? m0 + t : g.M - 1;
-    s_scale[t] = g.a_scale[row];
-    s_mean[t] = g.mean ? g.mean[row] : 0.f;
+  auto clear_tail = [&](int slot) {  // activations past K become zeros, each wavefront clearing what it copied
+    if (piece < last_k) return;
+#pragma unroll
+    for (int q = 0; q < C::PER; ++q)
+      if (C::A_UNIT(q))
+        *reinterpret_cast<v4i *>(smem + slot * C::STAGE + 1024 * (wave + C::NW * q) + 16 * lane) = (v4i){};
+  };
+#pragma unroll
+  for (int p = 0; p < C::NSLOT - 1; ++p) {
+#pragma unroll
+    for (int q = 0; q < C::PER; ++q) issue(q);
+    advance();
   }
 
+  // the epilogue's vectors, used after the main loop
   const int wm = wave / C::WN, wn = wave % C::WN;
-  v16i acc[TI][TJ];
+  float ws = 0.f, w1 = 0.f, bias = 0.f, al[TI], mu[TI];
+  {
+    const int col = n0 + (int)threadIdx.x;
+    if (threadIdx.x < C::BN && col < g.N) {
+      ws = g.w_scale[col];
+      if (g.mean) w1 = g.w1[col];
+      if (g.bias) bias = g.bias[col];
+    }
 #pragma unroll
-  for (int i = 0; i < TI; ++i)
-#pragma unroll
-    for (int j = 0; j < TJ; ++j) acc[i][j] = (v16i){};
+    for (int i = 0; i < TI; ++i) {
+      const int64_t row = m0 + 32 * (wm * TI + i) + r < g.M ? m0 + 32 * (wm * TI + i) + r : g.M - 1;
+      al[i] = g.a_scale[row];
+      mu[i] = g.mean ? g.mean[row] : 0.f;
+    }
+  }
 
   // fragment of 32 rows, k 32 kc + 16 half of the stage: row r of the block,
   // piece 2 kc + half in the row's order
   const uint8_t *fa = smem + (wm * 32 * TI + r) * 128, *fb = smem + (C::BM + wn * 32 * TJ + r) * 128;
   const int sw = (r >> 1) & 7;  // (row >> 1) & 7 of every row that is r modulo 32
 
+  v16i acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = (v16i){};
   // One chunk of 32 k: the MFMAs of each row block under the reads of the next
   // chunk's fragments and this wavefront's share of the next copies, spread
-  // over the first half of a stage's MFMAs so that neither holds them up.
+  // over the first half of a stage's MFMAs so that neither holds them up.  The
+  // product is formed transposed (rows: weights), so that a lane holds one
+  // token and four consecutive outputs per group of four registers.
   constexpr int GROUPS = 2 * TI;
   auto chunk = [&](const v4i (&a)[TI], const v4i (&b)[TJ], v4i (&an)[TI], v4i (&bn)[TJ], int slot, int kc, int part) {
     const int at = slot * C::STAGE + 16 * ((2 * kc + half) ^ sw);
@@ -161,7 +217,7 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
         for (int q = (part * TI + i) * C::PER / GROUPS; q < (part * TI + i + 1) * C::PER / GROUPS; ++q) issue(q);
       }
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[i], b[j], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < TJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[j], a[i], acc[i][j], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -175,15 +231,11 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
   for (int i = 0; i < TI; ++i) a[0][i] = (v4i){};  // the chunk before stage 0
 #pragma unroll
   for (int j = 0; j < TJ; ++j) b[0][j] = (v4i){};
-#pragma unroll
-  for (int p = 0; p < C::NSLOT - 1; ++p) {
-#pragma unroll
-    for (int q = 0; q < C::PER; ++q) issue(q);
-    advance();
-  }
   int slot = 0;
   for (int s = 0; s < S; ++s) {
     wait_vm<(C::NSLOT - 2) * C::PER>();
+    asm volatile("" ::: "memory");
+    if (s == S - 1 && last_k < 128) clear_tail(slot);
     wait_lgkm0();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
@@ -199,60 +251,54 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW == 8 || C::LDS <= 80 * 1024 
 #pragma unroll
   for (int i = 0; i < TI; ++i)
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[0][i], b[0][j], acc[i][j], 0, 0, 0);
-  wait_vm<0>();  // the slots are reused
+    for (int j = 0; j < TJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[0][j], a[0][i], acc[i][j], 0, 0, 0);
 
-  // Epilogue: 32-row slabs staged in this wavefront's own part of LDS (free
-  // once everybody has passed the barrier) for 16-byte stores.
-  __syncthreads();
-  float ws[TJ], w1v[TJ], bv[TJ];
-#pragma unroll
-  for (int j = 0; j < TJ; ++j) {
-    const int col = n0 + 32 * (wn * TJ + j) + r;
-    ws[j] = w1v[j] = bv[j] = 0.f;
-    if (col < g.N) {
-      ws[j] = g.w_scale[col];
-      if (g.mean) w1v[j] = g.w1[col];
-      if (g.bias) bv[j] = g.bias[col];
-    }
+  // Epilogue, in the ring's place once nobody copies to or reads from it: each
+  // wavefront stages the TJ tiles of a row block for 16-byte stores.  Without
+  // a mean or bias their zeros are added.
+  float *s_ws = reinterpret_cast<float *>(smem + C::VEC), *s_w1 = s_ws + C::BN, *s_b = s_w1 + C::BN;
+  if (threadIdx.x < C::BN) {
+    s_ws[threadIdx.x] = ws;
+    s_w1[threadIdx.x] = w1;
+    s_b[threadIdx.x] = bias;
   }
-  uint8_t *stg = smem + wave * (32 * C::SROW);
+  wait_vm<0>();
+  asm volatile("" ::: "memory");
+  __syncthreads();
+  uint8_t *stg = smem + wave * (TJ * 32 * C::SROW);
   const bool vec_ok = (reinterpret_cast<uintptr_t>(g.y) & 15) == 0 && g.ldy % 8 == 0;
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
     const int64_t mrow = m0 + 32 * (wm * TI + i);
-    if (mrow >= g.M) break;
 #pragma unroll
-    for (int e4 = 0; e4 < 4; ++e4) {
-      const int r4 = 8 * e4 + 4 * half;  // rows r4 .. r4 + 3 of the slab
-      const float4 al4 = *reinterpret_cast<const float4 *>(s_scale + 32 * (wm * TI + i) + r4);
-      const float4 mu4 = *reinterpret_cast<const float4 *>(s_mean + 32 * (wm * TI + i) + r4);
-      const float al[4] = {al4.x, al4.y, al4.z, al4.w}, mu[4] = {mu4.x, mu4.y, mu4.z, mu4.w};
+    for (int j = 0; j < TJ; ++j) {
 #pragma unroll
-      for (int e1 = 0; e1 < 4; ++e1)
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) {
-          float v = al[e1] * ws[j] * (float)acc[i][j][4 * e4 + e1];
-          if (g.mean) v = __builtin_fmaf(mu[e1], w1v[j], v);
-          if (g.bias) v = v + bv[j];
-          *reinterpret_cast<uint16_t *>(stg + (r4 + e1) * C::SROW + (32 * j + r) * 2) = f32_to_bf16_rne(v);
-        }
+      for (int e4 = 0; e4 < 4; ++e4) {
+        const int c = 32 * (wn * TJ + j) + 8 * e4 + 4 * half;
+        const float4 s4 = *reinterpret_cast<const float4 *>(s_ws + c);
+        const float4 w4 = *reinterpret_cast<const float4 *>(s_w1 + c);
+        const float4 b4 = *reinterpret_cast<const float4 *>(s_b + c);
+        const float v0 = __builtin_fmaf(mu[i], w4.x, al[i] * s4.x * (float)acc[i][j][4 * e4]) + b4.x;
+        const float v1 = __builtin_fmaf(mu[i], w4.y, al[i] * s4.y * (float)acc[i][j][4 * e4 + 1]) + b4.y;
+        const float v2 = __builtin_fmaf(mu[i], w4.z, al[i] * s4.z * (float)acc[i][j][4 * e4 + 2]) + b4.z;
+        const float v3 = __builtin_fmaf(mu[i], w4.w, al[i] * s4.w * (float)acc[i][j][4 * e4 + 3]) + b4.w;
+        *reinterpret_cast<uint2 *>(stg + (32 * j + r) * C::SROW + 16 * e4 + 8 * half) =
+            make_uint2((uint32_t)f32_to_bf16_rne(v0) | ((uint32_t)f32_to_bf16_rne(v1) << 16),
+                       (uint32_t)f32_to_bf16_rne(v2) | ((uint32_t)f32_to_bf16_rne(v3) << 16));
+      }
     }
-    constexpr int CPR = 4 * TJ;  // 16-byte pieces of a slab row
 #pragma unroll
     for (int q = 0; q < 2 * TJ; ++q) {
-      const int piece = lane + 64 * q;
-      const int rr = piece / CPR, cl = (piece % CPR) * 8;
-      const int col = n0 + 32 * wn * TJ + cl;
-      const u32x4 v = *reinterpret_cast<const u32x4 *>(stg + rr * C::SROW + cl * 2);
-      if (mrow + rr >= g.M) continue;
-      uint16_t *dst = g.y + (mrow + rr) * g.ldy + col;
+      const int at = (lane >> 2) + 16 * q;  // staged row: 32 per tile
+      const int64_t row = mrow + (at & 31);
+      const int col = n0 + 32 * (wn * TJ + (at >> 5)) + 8 * (lane & 3);
+      const u32x4 v = *reinterpret_cast<const u32x4 *>(stg + at * C::SROW + 16 * (lane & 3));
+      if (row >= g.M) continue;
+      uint16_t *dst = g.y + row * g.ldy + col;
       if (vec_ok && col + 8 <= g.N) {
         *reinterpret_cast<u32x4 *>(dst) = v;
       } else {
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (col + c < g.N) dst[c] = (uint16_t)(v[c >> 1] >> (16 * (c & 1)));
+        for (int x = 0; x < 8 && col + x < g.N; ++x) dst[x] = (uint16_t)(v[x >> 1] >> (16 * (x & 1)));
       }
     }
   }
@@ -338,9 +384,11 @@ hipError_t launch_tile(const GemmArgs &g, hipStream_t stream) {
   static std::atomic<bool> attr_set[64];
   const hipError_t e = lds_limit_once((const void *)gemm_w8a8_tile<C>, C::LDS, attr_set);
   if (e != hipSuccess) return e;
-  const int64_t tiles = ((g.M + C::BM - 1) / C::BM) * ((g.N + C::BN - 1) / C::BN);
-  if (tiles > 0x7fffffff) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(gemm_w8a8_tile<C>, dim3((unsigned)tiles), dim3(64 * C::NW), C::LDS, stream, g);
+  const int64_t mt = (g.M + C::BM - 1) / C::BM, nt = (g.N + C::BN - 1) / C::BN;
+  if (mt * nt > 0x7fffffff || 8 * nt > 0x7fffffff) return hipErrorInvalidConfiguration;
+  const int tiles = (int)(mt * nt);
+  const TileMap t{(int)mt, (int)nt, tiles / 8, tiles % 8, div_by((uint32_t)(8 * nt)), div_by(8), div_by(mt % 8 ? (uint32_t)(mt % 8) : 8)};
+  hipLaunchKernelGGL(gemm_w8a8_tile<C>, dim3((unsigned)tiles), dim3(64 * C::NW), C::LDS, stream, g, t);
   return hipGetLastError();
 }
 
@@ -363,11 +411,17 @@ hipError_t launch_gemm_w8a8(const int8_t *qa, int64_t lda, const float *a_scale,
   if (f == 2 && M <= 32) return launch_rows<2, 1, 4, 8>(g, stream);
   if (f == 3) return launch_tile<Tile<1, 1, 2, 2, 4>>(g, stream);
   if (f == 4) return launch_tile<Tile<2, 2, 2, 2, 2>>(g, stream);
-  if (f == 5) return launch_tile<Tile<4, 4, 2, 2, 2>>(g, stream);
   if (f == 6) return launch_tile<Tile<4, 2, 2, 4, 2>>(g, stream);
   if (f == 12) return launch_tile<Tile<2, 2, 2, 2, 3>>(g, stream);
-  if (f == 13) return launch_tile<Tile<2, 2, 2, 2, 4>>(g, stream);
+  if (f == 13) return launch_tile<Tile<2, 1, 2, 2, 3>>(g, stream);
   if (f == 14) return launch_tile<Tile<2, 4, 4, 2, 2>>(g, stream);
+  if (f == 15) return launch_tile<Tile<1, 2, 2, 2, 3>>(g, stream);
+  if (f == 16) return launch_tile<Tile<1, 1, 2, 2, 3>>(g, stream);
+  if (f == 17) return launch_tile<Tile<2, 1, 2, 4, 3>>(g, stream);
+  if (f == 18) return launch_tile<Tile<1, 1, 2, 4, 3>>(g, stream);
+  if (f == 19) return launch_tile<Tile<2, 2, 2, 4, 3>>(g, stream);
+  if (f == 20) return launch_tile<Tile<1, 1, 2, 4, 4>>(g, stream);
+  if (f == 21) return launch_tile<Tile<1, 1, 4, 4, 3>>(g, stream);
   if (f == 7 && M <= 16) return launch_rows<1, 1, 8, 8>(g, stream);
   if (f == 8 && M <= 16) return launch_rows<1, 1, 8, 4>(g, stream);
   if (f == 9 && M <= 16) return launch_rows<1, 1, 16, 4>(g, stream);

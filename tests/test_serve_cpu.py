@@ -27,7 +27,8 @@ GEMM = dict(qa=P, lda=1024, a_scale=P, M=4, K=1024, w=P, ldw=1024, w_scale=P, N=
     (dict(K=-16), UNS), (dict(mean=P), INV), (dict(w1=P), INV), (dict(qa=None), INV), (dict(a_scale=None), INV), (dict(w=None), INV),
     (dict(w_scale=None), INV), (dict(y=None), INV), (dict(lda=1008), INV), (dict(ldw=1008), INV), (dict(ldy=63), INV),
     (dict(lda=1032), ALN), (dict(ldw=1032), ALN), (dict(qa=P4), ALN), (dict(w=P4), ALN), (dict(y=P1), ALN), (dict(a_scale=P1), ALN),
-    (dict(bias=P1), ALN), (dict(M=(1 << 30) + 1), UNS)])
+    (dict(bias=P1), ALN), (dict(M=(1 << 30) + 1), UNS),
+    (dict(lda=(1 << 23) + 16), UNS), (dict(ldw=1 << 24), UNS)])
 def test_gemm_w8a8(change, code):
     assert _call("oq_gemm_w8a8", GEMM, change) == code and b"oq_gemm_w8a8" in oq.lib().oq_last_error()
 
