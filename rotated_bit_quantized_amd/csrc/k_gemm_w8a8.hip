@@ -17,8 +17,6 @@
 // MFMAs of the current ones.
 #include "oq_internal.h"
 
-#include <cstdlib>
-
 namespace oq {
 namespace {
 
@@ -405,33 +403,21 @@ hipError_t launch_gemm_w8a8(const int8_t *qa, int64_t lda, const float *a_scale,
                             int64_t ldw, const float *w_scale, int N, const float *mean, const float *w1,
                             const float *bias, uint16_t *y, int64_t ldy, hipStream_t stream) {
   const GemmArgs g{qa, lda, a_scale, M, K, w, ldw, w_scale, N, mean, w1, bias, y, ldy};
-  int f = 0;
-  if (const char *e = getenv("W8")) f = atoi(e);
-  if (f == 1 && M <= 16) return launch_rows<1, 1, 4, 8>(g, stream);
-  if (f == 2 && M <= 32) return launch_rows<2, 1, 4, 8>(g, stream);
-  if (f == 3) return launch_tile<Tile<1, 1, 2, 2, 4>>(g, stream);
-  if (f == 4) return launch_tile<Tile<2, 2, 2, 2, 2>>(g, stream);
-  if (f == 6) return launch_tile<Tile<4, 2, 2, 4, 2>>(g, stream);
-  if (f == 12) return launch_tile<Tile<2, 2, 2, 2, 3>>(g, stream);
-  if (f == 13) return launch_tile<Tile<2, 1, 2, 2, 3>>(g, stream);
-  if (f == 14) return launch_tile<Tile<2, 4, 4, 2, 2>>(g, stream);
-  if (f == 15) return launch_tile<Tile<1, 2, 2, 2, 3>>(g, stream);
-  if (f == 16) return launch_tile<Tile<1, 1, 2, 2, 3>>(g, stream);
-  if (f == 17) return launch_tile<Tile<2, 1, 2, 4, 3>>(g, stream);
-  if (f == 18) return launch_tile<Tile<1, 1, 2, 4, 3>>(g, stream);
-  if (f == 19) return launch_tile<Tile<2, 2, 2, 4, 3>>(g, stream);
-  if (f == 20) return launch_tile<Tile<1, 1, 2, 4, 4>>(g, stream);
-  if (f == 21) return launch_tile<Tile<1, 1, 4, 4, 3>>(g, stream);
-  if (f == 7 && M <= 16) return launch_rows<1, 1, 8, 8>(g, stream);
-  if (f == 8 && M <= 16) return launch_rows<1, 1, 8, 4>(g, stream);
-  if (f == 9 && M <= 16) return launch_rows<1, 1, 16, 4>(g, stream);
-  if (f == 10 && M <= 16) return launch_rows<1, 1, 4, 16>(g, stream);
-  if (f == 11 && M <= 16) return launch_rows<1, 2, 4, 8>(g, stream);
-  if (M <= 16) return launch_rows<1, 1, 4, 8>(g, stream);
+  if (M <= 16) return launch_rows<1, 1, 8, 8>(g, stream);
   if (M <= 32) return launch_rows<2, 1, 4, 8>(g, stream);
-  if (((M + 255) / 256) * ((N + 255) / 256) >= 128) return launch_tile<Tile<4, 2, 2, 4, 2>>(g, stream);
-  if (((M + 127) / 128) * ((N + 127) / 128) >= 128) return launch_tile<Tile<2, 2, 2, 2, 4>>(g, stream);
-  return launch_tile<Tile<1, 1, 2, 2, 4>>(g, stream);
+  // The tile with the least modelled time, rounds of workgroups over the CUs
+  // times the measured time of a round at K = 4096 (us; K scales all alike):
+  // 256 x 256 59, 128 x 256 34, 128 x 128 20, 64 x 64 7.3 and 4 for the first.
+  // Measured with K = 4096, N = 4096: 512 tokens 42.7 / 25.6 / 19.4 / 16.3, 1024
+  // 44.2 / 28.5 / 22.1 / 30, 2048 47.4 / 36.2 / 40.6, 4096 63.4 / 67.4 / 77.4.
+  const int64_t cus = device_cus();
+  auto rounds = [&](int64_t bm, int64_t bn) { return (double)(((M + bm - 1) / bm * ((N + bn - 1) / bn) + cus - 1) / cus); };
+  const double c256 = 59 * rounds(256, 256), c384 = 34 * rounds(128, 256), c128 = 20 * rounds(128, 128),
+               c64 = 4 + 7.3 * rounds(64, 64);
+  if (c256 <= c384 && c256 <= c128 && c256 <= c64) return launch_tile<Tile<2, 4, 4, 2, 2>>(g, stream);
+  if (c384 <= c128 && c384 <= c64) return launch_tile<Tile<2, 2, 2, 4, 3>>(g, stream);
+  if (c128 <= c64) return launch_tile<Tile<2, 1, 2, 4, 3>>(g, stream);
+  return launch_tile<Tile<1, 1, 2, 2, 3>>(g, stream);
 }
 
 }  // namespace oq

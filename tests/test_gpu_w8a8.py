@@ -29,7 +29,7 @@ def _case(M, K, N, center, bias, seed=0, lda=None, ldw=None, lo=-127, hi=127):
     mean = torch.randn(M, generator=g) * 3 if center else None
     w1 = torch.randn(N, generator=g) if center else None
     b = torch.randn(N, generator=g) if bias else None
-    acc = qa.double() @ w.double().t()
+    acc = (qa.to(DEV).double() @ w.to(DEV).double().t()).cpu()  # whole numbers below 2^53: exact
     p = a_s.double()[:, None] * w_s.double() * acc
     exact, mag = p.clone(), p.abs()
     if center:
@@ -67,6 +67,8 @@ SHAPES = [
     (129, 3072, 257), (200, 96, 1000), (256, 1024, 1024), (257, 1040, 383), (333, 1920, 770),
     # several tiles each way, odd remainders
     (511, 144, 513), (640, 2048, 1152), (1000, 1008, 1100), (1025, 528, 2049), (2049, 272, 777), (4096, 1040, 1100),
+    # the widest tiles, ragged
+    (4090, 400, 4085), (2030, 272, 4001), (1000, 144, 4099),
     # wide and tall
     (5, 64, 20001), (4097, 48, 3), (300, 16400, 40), (1, 131056, 5),
 ]
