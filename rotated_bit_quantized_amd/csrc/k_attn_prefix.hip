@@ -60,17 +60,27 @@ __device__ __forceinline__ int swz_k(int row) { return D == 128 ? row & 15 : (ro
 template <int D>
 __device__ __forceinline__ int swz_v(int row) { return D == 128 ? (row & 3) << 2 : ((row >> 1) & 1) << 2; }
 
-__device__ __forceinline__ float xhalf(float v) { return __shfl_xor(v, 32); }
+// the other half's value
+__device__ __forceinline__ float xhalf(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(threadIdx.x & 32 ? r[0] : r[1]);
+}
 
-template <int D, int NW, int QT, int KT>
-__global__ void __launch_bounds__(64 * NW, NW == 4 && QT == 2 ? 1 : 2)
+template <int C>
+__device__ __forceinline__ void wait_vm() {
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (C & 0xF) | ((C >> 4) << 14));
+}
+
+template <int D, int NW, int KT>
+__global__ void __launch_bounds__(64 * NW, 2)
 attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o, float2 *__restrict__ part_ml) {
   constexpr int KS = D / 16, DT = D / 32, SUB = KT / 32;
-  constexpr int ROWB = 2 * D;              // bytes of a key row
-  constexpr int TILE = KT * ROWB;          // bytes of a K or V tile
-  constexpr int PIECES = TILE / 1024 / NW;  // 1 KiB copies per wavefront and tile
+  constexpr int ROWB = 2 * D;               // bytes of a key row
+  constexpr int TILE = KT * ROWB;           // bytes of a K or V tile
+  constexpr int PIECES = TILE / 1024 / NW;  // 1 KiB copies per wavefront and K or V tile
+  constexpr int PROWS = 1024 / ROWB;        // key rows of one: 4 or 8, on one page
   static_assert(PIECES * NW * 1024 == TILE, "every wavefront copies the same share");
-  __shared__ __attribute__((aligned(1024))) uint8_t s_kv[2][2 * TILE];
+  __shared__ __attribute__((aligned(1024))) uint8_t s_kv[4 * TILE];  // K slots 0, 1, V slots 0, 1
   __shared__ int s_page[PAGES_MAX];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r32 = lane & 31, half = lane >> 5;
@@ -89,7 +99,7 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
   // rows [r0, rend) of key head hk, keys [k0, n) of the part's places
   const int rbase = p.suffix ? b * a.n_q * G : 0;
   const int rend = p.suffix ? rbase + a.n_q * G : p.rows;
-  const int r0 = rbase + tile * 32 * QT * NW + wave * 32 * QT;
+  const int r0 = rbase + tile * 32 * NW + wave * 32;
   int chunk = p.chunk;
   int len = a.prefix_len, first = 0;  // row r sees places below min(n, len - first + token)
   const int32_t *table = a.prefix_table;
@@ -100,7 +110,7 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
     len = a.lens[b] > 0 ? a.lens[b] : 0;
     first = a.n_q - 1;
     // what the tile's last row sees
-    int rl = rbase + (tile + 1) * 32 * QT * NW;
+    int rl = rbase + (tile + 1) * 32 * NW;
     if (rl > rend) rl = rend;
     const int64_t see = (int64_t)len - first + ((rl - 1) / G - b * a.n_q);
     n = see < 0 ? 0 : see < cap ? (int)see : cap;
@@ -113,10 +123,7 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
   const int k0 = k0l < n ? (int)k0l : n;
   const int64_t prow = (int64_t)(p.part0 + split) * a.kv.heads * p.rows + (int64_t)hk * p.rows;
   if (k0 >= n) {
-    if (half == 0)
-#pragma unroll
-      for (int t = 0; t < QT; ++t)
-        if (r0 + 32 * t + r32 < rend) part_ml[prow + r0 + 32 * t + r32] = make_float2(-INFINITY, 0.f);
+    if (half == 0 && r0 + r32 < rend) part_ml[prow + r0 + r32] = make_float2(-INFINITY, 0.f);
     return;
   }
   const int kend = n - k0 < chunk ? n : k0 + chunk;
@@ -131,200 +138,256 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
     bad |= (unsigned)pg >= (unsigned)a.kv.pages;
   }
   const bool any_bad = __syncthreads_or(bad);
+  const int kfull = any_bad ? k0 : kend;  // tiles that end at or below have all their keys
 
+  // Copies of tile `base` into a slot.  A piece is PROWS key rows of one page,
+  // so its source is a scalar base and a fixed offset per lane; the 16-byte
+  // chunks of a row are permuted by the row, on the source side, against bank
+  // conflicts.  In a tile with missing keys the rows of those come from zeros,
+  // so that no stale NaN meets a zero weight in the second product.
   const uint8_t *kb = reinterpret_cast<const uint8_t *>(a.kv.k + (int64_t)hk * a.kv.page * D);
   const uint8_t *vb = reinterpret_cast<const uint8_t *>(a.kv.v + (int64_t)hk * a.kv.page * D);
-  const uint32_t lds0 = lds_addr_of(&s_kv[0][0]);
-  auto issue = [&](int buf, int base) {
+  const uint32_t lds0 = lds_addr_of(s_kv);
+  const int prow_l = lane * 16 / ROWB, phys_l = lane * 16 % ROWB / 16;  // this lane's row and chunk of a piece
+  auto off_of = [&](int base, int q) -> int64_t {
+    const int key = base + (wave * PIECES + q) * PROWS;
+    const int pg = __builtin_amdgcn_readfirstlane(s_page[(key - k0) >> pl]);
+    return (int64_t)pg * (2 * a.kv.page_stride) + (key & (a.kv.page - 1)) * ROWB;
+  };
+  auto copy = [&](const uint8_t *from, bool is_v, int base, int slot) {
 #pragma unroll
     for (int q = 0; q < PIECES; ++q) {
-      const int pos = (wave * PIECES + q) * 1024 + lane * 16;
-      const int row = pos / ROWB, phys = (pos % ROWB) / 16;
-      const int key = base + row;
-      const int pg = key < kend ? s_page[(key - k0) >> pl] : -1;
-      const int ck = 16 * (phys ^ swz_k<D>(row)), cv = 16 * (phys ^ swz_v<D>(row));
-      const int64_t off = (int64_t)pg * (2 * a.kv.page_stride) + (key & (a.kv.page - 1)) * ROWB;
-      const bool ok = (unsigned)pg < (unsigned)a.kv.pages;
-      const uint8_t *zero = reinterpret_cast<const uint8_t *>(g_zero_row);
-      const uint8_t *sk = ok ? kb + off + ck : zero + ck;
-      const uint8_t *sv = ok ? vb + off + cv : zero + cv;
-      const uint32_t dst = lds0 + buf * 2 * TILE + (wave * PIECES + q) * 1024;
-      dma_lds16(sk, dst);
-      dma_lds16(sv, dst + TILE);
+      const int row = (wave * PIECES + q) * PROWS + prow_l;
+      const uint32_t c = 16 * (phys_l ^ (is_v ? swz_v<D>(row) : swz_k<D>(row)));
+      const uint32_t dst = lds0 + slot * TILE + (wave * PIECES + q) * 1024;
+      if (base + KT <= kfull) {
+        dma_lds16_s(from + off_of(base, q), prow_l * ROWB + c, dst);
+      } else {
+        const int key = base + row;
+        const int pg = key < kend ? s_page[(key - k0) >> pl] : -1;
+        const bool ok = (unsigned)pg < (unsigned)a.kv.pages;
+        const uint8_t *at = from + (int64_t)pg * (2 * a.kv.page_stride) + (key & (a.kv.page - 1)) * ROWB;
+        dma_lds16((ok ? at : reinterpret_cast<const uint8_t *>(g_zero_row)) + c, dst);
+      }
     }
   };
-  issue(0, k0);
+  copy(kb, false, k0, 0);
+  copy(kb, false, k0 + KT, 1);
+  copy(vb, true, k0, 2);
 
-  // this lane's rows: query fragments, number of places seen
-  v8bf qf[QT][KS];
-  int lim[QT];
-#pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    int r = r0 + 32 * t + r32;
+  // this lane's row: query fragments, number of places seen
+  v8bf qf[KS];
+  int lim;
+  {
+    int r = r0 + r32;
     if (r > rend - 1) r = rend - 1;
     const int tok = r / G, h = hk * G + (r - tok * G);
     const int64_t see = p.suffix ? (int64_t)len - first + (tok - b * a.n_q) : n;
-    lim[t] = see < kend ? (int)see : kend;
+    lim = see < kend ? (int)see : kend;
     const uint16_t *src = a.q + tok * a.q_ld + h * a.q_hs + 8 * half;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       u32x4 v = *reinterpret_cast<const u32x4 *>(src + 16 * ks);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = (v[e] & p.qand) ^ p.qxor;
-      qf[t][ks] = __builtin_bit_cast(v8bf, v);
+      qf[ks] = __builtin_bit_cast(v8bf, v);
     }
   }
 
-  v16f O[QT][DT];
-  float m[QT], l[QT];
+  // fragment addresses: K row r32 of a 32-key block, chunk 2 ks + half; V keys
+  // 16 kk + 8 w + 4 half + .. and d 32 dt + ..
+  auto k_frag = [&](int slot, int u, int ks) -> v8bf {
+    const int row = 32 * u + r32;
+    return *reinterpret_cast<const v8bf *>(s_kv + slot * TILE + row * ROWB + 16 * ((2 * ks + half) ^ swz_k<D>(row)));
+  };
+  auto v_frag = [&](int slot, int kk, int d) -> v8bf {
+    v8s vf;
 #pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    m[t] = -INFINITY;
-    l[t] = 0.f;
+    for (int w = 0; w < 2; ++w) {
+      const int row = 16 * kk + 8 * w + 4 * half + ((lane & 15) >> 2);
+      const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+      const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)(
+          s_kv + (2 + slot) * TILE + row * ROWB + 16 * (c ^ swz_v<D>(row)) + 8 * (lane & 1)));
 #pragma unroll
-    for (int d = 0; d < DT; ++d) O[t][d] = (v16f){};
+      for (int e = 0; e < 4; ++e) vf[4 * w + e] = x[e];
+    }
+    return __builtin_bit_cast(v8bf, vf);
+  };
+
+  v16f O[DT];
+  float m = -INFINITY, l[2] = {0.f, 0.f};
+#pragma unroll
+  for (int d = 0; d < DT; ++d) O[d] = (v16f){};
+
+  // Masks the scores of tile `base` where it needs it and moves the reference m
+  // (with O and l) where a row's maximum has outgrown it.
+  v16f S[SUB];
+  auto settle = [&](int base) {
+    if (base + KT > kfull || !__all(base + KT <= lim)) {
+      // the keys of the tile that are there: below kend, on a page of the cache
+      const int key = base + lane;
+      const uint64_t there =
+          __ballot(key < kend && (unsigned)s_page[(key < kend ? key - k0 : 0) >> pl] < (unsigned)a.kv.pages);
+      // bit 8 (e >> 2) + (e & 3) of a word: element e's key is there and seen
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+        const int s = lim - base - 32 * u;
+        uint32_t bits = (uint32_t)(there >> (32 * u)) & (s >= 32 ? ~0u : s <= 0 ? 0u : (1u << s) - 1u);
+        bits >>= 4 * half;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) S[u][e] = (bits >> (8 * (e >> 2) + (e & 3))) & 1u ? S[u][e] : -INFINITY;
+      }
+    }
+    float mx = S[0][0];
+#pragma unroll
+    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) mx = __builtin_elementwise_maximum(mx, S[u][e]);
+    mx = fmaxf(mx, xhalf(mx)) * p.c;
+    if (__any(mx > m + RESCALE)) {
+      const float mn = fmaxf(m, mx);
+      const float al = mn == -INFINITY ? 1.f : exp2f(m - mn);
+      m = mn;
+      l[0] *= al;
+      l[1] *= al;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) O[d][e] *= al;
+    }
+  };
+
+  // scores of the first tile
+  wait_vm<2 * PIECES>();
+  asm volatile("" ::: "memory");
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < SUB; ++u) {
+    S[u] = (v16f){};
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) S[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k_frag(0, u, ks), qf[ks], S[u], 0, 0, 0);
   }
+  settle(k0);
+
+  // Step i: scores of tile i + 1 (K slot (i + 1) & 1) and the value product of
+  // tile i (V slot i & 1), its softmax numerators formed in between, so that
+  // the matrix and the vector units work at the same time.  Per 32 keys KS +
+  // 2 DT products, each with its fragment read AHEAD products before and, after
+  // it, its share of the numerators (pairs of them; those of 8 keys per half
+  // wave, 4 pairs, are due before the first product that takes them).
+  constexpr int PER = KS + 2 * DT, SLOTS = SUB * PER, PAIRS = 8 * SUB, AHEAD = 3;
   const int steps = (kend - k0 + KT - 1) / KT;
   for (int st = 0; st < steps; ++st) {
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // this wavefront's copies of the tile have landed
+    const int base = k0 + st * KT, ks_slot = (st + 1) & 1, v_slot = st & 1;
+    wait_vm<0>();  // this wavefront's copies of K of tile i + 1 and V of tile i have landed
     asm volatile("" ::: "memory");
-    if (NW > 1) __builtin_amdgcn_s_barrier();  // and everybody's; nobody reads the other buffer any more
-    asm volatile("" ::: "memory");
-    const int base = k0 + st * KT;
-    if (st + 1 < steps) issue((st + 1) & 1, base + KT);
-    const uint8_t *tk = s_kv[st & 1], *tv = s_kv[st & 1] + TILE;
-
-    v16f S[QT][SUB];
-#pragma unroll
-    for (int u = 0; u < SUB; ++u) {
-#pragma unroll
-      for (int t = 0; t < QT; ++t) S[t][u] = (v16f){};
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const int row = 32 * u + r32;
-        const v8bf kf = *reinterpret_cast<const v8bf *>(tk + row * ROWB + 16 * ((2 * ks + half) ^ swz_k<D>(row)));
-#pragma unroll
-        for (int t = 0; t < QT; ++t) S[t][u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[t][ks], S[t][u], 0, 0, 0);
-      }
+    __syncthreads();  // and everybody's; nobody reads the other slots any more
+    if (st + 1 < steps) {
+      copy(kb, false, base + 2 * KT, v_slot);
+      copy(vb, true, base + KT, 2 + ks_slot);
     }
+    __builtin_amdgcn_sched_barrier(0);
 
-    // the keys of the tile that are there: below kend, on a page of the cache
-    const bool masked = any_bad || base + KT > kend;
-    uint64_t there = ~0ull;
-    if (masked) {
-      const int key = base + lane;
-      there = __ballot(key < kend && (unsigned)s_page[(key < kend ? key - k0 : 0) >> pl] < (unsigned)a.kv.pages);
-    }
-
-    v8bf pf[QT][2 * SUB];
+    const float mu = m == -INFINITY ? 0.f : m;
+    v16f Sn[SUB];
+    v8bf pf[2 * SUB], frag[AHEAD + 1];
+    auto frag_of = [&](int t) -> v8bf {
+      const int u = t / PER, w = t % PER;
+      return w < KS ? k_frag(ks_slot, u, w) : v_frag(v_slot, 2 * u + (w - KS) / DT, (w - KS) % DT);
+    };
 #pragma unroll
-    for (int t = 0; t < QT; ++t) {
-      if (masked || !__all(base + KT <= lim[t])) {
-        // bit 4 half + 8 (e >> 2) + (e & 3) of word u: element e's key is there and seen
-        const int seen = lim[t] - base;
+    for (int t = 0; t < AHEAD; ++t) frag[t] = frag_of(t);
 #pragma unroll
-        for (int u = 0; u < SUB; ++u) {
-          const int s = seen - 32 * u;
-          uint32_t bits = (uint32_t)(there >> (32 * u)) & (s >= 32 ? ~0u : s <= 0 ? 0u : (1u << s) - 1u);
-          bits >>= 4 * half;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) S[t][u][e] = (bits >> (8 * (e >> 2) + (e & 3))) & 1u ? S[t][u][e] : -INFINITY;
-        }
+    for (int t = 0; t < SLOTS; ++t) {
+      if (t + AHEAD < SLOTS) frag[(t + AHEAD) % (AHEAD + 1)] = frag_of(t + AHEAD);
+      const int u = t / PER, w = t % PER;
+      const v8bf f = frag[t % (AHEAD + 1)];
+      if (w < KS) {
+        Sn[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, qf[w], w == 0 ? (v16f){} : Sn[u], 0, 0, 0);
+      } else {
+        const int kk = 2 * u + (w - KS) / DT, d = (w - KS) % DT;
+        O[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pf[kk], O[d], 0, 0, 0);
       }
-      float mx = S[t][0][0];
+      constexpr int RATE = D == 64 ? 4 : 2;  // thirds of a pair per product
 #pragma unroll
-      for (int u = 0; u < SUB; ++u)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) mx = __builtin_elementwise_maximum(mx, S[t][u][e]);
-      mx = fmaxf(mx, xhalf(mx)) * p.c;
-      if (__any(mx > m[t] + RESCALE)) {
-        const float mn = fmaxf(m[t], mx);
-        const float al = mn == -INFINITY ? 1.f : exp2f(m[t] - mn);
-        m[t] = mn;
-        l[t] *= al;
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) O[t][d][e] *= al;
+      for (int pr = t * RATE / 3 + (t > 0); pr < (t + 1) * RATE / 3 + 1 && pr < PAIRS; ++pr) {
+        const int pu = pr / 8, e = 2 * (pr % 8);
+        const float x0 = __builtin_amdgcn_exp2f(__builtin_fmaf(S[pu][e], p.c, -mu));
+        const float x1 = __builtin_amdgcn_exp2f(__builtin_fmaf(S[pu][e + 1], p.c, -mu));
+        l[0] += x0;
+        l[1] += x1;
+        pf[2 * pu + (e >> 3)][e & 7] = (__bf16)x0;
+        pf[2 * pu + (e >> 3)][(e & 7) + 1] = (__bf16)x1;
       }
-      const float mu = m[t] == -INFINITY ? 0.f : m[t];
-#pragma unroll
-      for (int u = 0; u < SUB; ++u)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(S[t][u][e], p.c, -mu));
-          l[t] += x;
-          pf[t][2 * u + (e >> 3)][e & 7] = (__bf16)x;
-        }
+      __builtin_amdgcn_sched_barrier(0);
     }
-
 #pragma unroll
-    for (int kk = 0; kk < 2 * SUB; ++kk) {
-#pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        v8s vf;
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const int row = 16 * kk + 8 * w + 4 * half + ((lane & 15) >> 2);
-          const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-          const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (__attribute__((address_space(3))) v4s *)(tv + row * ROWB + 16 * (c ^ swz_v<D>(row)) + 8 * (lane & 1)));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) vf[4 * w + e] = x[e];
-        }
-#pragma unroll
-        for (int t = 0; t < QT; ++t)
-          O[t][d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, vf), pf[t][kk], O[t][d], 0, 0, 0);
-      }
-    }
-    if (NW == 1) __builtin_amdgcn_s_waitcnt(0xC07F);  // reads of this buffer are done before its next copies
+    for (int u = 0; u < SUB; ++u) S[u] = Sn[u];
+    if (st + 1 < steps) settle(base + KT);
   }
 
+  const int r = r0 + r32;
+  const float ls = l[0] + l[1], lt = ls + xhalf(ls);
+  if (r >= rend) return;
+  if (half == 0) part_ml[prow + r] = make_float2(m, lt);
+  float *dst = part_o + (prow + r) * D + 4 * half;
 #pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    const int r = r0 + 32 * t + r32;
-    const float lt = l[t] + xhalf(l[t]);
-    if (r >= rend) continue;
-    if (half == 0) part_ml[prow + r] = make_float2(m[t], lt);
-    float *dst = part_o + (prow + r) * D + 4 * half;
+  for (int d = 0; d < DT; ++d)
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        *reinterpret_cast<float4 *>(dst + 32 * d + 8 * e) =
-            make_float4(O[t][d][4 * e], O[t][d][4 * e + 1], O[t][d][4 * e + 2], O[t][d][4 * e + 3]);
-  }
+    for (int e = 0; e < 4; ++e)
+      *reinterpret_cast<float4 *>(dst + 32 * d + 8 * e) =
+          make_float4(O[d][4 * e], O[d][4 * e + 1], O[d][4 * e + 2], O[d][4 * e + 3]);
 }
 
-// The join: D / 4 lanes per row.
+// The join, one wavefront per row: lanes hold the parts' statistics, 64 parts
+// at a time; D / 4 lanes then take a part's O each, 256 / D parts at once.
 template <int D>
 __global__ void __launch_bounds__(256)
 attn_join_kernel(const AttnArgs a, int rows, int parts, const float *__restrict__ part_o, const float2 *__restrict__ part_ml) {
-  constexpr int L = D / 4;
+  constexpr int L = D / 4, AT = 64 / L;
   const int64_t all = (int64_t)rows * a.kv.heads;
-  const int64_t id = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
-  const int gl = threadIdx.x % L;
+  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, gl = lane % L, sub = lane / L;
   if (id >= all) return;
-  float m = -INFINITY;
-  for (int s = 0; s < parts; ++s) {
-    const float2 v = part_ml[s * all + id];
-    m = fmaxf(m, v.x);
-  }
-  float l = 0.f;
+  float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (m != -INFINITY) {
-    for (int s = 0; s < parts; ++s) {
-      const float2 v = part_ml[s * all + id];
-      if (v.y == 0.f) continue;  // no keys: its O is not written
-      const float w = exp2f(v.x - m);
-      const float4 x = *reinterpret_cast<const float4 *>(part_o + (s * all + id) * D + 4 * gl);
-      l = __builtin_fmaf(w, v.y, l);
-      o.x = __builtin_fmaf(w, x.x, o.x);
-      o.y = __builtin_fmaf(w, x.y, o.y);
-      o.z = __builtin_fmaf(w, x.z, o.z);
-      o.w = __builtin_fmaf(w, x.w, o.w);
+  for (int s0 = 0; s0 < parts; s0 += 64) {
+    float2 v = make_float2(-INFINITY, 0.f);
+    if (s0 + lane < parts) v = part_ml[(s0 + lane) * all + id];
+    float mx = v.x;
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) mx = fmaxf(mx, __shfl_xor(mx, x));
+    const float mn = fmaxf(m, mx);
+    if (mn == -INFINITY) continue;
+    const float al = exp2f(m - mn);
+    m = mn;
+    // a part without keys has no O written
+    const float w = v.y == 0.f ? 0.f : exp2f(v.x - m);
+    float ls = w * v.y;
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) ls += __shfl_xor(ls, x);
+    l = l * al + ls;
+    o.x *= al, o.y *= al, o.z *= al, o.w *= al;
+    const int np = parts - s0 < 64 ? parts - s0 : 64;
+#pragma unroll 4
+    for (int s = 0; s < np; s += AT) {
+      const float ws = __shfl(w, s + sub);
+      if (ws == 0.f) continue;  // parts past the end have weight zero
+      const float4 x = *reinterpret_cast<const float4 *>(part_o + ((s0 + s + sub) * all + id) * D + 4 * gl);
+      o.x = __builtin_fmaf(ws, x.x, o.x);
+      o.y = __builtin_fmaf(ws, x.y, o.y);
+      o.z = __builtin_fmaf(ws, x.z, o.z);
+      o.w = __builtin_fmaf(ws, x.w, o.w);
     }
   }
+#pragma unroll
+  for (int x = L; x < 64; x <<= 1) {
+    o.x += __shfl_xor(o.x, x);
+    o.y += __shfl_xor(o.y, x);
+    o.z += __shfl_xor(o.z, x);
+    o.w += __shfl_xor(o.w, x);
+  }
+  if (lane >= L) return;
   const int G = a.heads_q / a.kv.heads;
   const int hk = (int)(id / rows), r = (int)(id - (int64_t)hk * rows);
   const int tok = r / G, h = hk * G + (r - tok * G);
@@ -333,20 +396,20 @@ attn_join_kernel(const AttnArgs a, int rows, int parts, const float *__restrict_
   y.x = (uint32_t)f32_to_bf16_rne(o.x * inv) | ((uint32_t)f32_to_bf16_rne(o.y * inv) << 16);
   y.y = (uint32_t)f32_to_bf16_rne(o.z * inv) | ((uint32_t)f32_to_bf16_rne(o.w * inv) << 16);
   *reinterpret_cast<uint2 *>(a.o + tok * a.o_ld + h * a.o_hs + 4 * gl) = y;
-  if (a.lse && gl == 0) a.lse[(int64_t)tok * a.heads_q + h] = m == -INFINITY ? -INFINITY : LN2 * (m + log2f(l));
+  if (a.lse && lane == 0) a.lse[(int64_t)tok * a.heads_q + h] = m == -INFINITY ? -INFINITY : LN2 * (m + log2f(l));
 }
 
 // Row tile shape: wavefronts and 32-row blocks per wavefront.
 struct Shape {
-  int nw, qt, kt;
-  int rows() const { return 32 * nw * qt; }
+  int nw, kt;
+  int rows() const { return 32 * nw; }
 };
 
 Shape shape_for(int rows) {
-  if (rows <= 32) return {1, 1, 32};
-  if (rows <= 64) return {2, 1, 64};
-  if (rows <= 128) return {4, 1, 64};
-  return {4, 2, 64};
+  if (rows <= 32) return {1, 32};
+  if (rows <= 64) return {2, 64};
+  if (rows <= 128) return {4, 64};
+  return {8, 64};
 }
 
 struct Plan {
@@ -380,7 +443,7 @@ Plan plan_for(const AttnArgs &a) {
     const int64_t unit = a.kv.page > sh.kt ? a.kv.page : sh.kt;
     const int64_t groups = (int64_t)q.tiles * a.kv.heads * (s ? a.B : 1);
     // enough workgroups for every CU: 1 of 4 wavefronts with 64 rows each, 8 single ones
-    const int64_t want = (int64_t)device_cus() * (sh.nw == 4 ? (sh.qt == 2 ? 1 : 2) : sh.nw == 2 ? 4 : 8);
+    const int64_t want = (int64_t)device_cus() * (8 / sh.nw);
     int64_t splits = want / groups;
     if (splits < 1) splits = 1;
     int64_t chunk = round_up((keys + splits - 1) / splits, unit);
@@ -394,9 +457,9 @@ Plan plan_for(const AttnArgs &a) {
   return p;
 }
 
-template <int D, int NW, int QT, int KT>
+template <int D, int NW, int KT>
 hipError_t launch_part(const AttnArgs &a, const PartPlan &p, float *po, float2 *pm, hipStream_t stream) {
-  hipLaunchKernelGGL((attn_part_kernel<D, NW, QT, KT>), dim3((unsigned)p.items), dim3(64 * NW), 0, stream, a, p, po, pm);
+  hipLaunchKernelGGL((attn_part_kernel<D, NW, KT>), dim3((unsigned)p.items), dim3(64 * NW), 0, stream, a, p, po, pm);
   return hipGetLastError();
 }
 
@@ -406,14 +469,13 @@ hipError_t launch_d(const AttnArgs &a, const Plan &p, float *po, float2 *pm, hip
     if (!p.part[s].items) continue;
     if (p.part[s].items > 0x7fffffff) return hipErrorInvalidConfiguration;
     const Shape sh = p.shape[s];
-    const hipError_t e = sh.nw == 1   ? launch_part<D, 1, 1, 32>(a, p.part[s], po, pm, stream)
-                         : sh.nw == 2 ? launch_part<D, 2, 1, 64>(a, p.part[s], po, pm, stream)
-                         : sh.qt == 1 ? launch_part<D, 4, 1, 64>(a, p.part[s], po, pm, stream)
-                                      : launch_part<D, 4, 2, 64>(a, p.part[s], po, pm, stream);
+    const hipError_t e = sh.nw == 1   ? launch_part<D, 1, 32>(a, p.part[s], po, pm, stream)
+                         : sh.nw == 2 ? launch_part<D, 2, 64>(a, p.part[s], po, pm, stream)
+                         : sh.nw == 4 ? launch_part<D, 4, 64>(a, p.part[s], po, pm, stream)
+                                      : launch_part<D, 8, 64>(a, p.part[s], po, pm, stream);
     if (e != hipSuccess) return e;
   }
-  const int64_t per = 256 / (D / 4);
-  hipLaunchKernelGGL((attn_join_kernel<D>), dim3((unsigned)((p.rows_all + per - 1) / per)), dim3(256), 0, stream, a,
+  hipLaunchKernelGGL((attn_join_kernel<D>), dim3((unsigned)((p.rows_all + 3) / 4)), dim3(256), 0, stream, a,
                      p.part[0].rows, p.parts, po, pm);
   return hipGetLastError();
 }

@@ -107,6 +107,11 @@ __device__ __forceinline__ void dma_lds4(const void *g, uint32_t lds_addr) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(lds_addr)
                : "memory", "m0");
 }
+// dma_lds16 from a wave-uniform base and a 32-bit byte offset per lane
+__device__ __forceinline__ void dma_lds16_s(const void *base, uint32_t off, uint32_t lds_addr) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds_addr)
+               : "memory", "m0");
+}
 #pragma clang diagnostic pop
 
 // byte address of an LDS object, for dma_lds*
