@@ -71,7 +71,7 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt(0x0F70 | (C & 0xF) | ((C >> 4) << 14));
 }
 
-template <int D, int NW, int KT>
+template <int D, int NW, int KT, int GRP>
 __global__ void __launch_bounds__(64 * NW, 2)
 attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o, float2 *__restrict__ part_ml) {
   constexpr int KS = D / 16, DT = D / 32, SUB = KT / 32;
@@ -80,8 +80,10 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
   constexpr int PIECES = TILE / 1024 / NW;  // 1 KiB copies per wavefront and K or V tile
   constexpr int PROWS = 1024 / ROWB;        // key rows of one: 4 or 8, on one page
   static_assert(PIECES * NW * 1024 == TILE, "every wavefront copies the same share");
-  __shared__ __attribute__((aligned(1024))) uint8_t s_kv[4 * TILE];  // K slots 0, 1, V slots 0, 1
-  __shared__ int s_page[PAGES_MAX];
+  constexpr int RING = 2 * GRP;             // tile t of K and of V is in their slot t % RING
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  uint8_t *s_kv = smem;  // K slots, then V slots
+  int *s_page = reinterpret_cast<int *>(smem + 2 * RING * TILE);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r32 = lane & 31, half = lane >> 5;
 
@@ -140,40 +142,42 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
   const bool any_bad = __syncthreads_or(bad);
   const int kfull = any_bad ? k0 : kend;  // tiles that end at or below have all their keys
 
-  // Copies of tile `base` into a slot.  A piece is PROWS key rows of one page,
-  // so its source is a scalar base and a fixed offset per lane; the 16-byte
-  // chunks of a row are permuted by the row, on the source side, against bank
-  // conflicts.  In a tile with missing keys the rows of those come from zeros,
-  // so that no stale NaN meets a zero weight in the second product.
+  // Copies of tile t, piece q of this wavefront, K or V.  A piece is PROWS key
+  // rows of one page, so its source is a scalar base and a fixed offset per
+  // lane; the 16-byte chunks of a row are permuted by the row, on the source
+  // side, against bank conflicts.  In a tile with missing keys the rows of
+  // those come from zeros, so that no stale NaN meets a zero weight in the
+  // second product.
   const uint8_t *kb = reinterpret_cast<const uint8_t *>(a.kv.k + (int64_t)hk * a.kv.page * D);
   const uint8_t *vb = reinterpret_cast<const uint8_t *>(a.kv.v + (int64_t)hk * a.kv.page * D);
   const uint32_t lds0 = lds_addr_of(s_kv);
   const int prow_l = lane * 16 / ROWB, phys_l = lane * 16 % ROWB / 16;  // this lane's row and chunk of a piece
-  auto off_of = [&](int base, int q) -> int64_t {
-    const int key = base + (wave * PIECES + q) * PROWS;
-    const int pg = __builtin_amdgcn_readfirstlane(s_page[(key - k0) >> pl]);
-    return (int64_t)pg * (2 * a.kv.page_stride) + (key & (a.kv.page - 1)) * ROWB;
+  const int steps = (kend - k0 + KT - 1) / KT, full_steps = (kfull - k0) / KT;  // tiles; those that have all their keys
+  auto page_of = [&](int t, int q) { return s_page[(t * KT + (wave * PIECES + q) * PROWS) >> pl]; };
+  auto copy_full = [&](bool is_v, int t, int q, int pg) {
+    const int row = (wave * PIECES + q) * PROWS;
+    const uint32_t c = 16 * (phys_l ^ (is_v ? swz_v<D>(row + prow_l) : swz_k<D>(row + prow_l)));
+    const int64_t off = (int64_t)__builtin_amdgcn_readfirstlane(pg) * (2 * a.kv.page_stride) +
+                        ((k0 + t * KT + row) & (a.kv.page - 1)) * ROWB;
+    dma_lds16_s((is_v ? vb : kb) + off, prow_l * ROWB + c,
+                lds0 + ((is_v ? RING : 0) + t % RING) * TILE + (wave * PIECES + q) * 1024);
   };
-  auto copy = [&](const uint8_t *from, bool is_v, int base, int slot) {
+  auto copy_any = [&](bool is_v, int t) {
 #pragma unroll
     for (int q = 0; q < PIECES; ++q) {
-      const int row = (wave * PIECES + q) * PROWS + prow_l;
+      const int row = (wave * PIECES + q) * PROWS + prow_l, key = k0 + t * KT + row;
       const uint32_t c = 16 * (phys_l ^ (is_v ? swz_v<D>(row) : swz_k<D>(row)));
-      const uint32_t dst = lds0 + slot * TILE + (wave * PIECES + q) * 1024;
-      if (base + KT <= kfull) {
-        dma_lds16_s(from + off_of(base, q), prow_l * ROWB + c, dst);
-      } else {
-        const int key = base + row;
-        const int pg = key < kend ? s_page[(key - k0) >> pl] : -1;
-        const bool ok = (unsigned)pg < (unsigned)a.kv.pages;
-        const uint8_t *at = from + (int64_t)pg * (2 * a.kv.page_stride) + (key & (a.kv.page - 1)) * ROWB;
-        dma_lds16((ok ? at : reinterpret_cast<const uint8_t *>(g_zero_row)) + c, dst);
-      }
+      const int pg = key < kend ? s_page[(key - k0) >> pl] : -1;
+      const uint8_t *at = (is_v ? vb : kb) + (int64_t)pg * (2 * a.kv.page_stride) + (key & (a.kv.page - 1)) * ROWB;
+      dma_lds16(((unsigned)pg < (unsigned)a.kv.pages ? at : reinterpret_cast<const uint8_t *>(g_zero_row)) + c,
+                lds0 + ((is_v ? RING : 0) + t % RING) * TILE + (wave * PIECES + q) * 1024);
     }
   };
-  copy(kb, false, k0, 0);
-  copy(kb, false, k0 + KT, 1);
-  copy(vb, true, k0, 2);
+#pragma unroll
+  for (int t = 0; t <= GRP; ++t) {
+    copy_any(false, t);
+    if (t < GRP) copy_any(true, t);
+  }
 
   // this lane's row: query fragments, number of places seen
   v8bf qf[KS];
@@ -207,7 +211,7 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
       const int row = 16 * kk + 8 * w + 4 * half + ((lane & 15) >> 2);
       const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
       const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)(
-          s_kv + (2 + slot) * TILE + row * ROWB + 16 * (c ^ swz_v<D>(row)) + 8 * (lane & 1)));
+          s_kv + (RING + slot) * TILE + row * ROWB + 16 * (c ^ swz_v<D>(row)) + 8 * (lane & 1)));
 #pragma unroll
       for (int e = 0; e < 4; ++e) vf[4 * w + e] = x[e];
     }
@@ -258,7 +262,7 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
   };
 
   // scores of the first tile
-  wait_vm<2 * PIECES>();
+  wait_vm<0>();
   asm volatile("" ::: "memory");
   __syncthreads();
 #pragma unroll
@@ -269,25 +273,18 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
   }
   settle(k0);
 
-  // Step i: scores of tile i + 1 (K slot (i + 1) & 1) and the value product of
-  // tile i (V slot i & 1), its softmax numerators formed in between, so that
-  // the matrix and the vector units work at the same time.  Per 32 keys KS +
-  // 2 DT products, each with its fragment read AHEAD products before and, after
-  // it, its share of the numerators (pairs of them; those of 8 keys per half
-  // wave, 4 pairs, are due before the first product that takes them).
+  // Step t: scores of tile t + 1 and the value product of tile t, its softmax
+  // numerators formed in between, so that the matrix and the vector units work
+  // at the same time.  Per 32 keys KS + 2 DT products, each with its fragment
+  // read AHEAD products before and, after it, its share of the numerators
+  // (pairs of them; those of 8 keys per half wave, 4 pairs, are due before the
+  // first product that takes them) and of the next copies.
   constexpr int PER = KS + 2 * DT, SLOTS = SUB * PER, PAIRS = 8 * SUB, AHEAD = 3;
-  const int steps = (kend - k0 + KT - 1) / KT;
-  for (int st = 0; st < steps; ++st) {
-    const int base = k0 + st * KT, ks_slot = (st + 1) & 1, v_slot = st & 1;
-    wait_vm<0>();  // this wavefront's copies of K of tile i + 1 and V of tile i have landed
-    asm volatile("" ::: "memory");
-    __syncthreads();  // and everybody's; nobody reads the other slots any more
-    if (st + 1 < steps) {
-      copy(kb, false, base + 2 * KT, v_slot);
-      copy(vb, true, base + KT, 2 + ks_slot);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-
+  auto step = [&](bool fast, int t0) {
+    const int ks_slot = (t0 + 1) % RING, v_slot = t0 % RING;
+    int pg[2 * PIECES];  // of the copies, K and V pieces in turn (past the chunk they are not used)
+#pragma unroll
+    for (int x = 0; x < 2 * PIECES; ++x) pg[x] = page_of(fast ? t0 + GRP + 1 - (x & 1) : 0, x >> 1);
     const float mu = m == -INFINITY ? 0.f : m;
     v16f Sn[SUB];
     v8bf pf[2 * SUB], frag[AHEAD + 1];
@@ -319,12 +316,35 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
         pf[2 * pu + (e >> 3)][e & 7] = (__bf16)x0;
         pf[2 * pu + (e >> 3)][(e & 7) + 1] = (__bf16)x1;
       }
+#pragma unroll
+      for (int x = 0; x < 2 * PIECES; ++x)
+        if (t == 2 + x * (SLOTS - 4) / (2 * PIECES) && fast) copy_full(x & 1, t0 + GRP + 1 - (x & 1), x >> 1, pg[x]);
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int u = 0; u < SUB; ++u) S[u] = Sn[u];
-    if (st + 1 < steps) settle(base + KT);
+  };
+  // GRP steps between barriers: the tiles that they read have landed before,
+  // the copies that they send go to slots that nobody reads any more.
+  for (int t0 = 0; t0 < steps; t0 += GRP) {
+    wait_vm<0>();
+    asm volatile("" ::: "memory");
+    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+    const bool fast = t0 + 2 * GRP < full_steps;  // every tile to be copied has all its keys
+    if (!fast) {
+      for (int g = 0; g < GRP; ++g) {
+        copy_any(false, t0 + g + 1 + GRP);
+        copy_any(true, t0 + g + GRP);
+      }
+    }
+#pragma unroll 1
+    for (int g = t0; g < t0 + GRP && g < steps; ++g) {
+      step(fast, g);
+      if (g + 1 < steps) settle(k0 + (g + 1) * KT);
+    }
   }
+  wait_vm<0>();  // no copy outlives the workgroup
 
   const int r = r0 + r32;
   const float ls = l[0] + l[1], lt = ls + xhalf(ls);
@@ -457,9 +477,13 @@ Plan plan_for(const AttnArgs &a) {
   return p;
 }
 
-template <int D, int NW, int KT>
+template <int D, int NW, int KT, int GRP>
 hipError_t launch_part(const AttnArgs &a, const PartPlan &p, float *po, float2 *pm, hipStream_t stream) {
-  hipLaunchKernelGGL((attn_part_kernel<D, NW, KT>), dim3((unsigned)p.items), dim3(64 * NW), 0, stream, a, p, po, pm);
+  constexpr int LDS = 2 * 2 * GRP * KT * 2 * D + PAGES_MAX * 4;
+  static std::atomic<bool> attr_set[64];
+  const hipError_t e = lds_limit_once((const void *)attn_part_kernel<D, NW, KT, GRP>, LDS, attr_set);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((attn_part_kernel<D, NW, KT, GRP>), dim3((unsigned)p.items), dim3(64 * NW), LDS, stream, a, p, po, pm);
   return hipGetLastError();
 }
 
@@ -469,10 +493,10 @@ hipError_t launch_d(const AttnArgs &a, const Plan &p, float *po, float2 *pm, hip
     if (!p.part[s].items) continue;
     if (p.part[s].items > 0x7fffffff) return hipErrorInvalidConfiguration;
     const Shape sh = p.shape[s];
-    const hipError_t e = sh.nw == 1   ? launch_part<D, 1, 32>(a, p.part[s], po, pm, stream)
-                         : sh.nw == 2 ? launch_part<D, 2, 64>(a, p.part[s], po, pm, stream)
-                         : sh.nw == 4 ? launch_part<D, 4, 64>(a, p.part[s], po, pm, stream)
-                                      : launch_part<D, 8, 64>(a, p.part[s], po, pm, stream);
+    const hipError_t e = sh.nw == 1   ? launch_part<D, 1, 32, 1>(a, p.part[s], po, pm, stream)
+                         : sh.nw == 2 ? launch_part<D, 2, 64, 1>(a, p.part[s], po, pm, stream)
+                         : sh.nw == 4 ? launch_part<D, 4, 64, 1>(a, p.part[s], po, pm, stream)
+                                      : launch_part<D, 8, 64, 2>(a, p.part[s], po, pm, stream);
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL((attn_join_kernel<D>), dim3((unsigned)((p.rows_all + 3) / 4)), dim3(256), 0, stream, a,
