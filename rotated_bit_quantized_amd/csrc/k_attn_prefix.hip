@@ -154,13 +154,15 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
   const int prow_l = lane * 16 / ROWB, phys_l = lane * 16 % ROWB / 16;  // this lane's row and chunk of a piece
   const int steps = (kend - k0 + KT - 1) / KT, full_steps = (kfull - k0) / KT;  // tiles; those that have all their keys
   auto page_of = [&](int t, int q) { return s_page[(t * KT + (wave * PIECES + q) * PROWS) >> pl]; };
-  auto copy_full = [&](bool is_v, int t, int q, int pg) {
+  // (without a branch, so that it can stand between products: where the tile is
+  // not to be copied this way, page 0's first rows go to an unused KiB)
+  auto copy_full = [&](bool fast, bool is_v, int t, int q, int pg) {
     const int row = (wave * PIECES + q) * PROWS;
     const uint32_t c = 16 * (phys_l ^ (is_v ? swz_v<D>(row + prow_l) : swz_k<D>(row + prow_l)));
     const int64_t off = (int64_t)__builtin_amdgcn_readfirstlane(pg) * (2 * a.kv.page_stride) +
                         ((k0 + t * KT + row) & (a.kv.page - 1)) * ROWB;
-    dma_lds16_s((is_v ? vb : kb) + off, prow_l * ROWB + c,
-                lds0 + ((is_v ? RING : 0) + t % RING) * TILE + (wave * PIECES + q) * 1024);
+    const uint32_t dst = ((is_v ? RING : 0) + t % RING) * TILE + (wave * PIECES + q) * 1024;
+    dma_lds16_s((is_v ? vb : kb) + (fast ? off : 0), prow_l * ROWB + c, lds0 + (fast ? dst : 2 * RING * TILE + PAGES_MAX * 4));
   };
   auto copy_any = [&](bool is_v, int t) {
 #pragma unroll
@@ -225,8 +227,7 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
 
   // Masks the scores of tile `base` where it needs it and moves the reference m
   // (with O and l) where a row's maximum has outgrown it.
-  v16f S[SUB];
-  auto settle = [&](int base) {
+  auto settle = [&](v16f (&S)[SUB], int base) {
     if (base + KT > kfull || !__all(base + KT <= lim)) {
       // the keys of the tile that are there: below kend, on a page of the cache
       const int key = base + lane;
@@ -265,13 +266,14 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
   wait_vm<0>();
   asm volatile("" ::: "memory");
   __syncthreads();
+  v16f S[SUB], T[SUB];  // scores of two tiles in turn
 #pragma unroll
   for (int u = 0; u < SUB; ++u) {
     S[u] = (v16f){};
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) S[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k_frag(0, u, ks), qf[ks], S[u], 0, 0, 0);
   }
-  settle(k0);
+  settle(S, k0);
 
   // Step t: scores of tile t + 1 and the value product of tile t, its softmax
   // numerators formed in between, so that the matrix and the vector units work
@@ -280,13 +282,12 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
   // (pairs of them; those of 8 keys per half wave, 4 pairs, are due before the
   // first product that takes them) and of the next copies.
   constexpr int PER = KS + 2 * DT, SLOTS = SUB * PER, PAIRS = 8 * SUB, AHEAD = 3;
-  auto step = [&](bool fast, int t0) {
+  auto step = [&](bool fast, int t0, const v16f (&S)[SUB], v16f (&Sn)[SUB]) {
     const int ks_slot = (t0 + 1) % RING, v_slot = t0 % RING;
     int pg[2 * PIECES];  // of the copies, K and V pieces in turn (past the chunk they are not used)
 #pragma unroll
     for (int x = 0; x < 2 * PIECES; ++x) pg[x] = page_of(fast ? t0 + GRP + 1 - (x & 1) : 0, x >> 1);
     const float mu = m == -INFINITY ? 0.f : m;
-    v16f Sn[SUB];
     v8bf pf[2 * SUB], frag[AHEAD + 1];
     auto frag_of = [&](int t) -> v8bf {
       const int u = t / PER, w = t % PER;
@@ -318,31 +319,34 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
       }
 #pragma unroll
       for (int x = 0; x < 2 * PIECES; ++x)
-        if (t == 2 + x * (SLOTS - 4) / (2 * PIECES) && fast) copy_full(x & 1, t0 + GRP + 1 - (x & 1), x >> 1, pg[x]);
+        if (t == 2 + x * (SLOTS - 4) / (2 * PIECES)) copy_full(fast, x & 1, t0 + GRP + 1 - (x & 1), x >> 1, pg[x]);
       __builtin_amdgcn_sched_barrier(0);
     }
-#pragma unroll
-    for (int u = 0; u < SUB; ++u) S[u] = Sn[u];
   };
-  // GRP steps between barriers: the tiles that they read have landed before,
-  // the copies that they send go to slots that nobody reads any more.
-  for (int t0 = 0; t0 < steps; t0 += GRP) {
+  // GRP (1 or 2) steps between barriers: the tiles that they read have landed
+  // before, the copies that they send go to slots that nobody reads any more.
+  bool fast = false;
+  auto meet = [&](int t0) {
     wait_vm<0>();
     asm volatile("" ::: "memory");
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
-    const bool fast = t0 + 2 * GRP < full_steps;  // every tile to be copied has all its keys
+    fast = t0 + 2 * GRP < full_steps;  // every tile to be copied has all its keys
     if (!fast) {
       for (int g = 0; g < GRP; ++g) {
         copy_any(false, t0 + g + 1 + GRP);
         copy_any(true, t0 + g + GRP);
       }
     }
-#pragma unroll 1
-    for (int g = t0; g < t0 + GRP && g < steps; ++g) {
-      step(fast, g);
-      if (g + 1 < steps) settle(k0 + (g + 1) * KT);
-    }
+  };
+  for (int t0 = 0; t0 < steps; t0 += 2) {
+    meet(t0);
+    step(fast, t0, S, T);
+    if (t0 + 1 == steps) break;
+    settle(T, k0 + (t0 + 1) * KT);
+    if (GRP == 1) meet(t0 + 1);
+    step(fast, t0 + 1, T, S);
+    if (t0 + 2 < steps) settle(S, k0 + (t0 + 2) * KT);
   }
   wait_vm<0>();  // no copy outlives the workgroup
 
@@ -479,7 +483,7 @@ Plan plan_for(const AttnArgs &a) {
 
 template <int D, int NW, int KT, int GRP>
 hipError_t launch_part(const AttnArgs &a, const PartPlan &p, float *po, float2 *pm, hipStream_t stream) {
-  constexpr int LDS = 2 * 2 * GRP * KT * 2 * D + PAGES_MAX * 4;
+  constexpr int LDS = 2 * 2 * GRP * KT * 2 * D + PAGES_MAX * 4 + 1024;
   static std::atomic<bool> attr_set[64];
   const hipError_t e = lds_limit_once((const void *)attn_part_kernel<D, NW, KT, GRP>, LDS, attr_set);
   if (e != hipSuccess) return e;
