@@ -607,7 +607,7 @@ int oq_kv_append(const uint16_t *k, int64_t k_ld, int64_t k_hs, const uint16_t *
  * prefix_table int32 [ceil(prefix_len / page)], tables int32 [B][table_ld]:
  * page numbers in order; lens int32 [B], at most table_ld * page places are
  * read.  Keys on a page number outside [0, pages) are left out.  Cache places
- * that a row does not see may hold anything, NaN included.
+ * that no query token of a sequence sees may hold anything, NaN included.
  * The prefix is read once for all rows of a tile; scores, statistics and sums
  * are float32; softmax numerators enter the value product as bfloat16 (their
  * sum is of the float32 values).

@@ -140,45 +140,64 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
     bad |= (unsigned)pg >= (unsigned)a.kv.pages;
   }
   const bool any_bad = __syncthreads_or(bad);
-  const int kfull = any_bad ? k0 : kend;  // tiles that end at or below have all their keys
-
-  // Copies of tile t, piece q of this wavefront, K or V.  A piece is PROWS key
+  // Copies of tile t, this wavefront's pieces, K or V.  A piece is PROWS key
   // rows of one page, so its source is a scalar base and a fixed offset per
   // lane; the 16-byte chunks of a row are permuted by the row, on the source
-  // side, against bank conflicts.  In a tile with missing keys the rows of
-  // those come from zeros, so that no stale NaN meets a zero weight in the
-  // second product.
+  // side, against bank conflicts.
   const uint8_t *kb = reinterpret_cast<const uint8_t *>(a.kv.k + (int64_t)hk * a.kv.page * D);
   const uint8_t *vb = reinterpret_cast<const uint8_t *>(a.kv.v + (int64_t)hk * a.kv.page * D);
   const uint32_t lds0 = lds_addr_of(s_kv);
   const int prow_l = lane * 16 / ROWB, phys_l = lane * 16 % ROWB / 16;  // this lane's row and chunk of a piece
-  const int steps = (kend - k0 + KT - 1) / KT, full_steps = (kfull - k0) / KT;  // tiles; those that have all their keys
-  auto page_of = [&](int t, int q) { return s_page[(t * KT + (wave * PIECES + q) * PROWS) >> pl]; };
-  // (without a branch, so that it can stand between products: where the tile is
-  // not to be copied this way, page 0's first rows go to an unused KiB)
-  auto copy_full = [&](bool fast, bool is_v, int t, int q, int pg) {
+  const int steps = (kend - k0 + KT - 1) / KT;         // tiles
+  const int full_steps = any_bad ? 0 : (kend - k0) / KT;  // those that have all their keys
+  auto pages_of = [&](int t, int (&pg)[PIECES]) {
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q) pg[q] = s_page[(t * KT + (wave * PIECES + q) * PROWS) >> pl];
+  };
+  // Without a branch, so that it can stand between products: where `full` is
+  // false, page 0's first rows go to an unused KiB.
+  auto copy_full = [&](bool full, bool is_v, int t, int q, int pg) {
     const int row = (wave * PIECES + q) * PROWS;
     const uint32_t c = 16 * (phys_l ^ (is_v ? swz_v<D>(row + prow_l) : swz_k<D>(row + prow_l)));
     const int64_t off = (int64_t)__builtin_amdgcn_readfirstlane(pg) * (2 * a.kv.page_stride) +
                         ((k0 + t * KT + row) & (a.kv.page - 1)) * ROWB;
     const uint32_t dst = ((is_v ? RING : 0) + t % RING) * TILE + (wave * PIECES + q) * 1024;
-    dma_lds16_s((is_v ? vb : kb) + (fast ? off : 0), prow_l * ROWB + c, lds0 + (fast ? dst : 2 * RING * TILE + PAGES_MAX * 4));
+    dma_lds16_s((is_v ? vb : kb) + (full ? off : 0), prow_l * ROWB + c, lds0 + (full ? dst : 2 * RING * TILE + PAGES_MAX * 4));
   };
+  // A tile with missing keys: rows past the end repeat the last key, rows on a
+  // page outside the cache are zeros, so that what no row sees, NaN perhaps,
+  // does not meet a zero weight in the value product.
   auto copy_any = [&](bool is_v, int t) {
+    int pg[PIECES], key[PIECES];
 #pragma unroll
     for (int q = 0; q < PIECES; ++q) {
-      const int row = (wave * PIECES + q) * PROWS + prow_l, key = k0 + t * KT + row;
+      key[q] = k0 + t * KT + (wave * PIECES + q) * PROWS + prow_l;
+      if (key[q] > kend - 1) key[q] = kend - 1;
+      pg[q] = s_page[(key[q] - k0) >> pl];
+    }
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q) {
+      const int row = (wave * PIECES + q) * PROWS + prow_l;
       const uint32_t c = 16 * (phys_l ^ (is_v ? swz_v<D>(row) : swz_k<D>(row)));
-      const int pg = key < kend ? s_page[(key - k0) >> pl] : -1;
-      const uint8_t *at = (is_v ? vb : kb) + (int64_t)pg * (2 * a.kv.page_stride) + (key & (a.kv.page - 1)) * ROWB;
-      dma_lds16(((unsigned)pg < (unsigned)a.kv.pages ? at : reinterpret_cast<const uint8_t *>(g_zero_row)) + c,
+      const uint8_t *at = (is_v ? vb : kb) + (int64_t)pg[q] * (2 * a.kv.page_stride) + (key[q] & (a.kv.page - 1)) * ROWB;
+      dma_lds16(((unsigned)pg[q] < (unsigned)a.kv.pages ? at : reinterpret_cast<const uint8_t *>(g_zero_row)) + c,
                 lds0 + ((is_v ? RING : 0) + t % RING) * TILE + (wave * PIECES + q) * 1024);
     }
   };
 #pragma unroll
   for (int t = 0; t <= GRP; ++t) {
-    copy_any(false, t);
-    if (t < GRP) copy_any(true, t);
+    if (t < full_steps) {
+      int pg[PIECES];
+      pages_of(t, pg);
+#pragma unroll
+      for (int q = 0; q < PIECES; ++q) {
+        copy_full(true, false, t, q, pg[q]);
+        if (t < GRP) copy_full(true, true, t, q, pg[q]);
+      }
+    } else if (t < steps) {
+      copy_any(false, t);
+      if (t < GRP) copy_any(true, t);
+    }
   }
 
   // this lane's row: query fragments, number of places seen
@@ -228,7 +247,7 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
   // Masks the scores of tile `base` where it needs it and moves the reference m
   // (with O and l) where a row's maximum has outgrown it.
   auto settle = [&](v16f (&S)[SUB], int base) {
-    if (base + KT > kfull || !__all(base + KT <= lim)) {
+    if (any_bad || !__all(base + KT <= lim)) {
       // the keys of the tile that are there: below kend, on a page of the cache
       const int key = base + lane;
       const uint64_t there =
@@ -282,11 +301,13 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
   // (pairs of them; those of 8 keys per half wave, 4 pairs, are due before the
   // first product that takes them) and of the next copies.
   constexpr int PER = KS + 2 * DT, SLOTS = SUB * PER, PAIRS = 8 * SUB, AHEAD = 3;
-  auto step = [&](bool fast, int t0, const v16f (&S)[SUB], v16f (&Sn)[SUB]) {
+  auto step = [&](int t0, const v16f (&S)[SUB], v16f (&Sn)[SUB]) {
     const int ks_slot = (t0 + 1) % RING, v_slot = t0 % RING;
-    int pg[2 * PIECES];  // of the copies, K and V pieces in turn (past the chunk they are not used)
-#pragma unroll
-    for (int x = 0; x < 2 * PIECES; ++x) pg[x] = page_of(fast ? t0 + GRP + 1 - (x & 1) : 0, x >> 1);
+    const int tk = t0 + GRP + 1, tv = t0 + GRP;  // the tiles to copy, where they have all their keys
+    const bool full_k = tk < full_steps, full_v = tv < full_steps;
+    int pgk[PIECES], pgv[PIECES];
+    pages_of(full_k ? tk : 0, pgk);
+    pages_of(full_v ? tv : 0, pgv);
     const float mu = m == -INFINITY ? 0.f : m;
     v8bf pf[2 * SUB], frag[AHEAD + 1];
     auto frag_of = [&](int t) -> v8bf {
@@ -318,34 +339,36 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
         pf[2 * pu + (e >> 3)][(e & 7) + 1] = (__bf16)x1;
       }
 #pragma unroll
-      for (int x = 0; x < 2 * PIECES; ++x)
-        if (t == 2 + x * (SLOTS - 4) / (2 * PIECES)) copy_full(fast, x & 1, t0 + GRP + 1 - (x & 1), x >> 1, pg[x]);
+      for (int q = 0; q < PIECES; ++q) {
+        if (t == 2 + 2 * q * (SLOTS - 4) / (2 * PIECES)) copy_full(full_k, false, tk, q, pgk[q]);
+        if (t == 2 + (2 * q + 1) * (SLOTS - 4) / (2 * PIECES)) copy_full(full_v, true, tv, q, pgv[q]);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
   // GRP (1 or 2) steps between barriers: the tiles that they read have landed
   // before, the copies that they send go to slots that nobody reads any more.
-  bool fast = false;
   auto meet = [&](int t0) {
     wait_vm<0>();
     asm volatile("" ::: "memory");
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
-    fast = t0 + 2 * GRP < full_steps;  // every tile to be copied has all its keys
-    if (!fast) {
-      for (int g = 0; g < GRP; ++g) {
-        copy_any(false, t0 + g + 1 + GRP);
-        copy_any(true, t0 + g + GRP);
+    // the copies that the steps do not send: tiles with missing keys
+    if (t0 + 2 * GRP >= full_steps) {
+      for (int t = t0 + GRP; t <= t0 + 2 * GRP; ++t) {
+        if (t < full_steps || t >= steps) continue;
+        if (t > t0 + GRP) copy_any(false, t);
+        if (t < t0 + 2 * GRP) copy_any(true, t);
       }
     }
   };
   for (int t0 = 0; t0 < steps; t0 += 2) {
     meet(t0);
-    step(fast, t0, S, T);
+    step(t0, S, T);
     if (t0 + 1 == steps) break;
     settle(T, k0 + (t0 + 1) * KT);
     if (GRP == 1) meet(t0 + 1);
-    step(fast, t0 + 1, T, S);
+    step(t0 + 1, T, S);
     if (t0 + 2 < steps) settle(S, k0 + (t0 + 2) * KT);
   }
   wait_vm<0>();  // no copy outlives the workgroup
