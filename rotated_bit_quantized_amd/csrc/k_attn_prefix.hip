@@ -82,8 +82,11 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
   static_assert(PIECES * NW * 1024 == TILE, "every wavefront copies the same share");
   constexpr int RING = 2 * GRP;             // tile t of K and of V is in their slot t % RING
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  uint8_t *s_kv = smem;  // K slots, then V slots
-  int *s_page = reinterpret_cast<int *>(smem + 2 * RING * TILE);
+  constexpr bool DK = NW == 1;              // one wavefront: K fragments straight from memory
+  constexpr int VBASE = DK ? 0 : RING;      // K slots, then V slots
+  constexpr int PAGES_AT = (VBASE + RING) * TILE;
+  uint8_t *s_kv = smem;
+  int *s_page = reinterpret_cast<int *>(smem + PAGES_AT);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r32 = lane & 31, half = lane >> 5;
 
@@ -161,8 +164,8 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
     const uint32_t c = 16 * (phys_l ^ (is_v ? swz_v<D>(row + prow_l) : swz_k<D>(row + prow_l)));
     const int64_t off = (int64_t)__builtin_amdgcn_readfirstlane(pg) * (2 * a.kv.page_stride) +
                         ((k0 + t * KT + row) & (a.kv.page - 1)) * ROWB;
-    const uint32_t dst = ((is_v ? RING : 0) + t % RING) * TILE + (wave * PIECES + q) * 1024;
-    dma_lds16_s((is_v ? vb : kb) + (full ? off : 0), prow_l * ROWB + c, lds0 + (full ? dst : 2 * RING * TILE + PAGES_MAX * 4));
+    const uint32_t dst = ((is_v ? VBASE : 0) + t % RING) * TILE + (wave * PIECES + q) * 1024;
+    dma_lds16_s((is_v ? vb : kb) + (full ? off : 0), prow_l * ROWB + c, lds0 + (full ? dst : PAGES_AT + PAGES_MAX * 4));
   };
   // A tile with missing keys: rows past the end repeat the last key, rows on a
   // page outside the cache are zeros, so that what no row sees, NaN perhaps,
@@ -181,7 +184,7 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
       const uint32_t c = 16 * (phys_l ^ (is_v ? swz_v<D>(row) : swz_k<D>(row)));
       const uint8_t *at = (is_v ? vb : kb) + (int64_t)pg[q] * (2 * a.kv.page_stride) + (key[q] & (a.kv.page - 1)) * ROWB;
       dma_lds16(((unsigned)pg[q] < (unsigned)a.kv.pages ? at : reinterpret_cast<const uint8_t *>(g_zero_row)) + c,
-                lds0 + ((is_v ? RING : 0) + t % RING) * TILE + (wave * PIECES + q) * 1024);
+                lds0 + ((is_v ? VBASE : 0) + t % RING) * TILE + (wave * PIECES + q) * 1024);
     }
   };
 #pragma unroll
@@ -191,13 +194,28 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
       pages_of(t, pg);
 #pragma unroll
       for (int q = 0; q < PIECES; ++q) {
-        copy_full(true, false, t, q, pg[q]);
+        if (!DK) copy_full(true, false, t, q, pg[q]);
         if (t < GRP) copy_full(true, true, t, q, pg[q]);
       }
     } else if (t < steps) {
-      copy_any(false, t);
+      if (!DK) copy_any(false, t);
       if (t < GRP) copy_any(true, t);
     }
+  }
+  // K fragments of a tile in registers (DK): this lane's key row, chunks 2 ks +
+  // half; past the end the last key, on a page outside the cache zeros
+  v8bf kreg[DK ? KS : 1];
+  auto k_row = [&](int t) -> const uint8_t * {
+    int key = k0 + t * KT + r32;
+    if (key > kend - 1) key = kend - 1;
+    const int pg = s_page[(key - k0) >> pl];
+    const uint8_t *at = kb + (int64_t)pg * (2 * a.kv.page_stride) + (key & (a.kv.page - 1)) * ROWB;
+    return ((unsigned)pg < (unsigned)a.kv.pages ? at : reinterpret_cast<const uint8_t *>(g_zero_row)) + 16 * half;
+  };
+  if (DK) {
+    const uint8_t *at = k_row(0);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) kreg[ks] = *reinterpret_cast<const v8bf *>(at + 32 * ks);
   }
 
   // this lane's row: query fragments, number of places seen
@@ -232,7 +250,7 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
       const int row = 16 * kk + 8 * w + 4 * half + ((lane & 15) >> 2);
       const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
       const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)(
-          s_kv + (RING + slot) * TILE + row * ROWB + 16 * (c ^ swz_v<D>(row)) + 8 * (lane & 1)));
+          s_kv + (VBASE + slot) * TILE + row * ROWB + 16 * (c ^ swz_v<D>(row)) + 8 * (lane & 1)));
 #pragma unroll
       for (int e = 0; e < 4; ++e) vf[4 * w + e] = x[e];
     }
@@ -290,7 +308,13 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
   for (int u = 0; u < SUB; ++u) {
     S[u] = (v16f){};
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) S[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k_frag(0, u, ks), qf[ks], S[u], 0, 0, 0);
+    for (int ks = 0; ks < KS; ++ks)
+      S[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(DK ? kreg[ks] : k_frag(0, u, ks), qf[ks], S[u], 0, 0, 0);
+  }
+  if (DK) {
+    const uint8_t *at = k_row(1);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) kreg[ks] = *reinterpret_cast<const v8bf *>(at + 32 * ks);
   }
   settle(S, k0);
 
@@ -306,13 +330,14 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
     const int tk = t0 + GRP + 1, tv = t0 + GRP;  // the tiles to copy, where they have all their keys
     const bool full_k = tk < full_steps, full_v = tv < full_steps;
     int pgk[PIECES], pgv[PIECES];
-    pages_of(full_k ? tk : 0, pgk);
+    if (!DK) pages_of(full_k ? tk : 0, pgk);
     pages_of(full_v ? tv : 0, pgv);
+    const uint8_t *k_next = DK ? k_row(t0 + 2) : nullptr;
     const float mu = m == -INFINITY ? 0.f : m;
     v8bf pf[2 * SUB], frag[AHEAD + 1];
     auto frag_of = [&](int t) -> v8bf {
       const int u = t / PER, w = t % PER;
-      return w < KS ? k_frag(ks_slot, u, w) : v_frag(v_slot, 2 * u + (w - KS) / DT, (w - KS) % DT);
+      return w < KS ? (DK ? kreg[w] : k_frag(ks_slot, u, w)) : v_frag(v_slot, 2 * u + (w - KS) / DT, (w - KS) % DT);
     };
 #pragma unroll
     for (int t = 0; t < AHEAD; ++t) frag[t] = frag_of(t);
@@ -323,6 +348,7 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
       const v8bf f = frag[t % (AHEAD + 1)];
       if (w < KS) {
         Sn[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, qf[w], w == 0 ? (v16f){} : Sn[u], 0, 0, 0);
+        if (DK) kreg[w] = *reinterpret_cast<const v8bf *>(k_next + 32 * w);
       } else {
         const int kk = 2 * u + (w - KS) / DT, d = (w - KS) % DT;
         O[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pf[kk], O[d], 0, 0, 0);
@@ -340,7 +366,7 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
       }
 #pragma unroll
       for (int q = 0; q < PIECES; ++q) {
-        if (t == 2 + 2 * q * (SLOTS - 4) / (2 * PIECES)) copy_full(full_k, false, tk, q, pgk[q]);
+        if (!DK && t == 2 + 2 * q * (SLOTS - 4) / (2 * PIECES)) copy_full(full_k, false, tk, q, pgk[q]);
         if (t == 2 + (2 * q + 1) * (SLOTS - 4) / (2 * PIECES)) copy_full(full_v, true, tv, q, pgv[q]);
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -357,7 +383,7 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
     if (t0 + 2 * GRP >= full_steps) {
       for (int t = t0 + GRP; t <= t0 + 2 * GRP; ++t) {
         if (t < full_steps || t >= steps) continue;
-        if (t > t0 + GRP) copy_any(false, t);
+        if (!DK && t > t0 + GRP) copy_any(false, t);
         if (t < t0 + 2 * GRP) copy_any(true, t);
       }
     }
@@ -506,7 +532,7 @@ Plan plan_for(const AttnArgs &a) {
 
 template <int D, int NW, int KT, int GRP>
 hipError_t launch_part(const AttnArgs &a, const PartPlan &p, float *po, float2 *pm, hipStream_t stream) {
-  constexpr int LDS = 2 * 2 * GRP * KT * 2 * D + PAGES_MAX * 4 + 1024;
+  constexpr int LDS = (NW == 1 ? 1 : 2) * 2 * GRP * KT * 2 * D + PAGES_MAX * 4 + 1024;
   static std::atomic<bool> attr_set[64];
   const hipError_t e = lds_limit_once((const void *)attn_part_kernel<D, NW, KT, GRP>, LDS, attr_set);
   if (e != hipSuccess) return e;
