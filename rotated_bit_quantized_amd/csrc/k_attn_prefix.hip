@@ -33,7 +33,6 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int PAGES_MAX = 512;      // page numbers of one chunk, held in LDS
 constexpr float RESCALE = 8.f;      // log2 growth of a maximum that rescales O
 constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float LN2 = 0.69314718055994530942f;
@@ -41,18 +40,25 @@ constexpr float LN2 = 0.69314718055994530942f;
 // what masked key rows are copied from, so that they cannot put NaN into a product
 __device__ const uint4 g_zero_row[16] = {};
 
-// One launch's share of the work: the prefix (b < 0 side: table shared, rows
-// of all sequences) or the suffixes (one sequence per item).
+// The prefix's or the suffixes' share of the work.
 struct PartPlan {
-  int suffix;     // 0 prefix, 1 suffixes
+  int suffix;     // 0 prefix (one table, rows of all sequences), 1 suffixes (one sequence per item)
+  int wide;       // 1: a workgroup of 8 wavefronts per item, 0: one wavefront
   int tiles;      // row tiles per key head (prefix) or per sequence and key head (suffix)
   int splits;     // chunks of the keys
-  int chunk;      // keys per chunk: a multiple of KT and of the page (suffixes: the least)
-  int part0;      // number of this launch's first part
+  int chunk;      // keys per chunk: a multiple of the key tile and of the page (suffixes: the least)
+  int part0;      // number of the first part
   int rows;       // B n_q G, rows of one key head
-  int64_t items;  // workgroups
-  float c;        // log2(e) |scale|, or 1 where scale == 0
-  uint32_t qand, qxor;  // on the bits of q pairs: sign of the scale, or zero
+  int swizzle;    // give each XCD a run of items
+  int64_t items;
+};
+
+// One launch: the workgroups of wide items, then those of one-wavefront items.
+struct Launch {
+  PartPlan part[2];
+  int wide_items, narrow_items, waves;  // waves: wavefronts of a workgroup
+  float c;                              // log2(e) |scale|, or 1 where scale == 0
+  uint32_t qand, qxor;                  // on the bits of q pairs: sign of the scale, or zero
 };
 
 template <int D>
@@ -71,29 +77,47 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt(0x0F70 | (C & 0xF) | ((C >> 4) << 14));
 }
 
-template <int D, int NW, int KT, int GRP>
-__global__ void __launch_bounds__(64 * NW, 2)
-attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o, float2 *__restrict__ part_ml) {
+// LDS of an item: K (wide items) and V slots, page numbers, an unused KiB
+template <int D, int NW>
+struct Part {
+  static constexpr int KT = NW == 1 ? 32 : 64;      // keys of a tile
+  static constexpr int GRP = NW == 1 ? 1 : 2;       // steps between barriers
+  static constexpr int RING = 2 * GRP;              // tile t of K and of V is in their slot t % RING
+  static constexpr int TILE = KT * 2 * D;           // bytes of a K or V tile
+  static constexpr int VBASE = NW == 1 ? 0 : RING;  // K slots, then V slots; one wavefront has K in registers
+  static constexpr int PAGES_AT = (VBASE + RING) * TILE, PAGES_MAX = NW == 1 ? 256 : 512;
+  static constexpr int SPARE_AT = PAGES_AT + 4 * PAGES_MAX, LDS = SPARE_AT + 1024;
+};
+
+template <int D, int NW>
+__device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, const PartPlan &p, int item, uint8_t *smem,
+                                          float *__restrict__ part_o, float2 *__restrict__ part_ml) {
+  using P = Part<D, NW>;
+  constexpr int KT = P::KT, GRP = P::GRP, RING = P::RING, TILE = P::TILE;
   constexpr int KS = D / 16, DT = D / 32, SUB = KT / 32;
   constexpr int ROWB = 2 * D;               // bytes of a key row
-  constexpr int TILE = KT * ROWB;           // bytes of a K or V tile
   constexpr int PIECES = TILE / 1024 / NW;  // 1 KiB copies per wavefront and K or V tile
   constexpr int PROWS = 1024 / ROWB;        // key rows of one: 4 or 8, on one page
+  constexpr bool DK = NW == 1;              // K fragments straight from memory
   static_assert(PIECES * NW * 1024 == TILE, "every wavefront copies the same share");
-  constexpr int RING = 2 * GRP;             // tile t of K and of V is in their slot t % RING
-  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  constexpr bool DK = NW == 1;              // one wavefront: K fragments straight from memory
-  constexpr int VBASE = DK ? 0 : RING;      // K slots, then V slots
-  constexpr int PAGES_AT = (VBASE + RING) * TILE;
   uint8_t *s_kv = smem;
-  int *s_page = reinterpret_cast<int *>(smem + PAGES_AT);
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int *s_page = reinterpret_cast<int *>(smem + P::PAGES_AT);
+  const int lane = threadIdx.x & 63, wave = NW == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r32 = lane & 31, half = lane >> 5;
+  // the item's wavefronts meet; what they wrote to LDS is visible
+  auto meet_lds = [&]() {
+    if (NW > 1) {
+      __syncthreads();
+    } else {
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+      __builtin_amdgcn_wave_barrier();
+    }
+    asm volatile("" ::: "memory");
+  };
 
   // Consecutive workgroups go to the 8 XCDs in turn; items that read the same
   // keys (the row tiles of one chunk) are consecutive, so give each XCD a run.
-  int item = blockIdx.x;
-  if (p.items % 8 == 0) item = (item & 7) * (int)(p.items >> 3) + (item >> 3);
+  if (p.swizzle) item = (item & 7) * (int)(p.items >> 3) + (item >> 3);
   const int tile = item % p.tiles;
   item /= p.tiles;
   const int split = item % p.splits;
@@ -121,8 +145,8 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
     n = see < 0 ? 0 : see < cap ? (int)see : cap;
     // the splits share what this sequence has, not what its table could hold
     const int unit = a.kv.page > KT ? a.kv.page : KT;
-    const int even = ((n + p.splits - 1) / p.splits + unit - 1) / unit * unit;
-    if (even > chunk) chunk = even;
+    const int64_t even = (((int64_t)n + p.splits - 1) / p.splits + unit - 1) / unit * unit;
+    if (even > chunk) chunk = (int)even;
   }
   const int64_t k0l = (int64_t)split * chunk;
   const int k0 = k0l < n ? (int)k0l : n;
@@ -137,12 +161,15 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
   const int pl = __builtin_ctz((unsigned)a.kv.page);
   const int npages = ((kend - 1) >> pl) - (k0 >> pl) + 1;
   int bad = 0;
-  for (int i = threadIdx.x; i < npages; i += 64 * NW) {
+  for (int i = NW == 1 ? lane : threadIdx.x; i < npages; i += 64 * NW) {
     const int pg = table[(k0 >> pl) + i];
     s_page[i] = pg;
     bad |= (unsigned)pg >= (unsigned)a.kv.pages;
   }
-  const bool any_bad = __syncthreads_or(bad);
+  bool any_bad;
+  if (NW > 1) any_bad = __syncthreads_or(bad);
+  else any_bad = __any(bad);
+  meet_lds();
   // Copies of tile t, this wavefront's pieces, K or V.  A piece is PROWS key
   // rows of one page, so its source is a scalar base and a fixed offset per
   // lane; the 16-byte chunks of a row are permuted by the row, on the source
@@ -164,8 +191,8 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
     const uint32_t c = 16 * (phys_l ^ (is_v ? swz_v<D>(row + prow_l) : swz_k<D>(row + prow_l)));
     const int64_t off = (int64_t)__builtin_amdgcn_readfirstlane(pg) * (2 * a.kv.page_stride) +
                         ((k0 + t * KT + row) & (a.kv.page - 1)) * ROWB;
-    const uint32_t dst = ((is_v ? VBASE : 0) + t % RING) * TILE + (wave * PIECES + q) * 1024;
-    dma_lds16_s((is_v ? vb : kb) + (full ? off : 0), prow_l * ROWB + c, lds0 + (full ? dst : PAGES_AT + PAGES_MAX * 4));
+    const uint32_t dst = ((is_v ? P::VBASE : 0) + t % RING) * TILE + (wave * PIECES + q) * 1024;
+    dma_lds16_s((is_v ? vb : kb) + (full ? off : 0), prow_l * ROWB + c, lds0 + (full ? dst : P::SPARE_AT));
   };
   // A tile with missing keys: rows past the end repeat the last key, rows on a
   // page outside the cache are zeros, so that what no row sees, NaN perhaps,
@@ -184,7 +211,7 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
       const uint32_t c = 16 * (phys_l ^ (is_v ? swz_v<D>(row) : swz_k<D>(row)));
       const uint8_t *at = (is_v ? vb : kb) + (int64_t)pg[q] * (2 * a.kv.page_stride) + (key[q] & (a.kv.page - 1)) * ROWB;
       dma_lds16(((unsigned)pg[q] < (unsigned)a.kv.pages ? at : reinterpret_cast<const uint8_t *>(g_zero_row)) + c,
-                lds0 + ((is_v ? VBASE : 0) + t % RING) * TILE + (wave * PIECES + q) * 1024);
+                lds0 + ((is_v ? P::VBASE : 0) + t % RING) * TILE + (wave * PIECES + q) * 1024);
     }
   };
 #pragma unroll
@@ -232,7 +259,7 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
     for (int ks = 0; ks < KS; ++ks) {
       u32x4 v = *reinterpret_cast<const u32x4 *>(src + 16 * ks);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = (v[e] & p.qand) ^ p.qxor;
+      for (int e = 0; e < 4; ++e) v[e] = (v[e] & lp.qand) ^ lp.qxor;
       qf[ks] = __builtin_bit_cast(v8bf, v);
     }
   }
@@ -250,7 +277,7 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
       const int row = 16 * kk + 8 * w + 4 * half + ((lane & 15) >> 2);
       const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
       const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)(
-          s_kv + (VBASE + slot) * TILE + row * ROWB + 16 * (c ^ swz_v<D>(row)) + 8 * (lane & 1)));
+          s_kv + (P::VBASE + slot) * TILE + row * ROWB + 16 * (c ^ swz_v<D>(row)) + 8 * (lane & 1)));
 #pragma unroll
       for (int e = 0; e < 4; ++e) vf[4 * w + e] = x[e];
     }
@@ -285,7 +312,7 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
     for (int u = 0; u < SUB; ++u)
 #pragma unroll
       for (int e = 0; e < 16; ++e) mx = __builtin_elementwise_maximum(mx, S[u][e]);
-    mx = fmaxf(mx, xhalf(mx)) * p.c;
+    mx = fmaxf(mx, xhalf(mx)) * lp.c;
     if (__any(mx > m + RESCALE)) {
       const float mn = fmaxf(m, mx);
       const float al = mn == -INFINITY ? 1.f : exp2f(m - mn);
@@ -302,7 +329,7 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
   // scores of the first tile
   wait_vm<0>();
   asm volatile("" ::: "memory");
-  __syncthreads();
+  meet_lds();
   v16f S[SUB], T[SUB];  // scores of two tiles in turn
 #pragma unroll
   for (int u = 0; u < SUB; ++u) {
@@ -357,8 +384,8 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
 #pragma unroll
       for (int pr = t * RATE / 3 + (t > 0); pr < (t + 1) * RATE / 3 + 1 && pr < PAIRS; ++pr) {
         const int pu = pr / 8, e = 2 * (pr % 8);
-        const float x0 = __builtin_amdgcn_exp2f(__builtin_fmaf(S[pu][e], p.c, -mu));
-        const float x1 = __builtin_amdgcn_exp2f(__builtin_fmaf(S[pu][e + 1], p.c, -mu));
+        const float x0 = __builtin_amdgcn_exp2f(__builtin_fmaf(S[pu][e], lp.c, -mu));
+        const float x1 = __builtin_amdgcn_exp2f(__builtin_fmaf(S[pu][e + 1], lp.c, -mu));
         l[0] += x0;
         l[1] += x1;
         pf[2 * pu + (e >> 3)][e & 7] = (__bf16)x0;
@@ -377,7 +404,7 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
   auto meet = [&](int t0) {
     wait_vm<0>();
     asm volatile("" ::: "memory");
-    __syncthreads();
+    meet_lds();
     __builtin_amdgcn_sched_barrier(0);
     // the copies that the steps do not send: tiles with missing keys
     if (t0 + 2 * GRP >= full_steps) {
@@ -397,7 +424,7 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
     step(t0 + 1, T, S);
     if (t0 + 2 < steps) settle(S, k0 + (t0 + 2) * KT);
   }
-  wait_vm<0>();  // no copy outlives the workgroup
+  wait_vm<0>();  // no copy outlives the item
 
   const int r = r0 + r32;
   const float ls = l[0] + l[1], lt = ls + xhalf(ls);
@@ -410,6 +437,24 @@ attn_part_kernel(const AttnArgs a, const PartPlan p, float *__restrict__ part_o,
     for (int e = 0; e < 4; ++e)
       *reinterpret_cast<float4 *>(dst + 32 * d + 8 * e) =
           make_float4(O[d][4 * e], O[d][4 * e + 1], O[d][4 * e + 2], O[d][4 * e + 3]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(512, 2)
+attn_part_kernel(const AttnArgs a, const Launch lp, float *__restrict__ part_o, float2 *__restrict__ part_ml) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  if ((int)blockIdx.x < lp.wide_items) {
+    const int first = lp.part[0].wide ? (int)lp.part[0].items : 0;
+    const int w = (int)blockIdx.x >= first;
+    part_body<D, 8>(a, lp, lp.part[w], w ? blockIdx.x - first : blockIdx.x, smem, part_o, part_ml);
+  } else {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int item = ((int)blockIdx.x - lp.wide_items) * lp.waves + wave;
+    if (item >= lp.narrow_items) return;
+    const int first = lp.part[0].wide ? 0 : (int)lp.part[0].items;
+    const int w = item >= first;
+    part_body<D, 1>(a, lp, lp.part[w], w ? item - first : item, smem + wave * Part<D, 1>::LDS, part_o, part_ml);
+  }
 }
 
 // The join, one wavefront per row: lanes hold the parts' statistics, 64 parts
@@ -442,7 +487,7 @@ attn_join_kernel(const AttnArgs a, int rows, int parts, const float *__restrict_
     l = l * al + ls;
     o.x *= al, o.y *= al, o.z *= al, o.w *= al;
     const int np = parts - s0 < 64 ? parts - s0 : 64;
-#pragma unroll 4
+#pragma unroll 8
     for (int s = 0; s < np; s += AT) {
       const float ws = __shfl(w, s + sub);
       if (ws == 0.f) continue;  // parts past the end have weight zero
@@ -472,55 +517,42 @@ attn_join_kernel(const AttnArgs a, int rows, int parts, const float *__restrict_
   if (a.lse && lane == 0) a.lse[(int64_t)tok * a.heads_q + h] = m == -INFINITY ? -INFINITY : LN2 * (m + log2f(l));
 }
 
-// Row tile shape: wavefronts and 32-row blocks per wavefront.
-struct Shape {
-  int nw, kt;
-  int rows() const { return 32 * nw; }
-};
-
-Shape shape_for(int rows) {
-  if (rows <= 32) return {1, 32};
-  if (rows <= 64) return {2, 64};
-  if (rows <= 128) return {4, 64};
-  return {8, 64};
-}
-
 struct Plan {
-  PartPlan part[2];
-  Shape shape[2];
-  int parts;
+  Launch launch;
+  int rows, parts;
   int64_t rows_all;
 };
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 Plan plan_for(const AttnArgs &a) {
-  Plan p;
+  Plan p{};
   const int G = a.heads_q / a.kv.heads;
-  const int rows = a.B * a.n_q * G;
-  p.rows_all = (int64_t)rows * a.kv.heads;
-  p.parts = 0;
+  p.rows = a.B * a.n_q * G;
+  p.rows_all = (int64_t)p.rows * a.kv.heads;
   for (int s = 0; s < 2; ++s) {
-    PartPlan &q = p.part[s];
+    PartPlan &q = p.launch.part[s];
     const int64_t keys = a.kv.pages == 0 ? 0 : s ? (int64_t)a.table_ld * a.kv.page : a.prefix_len;
-    const int group_rows = s ? a.n_q * G : rows;
-    const Shape sh = p.shape[s] = shape_for(group_rows);
+    const int group_rows = s ? a.n_q * G : p.rows;
     q.suffix = s;
-    q.rows = rows;
+    q.rows = p.rows;
     q.part0 = p.parts;
-    q.tiles = (group_rows + sh.rows() - 1) / sh.rows();
-    q.splits = 0;
-    q.items = 0;
-    q.chunk = 0;
+    // Up to 128 rows every wavefront takes 32 of them by itself, eight to a CU
+    // where there are enough; above, they share the keys through LDS.
+    q.wide = group_rows > 128;
+    const int tile_rows = q.wide ? 256 : 32;
+    q.tiles = (group_rows + tile_rows - 1) / tile_rows;
     if (keys == 0) continue;
-    const int64_t unit = a.kv.page > sh.kt ? a.kv.page : sh.kt;
     const int64_t groups = (int64_t)q.tiles * a.kv.heads * (s ? a.B : 1);
-    // enough workgroups for every CU: 1 of 4 wavefronts with 64 rows each, 8 single ones
-    const int64_t want = (int64_t)device_cus() * (8 / sh.nw);
+    // chunks that give every CU a workgroup, or eight single wavefronts, but
+    // of no fewer than 64 keys (a part costs more than reading them)
+    const int64_t unit = a.kv.page > 64 ? a.kv.page : 64;
+    const int64_t want = (int64_t)device_cus() * (q.wide ? 1 : 8);
     int64_t splits = want / groups;
     if (splits < 1) splits = 1;
     int64_t chunk = round_up((keys + splits - 1) / splits, unit);
-    const int64_t most = (int64_t)(PAGES_MAX - 1) * a.kv.page / unit * unit;
+    const int64_t pages = q.wide ? Part<64, 8>::PAGES_MAX : Part<64, 1>::PAGES_MAX;
+    const int64_t most = (pages - 1) * a.kv.page / unit * unit;
     if (chunk > most) chunk = most;
     q.splits = (int)((keys + chunk - 1) / chunk);
     q.chunk = (int)(s ? unit : chunk);
@@ -530,30 +562,30 @@ Plan plan_for(const AttnArgs &a) {
   return p;
 }
 
-template <int D, int NW, int KT, int GRP>
-hipError_t launch_part(const AttnArgs &a, const PartPlan &p, float *po, float2 *pm, hipStream_t stream) {
-  constexpr int LDS = (NW == 1 ? 1 : 2) * 2 * GRP * KT * 2 * D + PAGES_MAX * 4 + 1024;
-  static std::atomic<bool> attr_set[64];
-  const hipError_t e = lds_limit_once((const void *)attn_part_kernel<D, NW, KT, GRP>, LDS, attr_set);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attn_part_kernel<D, NW, KT, GRP>), dim3((unsigned)p.items), dim3(64 * NW), LDS, stream, a, p, po, pm);
-  return hipGetLastError();
-}
-
 template <int D>
-hipError_t launch_d(const AttnArgs &a, const Plan &p, float *po, float2 *pm, hipStream_t stream) {
-  for (int s = 0; s < 2; ++s) {
-    if (!p.part[s].items) continue;
-    if (p.part[s].items > 0x7fffffff) return hipErrorInvalidConfiguration;
-    const Shape sh = p.shape[s];
-    const hipError_t e = sh.nw == 1   ? launch_part<D, 1, 32, 1>(a, p.part[s], po, pm, stream)
-                         : sh.nw == 2 ? launch_part<D, 2, 64, 1>(a, p.part[s], po, pm, stream)
-                         : sh.nw == 4 ? launch_part<D, 4, 64, 1>(a, p.part[s], po, pm, stream)
-                                      : launch_part<D, 8, 64, 2>(a, p.part[s], po, pm, stream);
+hipError_t launch_d(const AttnArgs &a, Plan &p, float *po, float2 *pm, hipStream_t stream) {
+  Launch &lp = p.launch;
+  int64_t wide = 0, narrow = 0;
+  for (PartPlan &q : lp.part) (q.wide ? wide : narrow) += q.items;
+  if (wide + narrow > 0x7fffffff || (p.rows_all + 3) / 4 > 0x7fffffff) return hipErrorInvalidConfiguration;
+  lp.wide_items = (int)wide;
+  lp.narrow_items = (int)narrow;
+  lp.waves = wide ? 8 : 1;
+  for (PartPlan &q : lp.part) q.swizzle = q.items % 8 == 0 && (q.wide || lp.waves == 1);
+  if (wide + narrow > 0) {
+    constexpr int WIDE = Part<D, 8>::LDS, ONE = Part<D, 1>::LDS, MOST = WIDE > 8 * ONE ? WIDE : 8 * ONE;
+    static_assert(MOST <= 160 * 1024, "LDS");
+    static std::atomic<bool> attr_set[64];
+    const hipError_t e = lds_limit_once((const void *)attn_part_kernel<D>, MOST, attr_set);
     if (e != hipSuccess) return e;
+    const int lds = wide ? (narrow ? MOST : WIDE) : ONE;
+    const int64_t blocks = wide + (narrow + lp.waves - 1) / lp.waves;
+    hipLaunchKernelGGL(attn_part_kernel<D>, dim3((unsigned)blocks), dim3(64 * lp.waves), lds, stream, a, lp, po, pm);
+    const hipError_t r = hipGetLastError();
+    if (r != hipSuccess) return r;
   }
-  hipLaunchKernelGGL((attn_join_kernel<D>), dim3((unsigned)((p.rows_all + 3) / 4)), dim3(256), 0, stream, a,
-                     p.part[0].rows, p.parts, po, pm);
+  hipLaunchKernelGGL((attn_join_kernel<D>), dim3((unsigned)((p.rows_all + 3) / 4)), dim3(256), 0, stream, a, p.rows, p.parts,
+                     po, pm);
   return hipGetLastError();
 }
 
@@ -566,11 +598,9 @@ size_t attn_prefix_ws(const AttnArgs &a) {
 
 hipError_t launch_attn_prefix(const AttnArgs &a, void *ws, hipStream_t stream) {
   Plan p = plan_for(a);
-  for (PartPlan &q : p.part) {
-    q.c = a.scale == 0.f ? 1.f : __builtin_fabsf(a.scale) * LOG2E;
-    q.qand = a.scale == 0.f ? 0u : 0xffffffffu;
-    q.qxor = a.scale < 0.f ? 0x80008000u : 0u;
-  }
+  p.launch.c = a.scale == 0.f ? 1.f : __builtin_fabsf(a.scale) * LOG2E;
+  p.launch.qand = a.scale == 0.f ? 0u : 0xffffffffu;
+  p.launch.qxor = a.scale < 0.f ? 0x80008000u : 0u;
   float *po = static_cast<float *>(ws);
   float2 *pm = reinterpret_cast<float2 *>(po + (size_t)p.parts * p.rows_all * a.kv.d);
   return a.kv.d == 64 ? launch_d<64>(a, p, po, pm, stream) : launch_d<128>(a, p, po, pm, stream);
