@@ -77,7 +77,7 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt(0x0F70 | (C & 0xF) | ((C >> 4) << 14));
 }
 
-// LDS of an item: K (wide items) and V slots, page numbers, an unused KiB
+// LDS of an item: K (wide items) and V slots, page numbers
 template <int D, int NW>
 struct Part {
   static constexpr int KT = NW == 1 ? 32 : 64;      // keys of a tile
@@ -86,12 +86,12 @@ struct Part {
   static constexpr int TILE = KT * 2 * D;           // bytes of a K or V tile
   static constexpr int VBASE = NW == 1 ? 0 : RING;  // K slots, then V slots; one wavefront has K in registers
   static constexpr int PAGES_AT = (VBASE + RING) * TILE, PAGES_MAX = NW == 1 ? 256 : 512;
-  static constexpr int SPARE_AT = PAGES_AT + 4 * PAGES_MAX, LDS = SPARE_AT + 1024;
+  static constexpr int LDS = PAGES_AT + 4 * PAGES_MAX;
 };
 
 template <int D, int NW>
 __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, const PartPlan &p, int item, uint8_t *smem,
-                                          float *__restrict__ part_o, float2 *__restrict__ part_ml) {
+                                          uint32_t spare, float *__restrict__ part_o, float2 *__restrict__ part_ml) {
   using P = Part<D, NW>;
   constexpr int KT = P::KT, GRP = P::GRP, RING = P::RING, TILE = P::TILE;
   constexpr int KS = D / 16, DT = D / 32, SUB = KT / 32;
@@ -192,7 +192,7 @@ __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, c
     const int64_t off = (int64_t)__builtin_amdgcn_readfirstlane(pg) * (2 * a.kv.page_stride) +
                         ((k0 + t * KT + row) & (a.kv.page - 1)) * ROWB;
     const uint32_t dst = ((is_v ? P::VBASE : 0) + t % RING) * TILE + (wave * PIECES + q) * 1024;
-    dma_lds16_s((is_v ? vb : kb) + (full ? off : 0), prow_l * ROWB + c, lds0 + (full ? dst : P::SPARE_AT));
+    dma_lds16_s((is_v ? vb : kb) + (full ? off : 0), prow_l * ROWB + c, full ? lds0 + dst : spare);
   };
   // A tile with missing keys: rows past the end repeat the last key, rows on a
   // page outside the cache are zeros, so that what no row sees, NaN perhaps,
@@ -443,17 +443,19 @@ template <int D>
 __global__ void __launch_bounds__(512, 2)
 attn_part_kernel(const AttnArgs a, const Launch lp, float *__restrict__ part_o, float2 *__restrict__ part_ml) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  const uint32_t spare = lds_addr_of(smem);  // a KiB that nobody reads
+  uint8_t *mine = smem + 1024;
   if ((int)blockIdx.x < lp.wide_items) {
     const int first = lp.part[0].wide ? (int)lp.part[0].items : 0;
     const int w = (int)blockIdx.x >= first;
-    part_body<D, 8>(a, lp, lp.part[w], w ? blockIdx.x - first : blockIdx.x, smem, part_o, part_ml);
+    part_body<D, 8>(a, lp, lp.part[w], w ? blockIdx.x - first : blockIdx.x, mine, spare, part_o, part_ml);
   } else {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int item = ((int)blockIdx.x - lp.wide_items) * lp.waves + wave;
     if (item >= lp.narrow_items) return;
     const int first = lp.part[0].wide ? 0 : (int)lp.part[0].items;
     const int w = item >= first;
-    part_body<D, 1>(a, lp, lp.part[w], w ? item - first : item, smem + wave * Part<D, 1>::LDS, part_o, part_ml);
+    part_body<D, 1>(a, lp, lp.part[w], w ? item - first : item, mine + wave * Part<D, 1>::LDS, spare, part_o, part_ml);
   }
 }
 
@@ -530,35 +532,61 @@ Plan plan_for(const AttnArgs &a) {
   const int G = a.heads_q / a.kv.heads;
   p.rows = a.B * a.n_q * G;
   p.rows_all = (int64_t)p.rows * a.kv.heads;
+  const int64_t cus = device_cus();
+  int64_t keys[2], groups[2];
+  double work[2];
   for (int s = 0; s < 2; ++s) {
     PartPlan &q = p.launch.part[s];
-    const int64_t keys = a.kv.pages == 0 ? 0 : s ? (int64_t)a.table_ld * a.kv.page : a.prefix_len;
+    keys[s] = a.kv.pages == 0 ? 0 : s ? (int64_t)a.table_ld * a.kv.page : a.prefix_len;
     const int group_rows = s ? a.n_q * G : p.rows;
     q.suffix = s;
     q.rows = p.rows;
-    q.part0 = p.parts;
     // Up to 128 rows every wavefront takes 32 of them by itself, eight to a CU
     // where there are enough; above, they share the keys through LDS.
     q.wide = group_rows > 128;
-    const int tile_rows = q.wide ? 256 : 32;
-    q.tiles = (group_rows + tile_rows - 1) / tile_rows;
-    if (keys == 0) continue;
-    const int64_t groups = (int64_t)q.tiles * a.kv.heads * (s ? a.B : 1);
-    // chunks that give every CU a workgroup, or eight single wavefronts, but
-    // of no fewer than 64 keys (a part costs more than reading them)
-    const int64_t unit = a.kv.page > 64 ? a.kv.page : 64;
-    const int64_t want = (int64_t)device_cus() * (q.wide ? 1 : 8);
-    int64_t splits = want / groups;
+    q.tiles = (group_rows + (q.wide ? 255 : 31)) / (q.wide ? 256 : 32);
+    groups[s] = (int64_t)q.tiles * a.kv.heads * (s ? a.B : 1);
+    // CU microseconds, as measured: 2.0 (d 128) or 1.1 (d 64) for 64 keys of a
+    // wide item, 4 and 1.9 or 1.2 per 32 keys for eight single wavefronts (used
+    // to share the CUs below); suffixes are taken to fill half of their tables
+    const double k = s ? 0.5 * (double)keys[s] : (double)keys[s];
+    work[s] = keys[s] == 0 ? 0
+              : q.wide     ? (double)groups[s] * k / 64 * (a.kv.d == 128 ? 2.0 : 1.1)
+                           : (double)groups[s] / 8 * (4 + k / 32 * (a.kv.d == 128 ? 1.9 : 1.2));
+  }
+  // Chunks that give every CU a workgroup, or eight single wavefronts.  Where
+  // there are both kinds and the single ones would be a mostly empty second
+  // round, wide items leave them their share of the CUs (24 sequences of 4
+  // tokens over 5000 + 333 keys: 21.2 us one kind after the other, 16.3 side by
+  // side); a full round of them comes after the wide ones (256 sequences over
+  // 32768 + 512: 224 us, 231 side by side).
+  const int w = p.launch.part[0].wide ? 0 : 1;
+  int64_t cus_for[2] = {cus, cus};
+  const bool mixed = p.launch.part[0].wide != p.launch.part[1].wide && keys[0] > 0 && keys[1] > 0 &&
+                     groups[1 - w] / 8 < cus / 2;
+  if (mixed) {
+    const double share = work[w] / (work[0] + work[1]);
+    cus_for[w] = (int64_t)((double)cus * (share < 0.75 ? 0.75 : share));
+  }
+  for (int i = 0; i < 2; ++i) {
+    const int s = i ? 1 - w : w;  // wide items first
+    PartPlan &q = p.launch.part[s];
+    if (keys[s] == 0) continue;
+    const int64_t unit = a.kv.page > 64 ? a.kv.page : 64;  // a part of fewer keys costs more than reading them
+    int64_t splits = (cus_for[s] * (q.wide ? 1 : 8) + (mixed ? groups[s] / 2 : 0)) / groups[s];
+    if (q.wide && splits > 1 && splits * groups[s] > cus) --splits;
     if (splits < 1) splits = 1;
-    int64_t chunk = round_up((keys + splits - 1) / splits, unit);
+    int64_t chunk = round_up((keys[s] + splits - 1) / splits, unit);
     const int64_t pages = q.wide ? Part<64, 8>::PAGES_MAX : Part<64, 1>::PAGES_MAX;
     const int64_t most = (pages - 1) * a.kv.page / unit * unit;
     if (chunk > most) chunk = most;
-    q.splits = (int)((keys + chunk - 1) / chunk);
+    q.splits = (int)((keys[s] + chunk - 1) / chunk);
     q.chunk = (int)(s ? unit : chunk);
-    q.items = groups * q.splits;
-    p.parts += q.splits;
+    q.items = groups[s] * q.splits;
+    if (mixed && q.wide && q.items < cus) cus_for[1 - s] = cus - q.items;
   }
+  p.launch.part[1].part0 = p.launch.part[0].splits;
+  p.parts = p.launch.part[0].splits + p.launch.part[1].splits;
   return p;
 }
 
@@ -573,12 +601,12 @@ hipError_t launch_d(const AttnArgs &a, Plan &p, float *po, float2 *pm, hipStream
   lp.waves = wide ? 8 : 1;
   for (PartPlan &q : lp.part) q.swizzle = q.items % 8 == 0 && (q.wide || lp.waves == 1);
   if (wide + narrow > 0) {
-    constexpr int WIDE = Part<D, 8>::LDS, ONE = Part<D, 1>::LDS, MOST = WIDE > 8 * ONE ? WIDE : 8 * ONE;
+    constexpr int WIDE = Part<D, 8>::LDS, ONE = Part<D, 1>::LDS, MOST = (WIDE > 8 * ONE ? WIDE : 8 * ONE) + 1024;
     static_assert(MOST <= 160 * 1024, "LDS");
     static std::atomic<bool> attr_set[64];
     const hipError_t e = lds_limit_once((const void *)attn_part_kernel<D>, MOST, attr_set);
     if (e != hipSuccess) return e;
-    const int lds = wide ? (narrow ? MOST : WIDE) : ONE;
+    const int lds = wide ? MOST : ONE + 1024;
     const int64_t blocks = wide + (narrow + lp.waves - 1) / lp.waves;
     hipLaunchKernelGGL(attn_part_kernel<D>, dim3((unsigned)blocks), dim3(64 * lp.waves), lds, stream, a, lp, po, pm);
     const hipError_t r = hipGetLastError();
