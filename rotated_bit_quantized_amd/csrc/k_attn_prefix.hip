@@ -22,6 +22,8 @@
 // is not.  O is rescaled only when a row's maximum has grown by more than
 // 2^8 since the last time (P then stays below 2^8, which costs float32 and
 // bfloat16 no precision).
+#include <type_traits>
+
 #include "oq_internal.h"
 
 namespace oq {
@@ -265,19 +267,27 @@ __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, c
   }
 
   // fragment addresses: K row r32 of a 32-key block, chunk 2 ks + half; V keys
-  // 16 kk + 8 w + 4 half + .. and d 32 dt + ..
+  // 16 kk + 8 w + 4 half + .. and d 32 dt + ..: a lane part that does not
+  // change and a constant
+  const uint8_t *k_at[DK ? 1 : KS], *v_at[DT];
+  if (!DK) {
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) k_at[ks] = s_kv + r32 * ROWB + 16 * ((2 * ks + half) ^ swz_k<D>(r32));
+  }
+#pragma unroll
+  for (int d = 0; d < DT; ++d) {
+    const int row = 4 * half + ((lane & 15) >> 2), c = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    v_at[d] = s_kv + P::VBASE * TILE + row * ROWB + 16 * (c ^ swz_v<D>(row)) + 8 * (lane & 1);
+  }
   auto k_frag = [&](int slot, int u, int ks) -> v8bf {
-    const int row = 32 * u + r32;
-    return *reinterpret_cast<const v8bf *>(s_kv + slot * TILE + row * ROWB + 16 * ((2 * ks + half) ^ swz_k<D>(row)));
+    return *reinterpret_cast<const v8bf *>(k_at[ks] + slot * TILE + 32 * u * ROWB);
   };
   auto v_frag = [&](int slot, int kk, int d) -> v8bf {
     v8s vf;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      const int row = 16 * kk + 8 * w + 4 * half + ((lane & 15) >> 2);
-      const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-      const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)(
-          s_kv + (P::VBASE + slot) * TILE + row * ROWB + 16 * (c ^ swz_v<D>(row)) + 8 * (lane & 1)));
+      const v4s x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (__attribute__((address_space(3))) v4s *)(v_at[d] + slot * TILE + (16 * kk + 8 * w) * ROWB));
 #pragma unroll
       for (int e = 0; e < 4; ++e) vf[4 * w + e] = x[e];
     }
@@ -307,11 +317,13 @@ __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, c
         for (int e = 0; e < 16; ++e) S[u][e] = (bits >> (8 * (e >> 2) + (e & 3))) & 1u ? S[u][e] : -INFINITY;
       }
     }
-    float mx = S[0][0];
+    float mq[4] = {S[0][0], S[0][1], S[0][2], S[0][3]};  // four chains
 #pragma unroll
     for (int u = 0; u < SUB; ++u)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) mx = __builtin_elementwise_maximum(mx, S[u][e]);
+      for (int e = u ? 0 : 4; e < 16; ++e) mq[e & 3] = __builtin_elementwise_maximum(mq[e & 3], S[u][e]);
+    float mx = __builtin_elementwise_maximum(__builtin_elementwise_maximum(mq[0], mq[1]),
+                                             __builtin_elementwise_maximum(mq[2], mq[3]));
     mx = fmaxf(mx, xhalf(mx)) * lp.c;
     if (__any(mx > m + RESCALE)) {
       const float mn = fmaxf(m, mx);
@@ -352,8 +364,8 @@ __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, c
   // (pairs of them; those of 8 keys per half wave, 4 pairs, are due before the
   // first product that takes them) and of the next copies.
   constexpr int PER = KS + 2 * DT, SLOTS = SUB * PER, PAIRS = 8 * SUB, AHEAD = 3;
-  auto step = [&](int t0, const v16f (&S)[SUB], v16f (&Sn)[SUB]) {
-    const int ks_slot = (t0 + 1) % RING, v_slot = t0 % RING;
+  auto step = [&](auto slot, int t0, const v16f (&S)[SUB], v16f (&Sn)[SUB]) {
+    constexpr int v_slot = slot, ks_slot = (v_slot + 1) % RING;  // t0 % RING
     const int tk = t0 + GRP + 1, tv = t0 + GRP;  // the tiles to copy, where they have all their keys
     const bool full_k = tk < full_steps, full_v = tv < full_steps;
     int pgk[PIECES], pgv[PIECES];
@@ -415,14 +427,27 @@ __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, c
       }
     }
   };
-  for (int t0 = 0; t0 < steps; t0 += 2) {
+  using Int0 = std::integral_constant<int, 0>;
+  using Int1 = std::integral_constant<int, 1>;
+  using Int2 = std::integral_constant<int, 2 % RING>;
+  using Int3 = std::integral_constant<int, 3 % RING>;
+  for (int t0 = 0; t0 < steps;) {
     meet(t0);
-    step(t0, S, T);
-    if (t0 + 1 == steps) break;
-    settle(T, k0 + (t0 + 1) * KT);
-    if (GRP == 1) meet(t0 + 1);
-    step(t0 + 1, T, S);
-    if (t0 + 2 < steps) settle(S, k0 + (t0 + 2) * KT);
+    step(Int0{}, t0, S, T);
+    if (++t0 == steps) break;
+    settle(T, k0 + t0 * KT);
+    if (GRP == 1) meet(t0);
+    step(Int1{}, t0, T, S);
+    if (++t0 == steps) break;
+    settle(S, k0 + t0 * KT);
+    if (RING == 2) continue;
+    meet(t0);
+    step(Int2{}, t0, S, T);
+    if (++t0 == steps) break;
+    settle(T, k0 + t0 * KT);
+    step(Int3{}, t0, T, S);
+    if (++t0 == steps) break;
+    settle(S, k0 + t0 * KT);
   }
   wait_vm<0>();  // no copy outlives the item
 
