@@ -122,8 +122,32 @@ def _p(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without the Stream object (2.9 us)
+
+
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    return _raw_stream(torch.cuda.current_device())
+
+
+def _stream_of(t: torch.Tensor):
+    """The current stream of the current device, where `t` has to live."""
+    if not t.is_cuda:
+        raise OQError(OQ_ERR_INVALID_ARG, "tensors must live on the GPU")
+    d = torch.cuda.current_device()
+    if t.get_device() != d:
+        raise OQError(OQ_ERR_INVALID_ARG, f"tensors live on GPU {t.get_device()}, the current device is {d}")
+    return _raw_stream(d)
+
+
+def _vec(t: torch.Tensor, n: int, dtype, what: str):
+    """Address of a contiguous GPU vector of at least n elements of `dtype`."""
+    if t is None or t.dtype is not dtype or not t.is_cuda or t.numel() < n or not t.is_contiguous():
+        _need(t, n * dtype.itemsize, what, (dtype,))
+    return t.data_ptr()
+
+
+def _opt(t: Optional[torch.Tensor], n: int, dtype, what: str):
+    return None if t is None else _vec(t, n, dtype, what)
 
 
 def _dev(t: torch.Tensor):
@@ -624,17 +648,21 @@ def oq_gemm_w8a8(qa, a_scale, w, w_scale, mean=None, w1=None, bias=None, y=None)
     (lda, ca), (ldw, cw) = qa.stride(), w.stride()
     if K != Kw or ca != 1 or cw != 1:
         raise OQError(OQ_ERR_INVALID_ARG, f"qa [M][K] and w [N][K] with unit column strides, got {qa.shape} and {w.shape}")
-    if not (qa.is_cuda and w.is_cuda):
-        raise OQError(OQ_ERR_INVALID_ARG, "tensors must live on the GPU")
-    _need(a_scale, 4 * M, "a_scale", _F32)
-    _need(w_scale, 4 * N, "w_scale", _F32)
-    if mean is not None or w1 is not None or bias is not None:
-        _epilogue_args(M, N, mean, w1, bias)
-    y = _out_y(y, M, N, qa.device)
+    stream = _stream_of(qa)
+    if not w.is_cuda:
+        raise OQError(OQ_ERR_INVALID_ARG, "w must live on the GPU")
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=qa.device)
+    elif y.dtype not in _BF16 or y.dim() != 2 or y.shape[0] < M or y.shape[1] < N:
+        _out_y(y, M, N, qa.device)
+    ldy, cy = y.stride()
+    if cy != 1 or not y.is_cuda:
+        _out_y(y, M, N, qa.device)
     # a matrix of one row has no row stride to speak of
-    _check(_lib.oq_gemm_w8a8(qa.data_ptr(), lda if M > 1 else (K + 15) // 16 * 16, a_scale.data_ptr(), M, K, w.data_ptr(),
-                             ldw if N > 1 else (K + 15) // 16 * 16, w_scale.data_ptr(), N, _p(mean), _p(w1), _p(bias),
-                             y.data_ptr(), y.stride(0) if y.shape[0] > 1 else N, _stream()))
+    _check(_lib.oq_gemm_w8a8(qa.data_ptr(), lda if M > 1 else (K + 15) // 16 * 16, _vec(a_scale, M, _F, "a_scale"), M, K,
+                             w.data_ptr(), ldw if N > 1 else (K + 15) // 16 * 16, _vec(w_scale, N, _F, "w_scale"), N,
+                             _opt(mean, M, _F, "mean"), _opt(w1, N, _F, "w1"), _opt(bias, N, _F, "bias"), y.data_ptr(),
+                             ldy if M > 1 else N, stream))
     return y
 
 
@@ -680,24 +708,23 @@ class PagedKV:
         self.ref = ctypes.byref(self.c)
 
 
-def _heads(t: torch.Tensor, what: str):
+def _heads(t: torch.Tensor, shape, what: str):
     """(address, token stride, head stride) of a GPU bfloat16 tensor [T][heads][d]."""
-    if t.dim() != 3 or not t.is_cuda or t.dtype not in _BF16:
-        raise OQError(OQ_ERR_INVALID_ARG, f"{what} must be a GPU bfloat16 tensor [T][heads][d]")
+    if t.shape != shape or not t.is_cuda or t.dtype not in _BF16:
+        raise OQError(OQ_ERR_INVALID_ARG, f"{what} must be a GPU bfloat16 tensor of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     ld, hs, es = t.stride()
-    if es != 1 and t.shape[2] > 1:
+    if es != 1:
         raise OQError(OQ_ERR_INVALID_ARG, f"{what} must have unit stride within a head")
-    T, H, d = t.shape
-    # the stride over a single token or head is never used
-    return t.data_ptr(), ld if T > 1 else 0, hs if H > 1 else 0
+    return t.data_ptr(), ld, hs
 
 
-def _same(t: torch.Tensor, shape, what: str):
-    if tuple(t.shape) != tuple(shape):
-        raise OQError(OQ_ERR_INVALID_ARG, f"{what} has shape {tuple(t.shape)}, {tuple(shape)} needed")
+def _tokens(t: torch.Tensor, what: str):
+    if t.dim() != 3:
+        raise OQError(OQ_ERR_INVALID_ARG, f"{what} must be a tensor [T][heads][d]")
+    return t.shape
 
 
-_I32, _I64 = (torch.int32,), (torch.int64,)
+_F, _I32, _I64 = torch.float32, torch.int32, torch.int64
 
 
 def oq_qk_norm_rope(q, k, w_q=None, w_k=None, eps: float = 1e-6, rope: Optional[Rope] = None, pos=None, q_out=None,
@@ -707,39 +734,35 @@ def oq_qk_norm_rope(q, k, w_q=None, w_k=None, eps: float = 1e-6, rope: Optional[
     x = q if q is not None else k
     if x is None:
         raise OQError(OQ_ERR_INVALID_ARG, "q or k is required")
-    T, _, d = x.shape
+    T, _, d = _tokens(x, "q" if q is not None else "k")
+    stream = _stream_of(x)
     args = [None, 0, 0, 0, None, 0, 0, 0]
     outs = [None, 0, 0, None, 0, 0]
     if q is not None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-        _same(q_out, q.shape, "q_out")
-        args[0:4] = *_heads(q, "q"), q.shape[1]
-        outs[0:3] = _heads(q_out, "q_out")
+        shape = q.shape
+        q_out = torch.empty(shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        args[0:4] = *_heads(q, shape, "q"), shape[1]
+        outs[0:3] = _heads(q_out, shape, "q_out")
     if k is not None:
-        if q is not None and (k.shape[0] != T or k.shape[2] != d):
-            raise OQError(OQ_ERR_INVALID_ARG, f"q and k differ: {tuple(q.shape)}, {tuple(k.shape)}")
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
-        _same(k_out, k.shape, "k_out")
-        args[4:8] = *_heads(k, "k"), k.shape[1]
-        outs[3:6] = _heads(k_out, "k_out")
-    _need(w_q, 4 * d, "w_q", _F32, optional=True)
-    _need(w_k, 4 * d, "w_k", _F32, optional=True)
-    _need(pos, 4 * T, "pos", _I32, optional=True)
-    _check(_lib.oq_qk_norm_rope(*args, T, d, _p(w_q), _p(w_k), eps, None if rope is None else rope.ref, _p(pos), *outs,
-                                _stream()))
+        shape = _tokens(k, "k")
+        if shape[0] != T or shape[2] != d:
+            raise OQError(OQ_ERR_INVALID_ARG, f"q and k differ: {tuple(x.shape)}, {tuple(shape)}")
+        k_out = torch.empty(shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
+        args[4:8] = *_heads(k, shape, "k"), shape[1]
+        outs[3:6] = _heads(k_out, shape, "k_out")
+    _check(_lib.oq_qk_norm_rope(*args, T, d, _opt(w_q, d, _F, "w_q"), _opt(w_k, d, _F, "w_k"), eps,
+                                None if rope is None else rope.ref, _opt(pos, T, _I32, "pos"), *outs, stream))
     return q_out, k_out
 
 
 def oq_kv_append(k, v, slot, kv: PagedKV, w_k=None, eps: float = 1e-6, rope: Optional[Rope] = None, pos=None):
     """k, v [T][heads][d] into the places slot (int64 [T], negative: skipped) of the cache."""
-    T = k.shape[0]
-    _same(k, (T, kv.heads, kv.d), "k")
-    _same(v, (T, kv.heads, kv.d), "v")
-    _need(slot, 8 * T, "slot", _I64)
-    _need(w_k, 4 * kv.d, "w_k", _F32, optional=True)
-    _need(pos, 4 * T, "pos", _I32, optional=True)
-    _check(_lib.oq_kv_append(*_heads(k, "k"), *_heads(v, "v"), T, _p(w_k), eps, None if rope is None else rope.ref, _p(pos),
-                             slot.data_ptr(), kv.ref, _stream()))
+    T, d = k.shape[0], kv.d
+    stream = _stream_of(k)
+    shape = (T, kv.heads, d)
+    _check(_lib.oq_kv_append(*_heads(k, shape, "k"), *_heads(v, shape, "v"), T, _opt(w_k, d, _F, "w_k"), eps,
+                             None if rope is None else rope.ref, _opt(pos, T, _I32, "pos"), _vec(slot, T, _I64, "slot"),
+                             kv.ref, stream))
 
 
 def oq_attn_prefix_ws_bytes(B: int, n_q: int, heads_q: int, kv: PagedKV, prefix_len: int, table_ld: int) -> int:
@@ -751,29 +774,28 @@ def oq_attn_prefix(q, n_q: int, kv: PagedKV, prefix_table, prefix_len: int, tabl
     """q [B n_q][heads_q][d]; prefix_table int32 [>= ceil(prefix_len / page)] (None
     without a prefix); tables int32 [B][table_ld] and lens int32 [B] (both None
     without suffixes); returns (o, lse)."""
-    T, heads_q, d = q.shape
+    shape = _tokens(q, "q")
+    T, heads_q, d = shape
     if n_q < 1 or T % n_q or d != kv.d:
-        raise OQError(OQ_ERR_INVALID_ARG, f"q of shape {tuple(q.shape)} for n_q={n_q} and heads of {kv.d}")
+        raise OQError(OQ_ERR_INVALID_ARG, f"q of shape {tuple(shape)} for n_q={n_q} and heads of {kv.d}")
     B = T // n_q
-    _need(prefix_table, 4 * (-(-prefix_len // kv.page)), "prefix_table", _I32, optional=prefix_len <= 0)
-    table_ld = 0
+    stream = _stream_of(q)
+    table_ld, table_at, lens_at = 0, None, None
     if tables is not None:
         if tables.dim() != 2 or tables.shape[0] != B:
             raise OQError(OQ_ERR_INVALID_ARG, f"tables must be a matrix of {B} rows")
         table_ld = tables.shape[1]
-        _need(tables, 0, "tables", _I32)
-        _need(lens, 4 * B, "lens", _I32)
+        table_at, lens_at = _vec(tables, 0, _I32, "tables"), _vec(lens, B, _I32, "lens")
     if o is None:
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    _same(o, q.shape, "o")
+        o = torch.empty(shape, dtype=q.dtype, device=q.device)
     if lse is None and want_lse:
-        lse = torch.empty((T, heads_q), dtype=torch.float32, device=q.device)
-    _need(lse, 4 * T * heads_q, "lse", _F32, optional=True)
+        lse = torch.empty((T, heads_q), dtype=_F, device=q.device)
     if ws is None:
         ws = torch.empty(oq_attn_prefix_ws_bytes(B, n_q, heads_q, kv, prefix_len, table_ld), dtype=torch.uint8, device=q.device)
     elif not ws.is_cuda or not ws.is_contiguous():
         raise OQError(OQ_ERR_INVALID_ARG, "ws must be a contiguous GPU tensor")
-    _check(_lib.oq_attn_prefix(*_heads(q, "q"), B, n_q, heads_q, kv.ref, _p(prefix_table), prefix_len, _p(tables), table_ld,
-                               _p(lens), scale, *_heads(o, "o"), _p(lse), ws.data_ptr(), ws.numel() * ws.element_size(),
-                               _stream()))
+    prefix_at = _vec(prefix_table, -(-prefix_len // kv.page), _I32, "prefix_table") if prefix_len > 0 else None
+    _check(_lib.oq_attn_prefix(*_heads(q, shape, "q"), B, n_q, heads_q, kv.ref, prefix_at, prefix_len, table_at, table_ld,
+                               lens_at, scale, *_heads(o, shape, "o"), _opt(lse, T * heads_q, _F, "lse"), ws.data_ptr(),
+                               ws.numel() * ws.element_size(), stream))
     return o, lse
