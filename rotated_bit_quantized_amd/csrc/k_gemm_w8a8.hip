@@ -293,79 +293,98 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW / 4 * C::RESIDENT) gemm_w8a8
   }
 }
 
-// Up to 16 MT rows: a workgroup takes 16 NT weight rows, its NW wavefronts
-// the k blocks of 64 in turn, fragments straight from memory (each weight
-// byte is used once, so LDS would only add a trip), DEPTH blocks of loads in
-// flight per wavefront; the wavefronts' int32 sums meet in LDS.
-template <int MT, int NT, int NW, int DEPTH>
-__global__ void __launch_bounds__(64 * NW) gemm_w8a8_rows(const GemmArgs g) {
-  __shared__ int part[NW][MT * NT * 256];
+// Up to 16 MT tokens: a workgroup takes 16 weight rows, its 8 wavefronts the k
+// blocks of 64 in turn.  Weight fragments come straight from memory (each byte
+// is used once, so LDS would only add a trip), two batches of 2 loads in flight
+// per wavefront; the activations, which every workgroup reads, go through LDS in
+// chunks of as many k as fit, sent before the first weight loads and with each
+// row's 16-byte pieces permuted by the row against bank conflicts.  The
+// wavefronts' int32 sums meet in LDS.  Measured: 1 x 4096 x 6144 7.7 us (batches
+// of 4 7.8, of 8 11), 16 x 1920 x 7680 6.1 (7.3, 10.8), 32 x 4096 x 14336 20.4
+// (2.9 TB/s of weights).
+template <int MT>
+__global__ void __launch_bounds__(512) gemm_w8a8_rows(const GemmArgs g, const int CH) {
+  constexpr int NW = 8, DEPTH = 2;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  __shared__ int part[NW][MT * 256];
+  const uint32_t lds0 = lds_addr_of(smem);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r16 = lane & 15, kq = 16 * (lane >> 4);
-  const int n0 = blockIdx.x * 16 * NT;
-  const int8_t *wp[NT], *ap[MT];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int64_t n = n0 + 16 * j + r16 < g.N ? n0 + 16 * j + r16 : g.N - 1;
-    wp[j] = g.w + n * g.ldw;
-  }
+  const int r16 = lane & 15, kq = lane >> 4;
+  const int64_t n = (int64_t)blockIdx.x * 16 + r16;
+  const int8_t *wp = g.w + (n < g.N ? n : g.N - 1) * g.ldw + 16 * kq;
+  const int rows = (int)g.M;
+  v4i acc[MT];
+  const uint8_t *arow[MT];  // rows past M are not stored
+  int asw[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
-    const int64_t m = 16 * i + r16 < g.M ? 16 * i + r16 : g.M - 1;
-    ap[i] = g.qa + m * g.lda;
+    acc[i] = (v4i){};
+    const int row = 16 * i + r16 < rows ? 16 * i + r16 : rows - 1;
+    arow[i] = smem + row * CH;
+    asw[i] = row & 15;
   }
-  v4i acc[MT][NT];
+  for (int k0 = 0; k0 < g.K; k0 += CH) {
+    const int kn = g.K - k0 < CH ? g.K - k0 : CH, blocks = (kn + 63) / 64;
+    // weights of blocks b, b + NW, ..; what lies past the chunk is zero
+    auto load = [&](v4i (&W)[DEPTH], int b) {
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = (v4i){};
-
-  const int blocks = (g.K + 63) / 64;
-  for (int b0 = wave; b0 < blocks; b0 += NW * DEPTH) {
-    v4i W[DEPTH][NT], A[DEPTH][MT];
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d) {
-      // blocks past the end and the missing k of the last one: weights of zero
-      const int k = 64 * (b0 + NW * d) + kq;
-      const bool ok = k < g.K;
-      const int kc = ok ? k : 0;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        W[d][j] = *reinterpret_cast<const v4i *>(wp[j] + kc);
-        if (!ok) W[d][j] = (v4i){};
+      for (int d = 0; d < DEPTH; ++d) {
+        const int k = 64 * (b + NW * d);
+        W[d] = *reinterpret_cast<const v4i *>(wp + (k + 16 * kq < kn ? k0 + k : -16 * kq));
       }
+    };
+    auto use = [&](v4i (&W)[DEPTH], int b) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i) A[d][i] = *reinterpret_cast<const v4i *>(ap[i] + kc);
+      for (int d = 0; d < DEPTH; ++d) {
+        const int blk = b + NW * d;
+        if (blk >= blocks) break;
+        if (64 * blk + 16 * kq >= kn) W[d] = (v4i){};
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const v4i A = *reinterpret_cast<const v4i *>(arow[i] + 16 * ((4 * blk + kq) ^ asw[i]));
+          acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(A, W[d], acc[i], 0, 0, 0);
+        }
+      }
+    };
+    // 1 KiB pieces of the chunk's activations, rows in turn
+    const int per_row = CH / 1024;
+    for (int u = wave; u < rows * per_row; u += NW) {
+      const int row = u / per_row, k = 1024 * (u - row * per_row) + 16 * (lane ^ (row & 15));
+      dma_lds16(g.qa + row * g.lda + (k < kn ? k0 + k : 0), lds0 + 1024 * u);
     }
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(A[d][i], W[d][j], acc[i][j], 0, 0, 0);
+    asm volatile("" ::: "memory");
+    v4i W[2][DEPTH];
+    load(W[0], wave);
+    load(W[1], wave + NW * DEPTH);
+    asm volatile("" ::: "memory");
+    wait_vm<2 * DEPTH>();  // the activations; the weights may still come
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    for (int b = wave; b < blocks; b += 2 * NW * DEPTH) {
+      use(W[0], b);
+      if (b + 2 * NW * DEPTH < blocks) load(W[0], b + 2 * NW * DEPTH);
+      use(W[1], b + NW * DEPTH);
+      if (b + 3 * NW * DEPTH < blocks) load(W[1], b + 3 * NW * DEPTH);
+    }
+    if (k0 + CH < g.K) __syncthreads();
   }
   // lane: column (weight row) l % 16, rows 4 (l / 16) + e
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) part[wave][(i * NT + j) * 256 + (4 * (lane >> 4) + e) * 16 + r16] = acc[i][j][e];
+    for (int e = 0; e < 4; ++e) part[wave][i * 256 + (4 * kq + e) * 16 + r16] = acc[i][e];
   __syncthreads();
-  for (int at = threadIdx.x; at < MT * NT * 256; at += 64 * NW) {
-    const int blk = at / 256, i = blk / NT, j = blk % NT;
-    const int64_t row = 16 * i + (at % 256) / 16;
-    const int col = n0 + 16 * j + at % 16;
-    if (row >= g.M || col >= g.N) continue;
-    int s = 0;
+  const int at = threadIdx.x;
+  const int64_t row = at / 16, col = (int64_t)blockIdx.x * 16 + at % 16;
+  if (at >= MT * 256 || row >= g.M || col >= g.N) return;
+  int s = 0;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) s += part[w][at];
-    float v = g.a_scale[row] * g.w_scale[col] * (float)s;
-    if (g.mean) v = __builtin_fmaf(g.mean[row], g.w1[col], v);
-    if (g.bias) v = v + g.bias[col];
-    g.y[row * g.ldy + col] = f32_to_bf16_rne(v);
-  }
+  for (int w = 0; w < NW; ++w) s += part[w][at];
+  float v = g.a_scale[row] * g.w_scale[col] * (float)s;
+  if (g.mean) v = __builtin_fmaf(g.mean[row], g.w1[col], v);
+  if (g.bias) v = v + g.bias[col];
+  g.y[row * g.ldy + col] = f32_to_bf16_rne(v);
 }
 
 template <class C>
@@ -381,10 +400,18 @@ hipError_t launch_tile(const GemmArgs &g, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int MT, int NT, int NW, int DEPTH>
+template <int MT>
 hipError_t launch_rows(const GemmArgs &g, hipStream_t stream) {
-  hipLaunchKernelGGL((gemm_w8a8_rows<MT, NT, NW, DEPTH>), dim3((unsigned)((g.N + 16 * NT - 1) / (16 * NT))), dim3(64 * NW), 0,
-                     stream, g);
+  // 64 KiB of activations at a time lets two workgroups share a CU; where one
+  // round of workgroups covers N, 128 KiB.  16 tokens, K = 14336, N = 4096: 16.6
+  // us with 128 KiB against 17.5; 32 tokens, K = N = 4096: 8.9 against 9.5.
+  const int lds = (g.N + 15) / 16 <= device_cus() ? 131072 : 65536;
+  int ch = lds / 1024 / (int)g.M * 1024;
+  if (ch > (g.K + 1023) / 1024 * 1024) ch = (g.K + 1023) / 1024 * 1024;
+  static std::atomic<bool> attr_set[64];
+  const hipError_t e = lds_limit_once((const void *)gemm_w8a8_rows<MT>, 131072, attr_set);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(gemm_w8a8_rows<MT>, dim3((unsigned)((g.N + 15) / 16)), dim3(512), (size_t)g.M * ch, stream, g, ch);
   return hipGetLastError();
 }
 
@@ -394,8 +421,8 @@ hipError_t launch_gemm_w8a8(const int8_t *qa, int64_t lda, const float *a_scale,
                             int64_t ldw, const float *w_scale, int N, const float *mean, const float *w1,
                             const float *bias, uint16_t *y, int64_t ldy, hipStream_t stream) {
   const GemmArgs g{qa, lda, a_scale, M, K, w, ldw, w_scale, N, mean, w1, bias, y, ldy};
-  if (M <= 16) return launch_rows<1, 1, 8, 8>(g, stream);
-  if (M <= 32) return launch_rows<2, 1, 4, 8>(g, stream);
+  if (M <= 16) return launch_rows<1>(g, stream);
+  if (M <= 32) return launch_rows<2>(g, stream);
   // The tile with the least modelled time, rounds of workgroups over the CUs
   // times the measured time of a round at K = 4096 (us; K scales all alike):
   // 256 x 256 59, 128 x 256 34, 128 x 128 20, 64 x 64 7.3 and 4 for the first.
