@@ -4,9 +4,8 @@
 //   acc = exact int32 sum over K, converted to float32 with one rounding (a
 //   sum of at most 2^31 keeps 24 bits, far more than the bfloat16 output).
 //
-// Both operands are row-major with K contiguous.  Two kernels:
-//
-// gemm_w8a8_tile: a workgroup of WM x WN wavefronts, each TI x TJ tiles of
+// Both operands are row-major with K contiguous.  Up to 32 tokens the weights
+// have to be read and little else: gemm_w8a8_rows.  Above, gemm_w8a8_tile: a workgroup of WM x WN wavefronts, each TI x TJ tiles of
 // 32 x 32 on v_mfma_i32_32x32x32_i8, accumulated in place (nothing happens
 // between k steps, so the accumulators stay where the MFMA wants them).  k
 // advances in stages of 128 through a ring of NSLOT LDS slots, filled global ->
@@ -300,8 +299,8 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW / 4 * C::RESIDENT) gemm_w8a8
 // chunks of as many k as fit, sent before the first weight loads and with each
 // row's 16-byte pieces permuted by the row against bank conflicts.  The
 // wavefronts' int32 sums meet in LDS.  Measured: 1 x 4096 x 6144 7.7 us (batches
-// of 4 7.8, of 8 11), 16 x 1920 x 7680 6.1 (7.3, 10.8), 32 x 4096 x 14336 20.4
-// (2.9 TB/s of weights).
+// of 4 7.8, of 8 11), 16 x 1920 x 7680 6.1 (7.3, 10.8), 32 x 4096 x 14336 19.7
+// (3.0 TB/s of weights).
 template <int MT>
 __global__ void __launch_bounds__(512) gemm_w8a8_rows(const GemmArgs g, const int CH) {
   constexpr int NW = 8, DEPTH = 2;
@@ -367,6 +366,7 @@ __global__ void __launch_bounds__(512) gemm_w8a8_rows(const GemmArgs g, const in
       use(W[1], b + NW * DEPTH);
       if (b + 3 * NW * DEPTH < blocks) load(W[1], b + 3 * NW * DEPTH);
     }
+    wait_vm<0>();  // weights past the chunk that nobody used: else the next copies wait for each other
     if (k0 + CH < g.K) __syncthreads();
   }
   // lane: column (weight row) l % 16, rows 4 (l / 16) + e
@@ -404,7 +404,8 @@ template <int MT>
 hipError_t launch_rows(const GemmArgs &g, hipStream_t stream) {
   // 64 KiB of activations at a time lets two workgroups share a CU; where one
   // round of workgroups covers N, 128 KiB.  16 tokens, K = 14336, N = 4096: 16.6
-  // us with 128 KiB against 17.5; 32 tokens, K = N = 4096: 8.9 against 9.5.
+  // us with 128 KiB against 17.5; 32 tokens, K = N = 4096: 8.9 against 9.5
+  // (both before the wait at the chunk's end, 14.9 and 7.9 since).
   const int lds = (g.N + 15) / 16 <= device_cus() ? 131072 : 65536;
   int ch = lds / 1024 / (int)g.M * 1024;
   if (ch > (g.K + 1023) / 1024 * 1024) ch = (g.K + 1023) / 1024 * 1024;
