@@ -261,3 +261,40 @@ def test_streams_and_graph(B, prefix):
         want = c.run()
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
     c.check(o, lse)
+
+
+MORE = [
+    # so many small pages that a split's page numbers come in several rounds
+    dict(B=1, n_q=1, Hk=1, G=4, D=64, page=8, prefix=70001, lens=[13]),
+    dict(B=40, n_q=1, Hk=1, G=4, D=64, page=8, prefix=30000, lens=[b % 9 for b in range(40)]),
+    dict(B=2, n_q=1, Hk=1, G=2, D=128, page=8, prefix=5, lens=[20000, 9001]),
+    # prefix rows in several narrow tiles, the last one ragged
+    dict(B=9, n_q=1, Hk=2, G=4, D=128, page=16, prefix=900, lens=[b for b in range(9)]),
+    dict(B=31, n_q=1, Hk=2, G=4, D=64, page=32, prefix=1111, lens=[3 * b for b in range(31)]),
+    dict(B=32, n_q=1, Hk=1, G=4, D=128, page=64, prefix=640, lens=[b for b in range(32)]),
+    # just past them: one wide tile, two wide tiles
+    dict(B=43, n_q=1, Hk=1, G=3, D=64, page=16, prefix=1500, lens=[b for b in range(43)]),
+    dict(B=129, n_q=1, Hk=1, G=2, D=128, page=16, prefix=257, lens=[b % 50 for b in range(129)]),
+    dict(B=57, n_q=3, Hk=2, G=3, D=128, page=32, prefix=65, lens=[3 + b for b in range(57)]),
+    # a sequence's own rows fill a wide tile, beside a prefix and alone
+    dict(B=2, n_q=130, Hk=2, G=2, D=64, page=16, prefix=777, lens=[400, 131]),
+    dict(B=2, n_q=131, Hk=1, G=2, D=128, page=64, prefix=0, lens=[700, 60]),
+    dict(B=1, n_q=300, Hk=1, G=4, D=128, page=128, prefix=333, lens=[300]),
+]
+
+
+@pytest.mark.parametrize("n", range(len(MORE)))
+def test_tiles_and_splits_against_float64(n):
+    c = Case(seed=100 + n, **MORE[n])
+    c.check(*c.run())
+
+
+def test_sequences_are_independent():
+    """What a sequence returns does not depend on the contents of the others."""
+    c = Case(40, 1, 2, 4, 128, 16, 1000, [30 + b for b in range(40)], seed=13)
+    o, lse = c.run()
+    c.q[1:] *= -3
+    for b in range(1, 40):
+        c.v[c.tables[b].long()] += 1
+    p, lse2 = c.run()
+    assert torch.equal(o[0], p[0]) and torch.equal(lse[0], lse2[0])
