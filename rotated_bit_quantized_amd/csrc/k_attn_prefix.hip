@@ -299,6 +299,17 @@ __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, c
 #pragma unroll
   for (int d = 0; d < DT; ++d) O[d] = (v16f){};
 
+  // largest score of a lane in four chains
+  float mq[4];
+  auto max_of = [&](const v16f (&S)[SUB], int u, int e) {
+    mq[e & 3] = u == 0 && e < 4 ? S[0][e] : __builtin_elementwise_maximum(mq[e & 3], S[u][e]);
+  };
+  auto max_all = [&](const v16f (&S)[SUB]) {
+#pragma unroll
+    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) max_of(S, u, e);
+  };
   // Masks the scores of tile `base` where it needs it and moves the reference m
   // (with O and l) where a row's maximum has outgrown it.
   auto settle = [&](v16f (&S)[SUB], int base) {
@@ -316,12 +327,8 @@ __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, c
 #pragma unroll
         for (int e = 0; e < 16; ++e) S[u][e] = (bits >> (8 * (e >> 2) + (e & 3))) & 1u ? S[u][e] : -INFINITY;
       }
+      max_all(S);
     }
-    float mq[4] = {S[0][0], S[0][1], S[0][2], S[0][3]};  // four chains
-#pragma unroll
-    for (int u = 0; u < SUB; ++u)
-#pragma unroll
-      for (int e = u ? 0 : 4; e < 16; ++e) mq[e & 3] = __builtin_elementwise_maximum(mq[e & 3], S[u][e]);
     float mx = __builtin_elementwise_maximum(__builtin_elementwise_maximum(mq[0], mq[1]),
                                              __builtin_elementwise_maximum(mq[2], mq[3]));
     mx = fmaxf(mx, xhalf(mx)) * lp.c;
@@ -355,6 +362,7 @@ __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, c
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) kreg[ks] = *reinterpret_cast<const v8bf *>(at + 32 * ks);
   }
+  max_all(S);
   settle(S, k0);
 
   // Step t: scores of tile t + 1 and the value product of tile t, its softmax
@@ -392,6 +400,12 @@ __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, c
         const int kk = 2 * u + (w - KS) / DT, d = (w - KS) % DT;
         O[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pf[kk], O[d], 0, 0, 0);
       }
+      // a 32 keys' scores stand two products after their last: their maximum
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+#pragma unroll
+        for (int x = 0; x < SUB; ++x)
+          if (t == x * PER + KS + 2 + e * (2 * DT - 2) / 16) max_of(Sn, x, e);
       constexpr int RATE = D == 64 ? 4 : 2;  // thirds of a pair per product
 #pragma unroll
       for (int pr = t * RATE / 3 + (t > 0); pr < (t + 1) * RATE / 3 + 1 && pr < PAIRS; ++pr) {
