@@ -58,7 +58,7 @@ struct PartPlan {
 // One launch: the workgroups of wide items, then those of one-wavefront items.
 struct Launch {
   PartPlan part[2];
-  int wide_items, narrow_items, waves;  // waves: wavefronts of a workgroup
+  int lead, wide_items, narrow_items, waves;  // workgroups of narrow items before the wide ones; wavefronts of a workgroup
   float c;                              // log2(e) |scale|, or 1 where scale == 0
   uint32_t qand, qxor;                  // on the bits of q pairs: sign of the scale, or zero
 };
@@ -333,7 +333,7 @@ __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, c
                                              __builtin_elementwise_maximum(mq[2], mq[3]));
     mx = fmaxf(mx, xhalf(mx)) * lp.c;
     if (__any(mx > m + RESCALE)) {
-      const float mn = fmaxf(m, mx);
+      const float mn = mx > m + RESCALE ? mx : m;  // a row's own decision: its result does not depend on the others
       const float al = mn == -INFINITY ? 1.f : exp2f(m - mn);
       m = mn;
       l[0] *= al;
@@ -484,13 +484,14 @@ attn_part_kernel(const AttnArgs a, const Launch lp, float *__restrict__ part_o, 
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const uint32_t spare = lds_addr_of(smem);  // a KiB that nobody reads
   uint8_t *mine = smem + 1024;
-  if ((int)blockIdx.x < lp.wide_items) {
+  const int past = (int)blockIdx.x - lp.lead;
+  if (past >= 0 && past < lp.wide_items) {
     const int first = lp.part[0].wide ? (int)lp.part[0].items : 0;
-    const int w = (int)blockIdx.x >= first;
-    part_body<D, 8>(a, lp, lp.part[w], w ? blockIdx.x - first : blockIdx.x, mine, spare, part_o, part_ml);
+    const int w = past >= first;
+    part_body<D, 8>(a, lp, lp.part[w], w ? past - first : past, mine, spare, part_o, part_ml);
   } else {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int item = ((int)blockIdx.x - lp.wide_items) * lp.waves + wave;
+    const int item = (past < 0 ? (int)blockIdx.x : (int)blockIdx.x - lp.wide_items) * lp.waves + wave;
     if (item >= lp.narrow_items) return;
     const int first = lp.part[0].wide ? 0 : (int)lp.part[0].items;
     const int w = item >= first;
@@ -512,40 +513,44 @@ __device__ __forceinline__ float wave_all(float v, F f) {
   return f(v, xhalf(v));
 }
 
-// The join, one wavefront per row: lanes hold the parts' statistics, 64 parts
-// at a time; D / 4 lanes then take a part's O each, 256 / D parts at once.
-// Latency bounds it up to some 4096 rows, so there the first BATCH loads of O
-// leave beside those of the statistics, whatever their weights (what a part
-// without keys has left unwritten is dropped): 96 rows, 14 parts 3.8 us against
-// 5.6.  Above, the traffic counts, and parts without keys are not read: 8192
-// rows 10.3 us against 11.4.
-template <int D, bool EARLY>
+// The join: lanes hold the parts' statistics, 64 parts at a time; D / 4 lanes
+// then take a part's O each, 256 / D parts at once.  Latency bounds it where
+// there are few rows: there the first BATCH loads of O leave beside those of the
+// statistics, whatever their weights (what a part without keys has left unwritten
+// is dropped), and with WAVES = 4 four wavefronts share a row, all of 64 parts'
+// loads on their way at once, and their sums meet in LDS.  1 row of 8 heads, 64
+// parts: 20 us with the parts' kernel, 28 with a wavefront a row.  96 rows, 14
+// parts: 3.8 us against 5.6 without the early loads.  Where there are many rows
+// the traffic counts, and parts without keys are not read (WAVES = 0): 8192 rows
+// 10.3 us, 11.4 with early loads.
+template <int D, int WAVES>
 __global__ void __launch_bounds__(256)
 attn_join_kernel(const AttnArgs a, int rows, int parts, const float *__restrict__ part_o, const float2 *__restrict__ part_ml) {
-  constexpr int L = D / 4, AT = 64 / L, BATCH = 8;
+  constexpr int L = D / 4, AT = 64 / L, STEP = WAVES == 4 ? 4 * AT : AT;
+  constexpr int BATCH = WAVES == 0 ? 0 : 64 / STEP < 8 ? 64 / STEP : 8;
+  __shared__ float4 sum[WAVES == 4 ? 4 : 1][L];
   const int64_t all = (int64_t)rows * a.kv.heads;
-  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63, gl = lane % L, sub = lane / L;
+  const int wave = threadIdx.x >> 6;
+  const int64_t id = WAVES == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
+  const int lane = threadIdx.x & 63, gl = lane % L, sub = (WAVES == 4 ? wave * AT : 0) + lane / L;
   if (id >= all) return;
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float w, const float4 &v) {
+    o.x = __builtin_fmaf(w, v.x, o.x);
+    o.y = __builtin_fmaf(w, v.y, o.y);
+    o.z = __builtin_fmaf(w, v.z, o.z);
+    o.w = __builtin_fmaf(w, v.w, o.w);
+  };
   for (int s0 = 0; s0 < parts; s0 += 64) {
     const int np = parts - s0 < 64 ? parts - s0 : 64;
-    float4 x[BATCH];
     auto read = [&](int s) { return *reinterpret_cast<const float4 *>(part_o + ((s0 + s) * all + id) * D + 4 * gl); };
-    auto add = [&](float ws, const float4 &v) {
-      o.x = __builtin_fmaf(ws, v.x, o.x);
-      o.y = __builtin_fmaf(ws, v.y, o.y);
-      o.z = __builtin_fmaf(ws, v.z, o.z);
-      o.w = __builtin_fmaf(ws, v.w, o.w);
-    };
     float2 v = make_float2(-INFINITY, 0.f);
     if (lane < np) v = part_ml[(s0 + lane) * all + id];
-    if (EARLY) {
+    float4 x[BATCH + 1];
 #pragma unroll
-      for (int u = 0; u < BATCH; ++u)
-        if (u * AT < np) x[u] = read(u * AT + sub < np ? u * AT + sub : np - 1);
-    }
+    for (int u = 0; u < BATCH; ++u)
+      if (u * STEP < np) x[u] = read(u * STEP + sub < np ? u * STEP + sub : np - 1);
     const float mx = wave_all(v.x, [](float p, float q) { return fmaxf(p, q); });
     const float mn = fmaxf(m, mx);
     if (mn == -INFINITY) continue;
@@ -554,14 +559,12 @@ attn_join_kernel(const AttnArgs a, int rows, int parts, const float *__restrict_
     const float w = v.y == 0.f ? 0.f : exp2f(v.x - m);
     l = l * al + wave_all(w * v.y, [](float p, float q) { return p + q; });
     o.x *= al, o.y *= al, o.z *= al, o.w *= al;
-    if (EARLY) {
 #pragma unroll
-      for (int u = 0; u < BATCH; ++u) {
-        const float ws = __shfl(w, u * AT + sub);  // lanes past the end have weight zero
-        add(ws, ws == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : x[u]);
-      }
+    for (int u = 0; u < BATCH; ++u) {
+      const float ws = __shfl(w, u * STEP + sub);  // lanes past the end have weight zero
+      add(ws, ws == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : x[u]);
     }
-    for (int s = EARLY ? BATCH * AT : 0; s < np; s += AT) {
+    for (int s = BATCH * STEP; s < np; s += STEP) {
       const float ws = __shfl(w, s + sub);
       if (ws != 0.f) add(ws, read(s + sub));
     }
@@ -572,6 +575,14 @@ attn_join_kernel(const AttnArgs a, int rows, int parts, const float *__restrict_
     o.y += __shfl_xor(o.y, x);
     o.z += __shfl_xor(o.z, x);
     o.w += __shfl_xor(o.w, x);
+  }
+  if (WAVES == 4) {
+    if (lane < L) sum[wave][lane] = o;
+    __syncthreads();
+    if (wave) return;
+    o = sum[0][gl];
+#pragma unroll
+    for (int u = 1; u < 4; ++u) add(1.f, sum[u][gl]);
   }
   if (lane >= L) return;
   const int G = a.heads_q / a.kv.heads;
@@ -589,6 +600,7 @@ struct Plan {
   Launch launch;
   int rows, parts;
   int64_t rows_all;
+  bool mixed;
 };
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
@@ -607,9 +619,14 @@ Plan plan_for(const AttnArgs &a) {
     const int group_rows = s ? a.n_q * G : p.rows;
     q.suffix = s;
     q.rows = p.rows;
-    // Up to 128 rows every wavefront takes 32 of them by itself, eight to a CU
-    // where there are enough; above, they share the keys through LDS.
-    q.wide = group_rows > 128;
+    // Wavefronts on their own read a key once per 32 rows, but start at once and
+    // go to every CU; eight that share keys through LDS read them once per 256
+    // rows.  Single ones up to 64 rows, or where 16 a CU with 64 keys each are
+    // enough.  Single against shared: 96 rows of 8 heads over 16384
+    // keys 40.9 us (33.4), over 2000 15.9 (21.1); 160 of 8 over 8000 31.7 (28.4);
+    // 256 of 4 over 2000 17.7 (23.9).
+    const int64_t singles = (int64_t)((group_rows + 31) / 32) * a.kv.heads * (s ? a.B : 1) * ((keys[s] + 63) / 64);
+    q.wide = group_rows > 64 && singles > 16 * cus;
     q.tiles = (group_rows + (q.wide ? 255 : 31)) / (q.wide ? 256 : 32);
     groups[s] = (int64_t)q.tiles * a.kv.heads * (s ? a.B : 1);
     // CU microseconds, as measured: 2.0 (d 128) or 1.1 (d 64) for 64 keys of a
@@ -621,19 +638,22 @@ Plan plan_for(const AttnArgs &a) {
                            : (double)groups[s] / 8 * (4 + k / 32 * (a.kv.d == 128 ? 1.9 : 1.2));
   }
   // Chunks that give every CU a workgroup, or eight single wavefronts.  Where
-  // there are both kinds and the single ones would be a mostly empty second
-  // round, wide items leave them their share of the CUs (24 sequences of 4
-  // tokens over 5000 + 333 keys: 21.2 us one kind after the other, 16.3 side by
-  // side); a full round of them comes after the wide ones (256 sequences over
-  // 32768 + 512: 224 us, 231 side by side).
+  // there are both kinds, either wide items leave the single ones a share of the
+  // CUs, at most a quarter, all in one round; or each kind has all CUs, which
+  // costs a second round's start and end, some 6 us.  One round (measured against
+  // two): 24 x 4 sequences over 5000 + 333 keys 16.3 us (21.2), 40 over 2000 + 50
+  // 22 (33), 40 over 8000 + 100 28 (36).  Two: 64 over 16384 + 2048 156 us (275),
+  // 33 over 2000 + 4000 136 (164).
   const int w = p.launch.part[0].wide ? 0 : 1;
   int64_t cus_for[2] = {cus, cus};
-  const bool mixed = p.launch.part[0].wide != p.launch.part[1].wide && keys[0] > 0 && keys[1] > 0 &&
-                     groups[1 - w] / 8 < cus / 2;
+  bool mixed = p.launch.part[0].wide != p.launch.part[1].wide && keys[0] > 0 && keys[1] > 0 && groups[1 - w] / 8 < cus / 2;
   if (mixed) {
-    const double share = work[w] / (work[0] + work[1]);
-    cus_for[w] = (int64_t)((double)cus * (share < 0.75 ? 0.75 : share));
+    const double all = work[0] + work[1], share = work[w] < 0.75 * all ? 0.75 : work[w] / all;
+    const double wide_us = work[w] / (share * (double)cus), narrow_us = work[1 - w] / ((1 - share) * (double)cus);
+    mixed = (wide_us > narrow_us ? wide_us : narrow_us) < 6 + all / (double)cus;
+    if (mixed) cus_for[w] = (int64_t)((double)cus * share);
   }
+  p.mixed = mixed;
   for (int i = 0; i < 2; ++i) {
     const int s = i ? 1 - w : w;  // wide items first
     PartPlan &q = p.launch.part[s];
@@ -641,6 +661,15 @@ Plan plan_for(const AttnArgs &a) {
     const int64_t unit = a.kv.page > 64 ? a.kv.page : 64;  // a part of fewer keys costs more than reading them
     int64_t splits = (cus_for[s] * (q.wide ? 1 : 8) + (mixed ? groups[s] / 2 : 0)) / groups[s];
     if (q.wide && splits > 1 && splits * groups[s] > cus) --splits;
+    // Two wavefronts a CU nearly fill the memory's bandwidth; more are for
+    // chunks of 256 keys at least, as each costs a partial O.  One sequence of 8
+    // heads x 4 over 16384 keys: 64 chunks 20 us, 256 24; 16 of them with 8000
+    // keys each: 16 chunks 105 us, 4 121.
+    if (!q.wide && !mixed) {
+      const int64_t two = 2 * cus / groups[s], most = keys[s] / 256;
+      if (splits > most) splits = most;
+      if (splits < two) splits = two;
+    }
     if (splits < 1) splits = 1;
     int64_t chunk = round_up((keys[s] + splits - 1) / splits, unit);
     const int64_t pages = q.wide ? Part<64, 8>::PAGES_MAX : Part<64, 1>::PAGES_MAX;
@@ -665,6 +694,10 @@ hipError_t launch_d(const AttnArgs &a, Plan &p, float *po, float2 *pm, hipStream
   lp.wide_items = (int)wide;
   lp.narrow_items = (int)narrow;
   lp.waves = wide ? 8 : 1;
+  // In two rounds, half of the single wavefronts' workgroups go first and half
+  // last, so that their traffic and the wide items' products overlap: 256
+  // sequences over 32768 + 512 keys 238 us (258 with all of them last).
+  lp.lead = wide && !p.mixed ? (int)((narrow + 7) / 8 / 2) & ~7 : 0;
   for (PartPlan &q : lp.part) q.swizzle = q.items % 8 == 0 && (q.wide || lp.waves == 1);
   if (wide + narrow > 0) {
     constexpr int WIDE = Part<D, 8>::LDS, ONE = Part<D, 1>::LDS, MOST = (WIDE > 8 * ONE ? WIDE : 8 * ONE) + 1024;
@@ -678,8 +711,12 @@ hipError_t launch_d(const AttnArgs &a, Plan &p, float *po, float2 *pm, hipStream
     const hipError_t r = hipGetLastError();
     if (r != hipSuccess) return r;
   }
-  hipLaunchKernelGGL((p.rows_all <= 4096 ? attn_join_kernel<D, true> : attn_join_kernel<D, false>),
-                     dim3((unsigned)((p.rows_all + 3) / 4)), dim3(256), 0, stream, a, p.rows, p.parts, po, pm);
+  const bool shared = p.rows_all <= 512;
+  const int64_t blocks = shared ? p.rows_all : (p.rows_all + 3) / 4;
+  const auto join = shared                ? attn_join_kernel<D, 4>
+                    : p.rows_all <= 4096 ? attn_join_kernel<D, 1>
+                                          : attn_join_kernel<D, 0>;
+  hipLaunchKernelGGL(join, dim3((unsigned)blocks), dim3(256), 0, stream, a, p.rows, p.parts, po, pm);
   return hipGetLastError();
 }
 
