@@ -298,3 +298,23 @@ def test_sequences_are_independent():
         c.v[c.tables[b].long()] += 1
     p, lse2 = c.run()
     assert torch.equal(o[0], p[0]) and torch.equal(lse[0], lse2[0])
+
+
+@pytest.mark.parametrize("n_q", [1, 3])
+def test_other_rows_do_not_move_a_rows_maximum(n_q):
+    """Rows of one tile whose scores rise at different places of the prefix: each keeps its bits."""
+    c = Case(6, n_q, 1, 4, 64, 16, 2500, [20 + b for b in range(6)], seed=14)
+    o, lse = c.run()
+    for f in (0.0, 40.0):
+        c.q[n_q:] *= f
+        p, lse2 = c.run()
+        assert torch.equal(o[:n_q], p[:n_q]) and torch.equal(lse[:n_q], lse2[:n_q])
+    c.check(p, lse2)
+
+
+def test_many_parts_and_few():
+    """One row over a long prefix (all its parts joined together), and many rows over a short one."""
+    c = Case(1, 1, 1, 1, 128, 16, 33000, [0], seed=15)
+    c.check(*c.run())
+    c = Case(700, 1, 1, 8, 64, 32, 40, [b % 4 for b in range(700)], seed=16)
+    c.check(*c.run())
