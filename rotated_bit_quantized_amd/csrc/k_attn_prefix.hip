@@ -7,12 +7,15 @@
 //     o = sum_p 2^(m_p - m) O_p / sum_p 2^(m_p - m) l_p,  m = max_p m_p.
 //
 // Rows of one key head are its query vectors in the order (token, query
-// head): the prefix part takes them in tiles of 32 QT NW rows whatever
-// sequence they belong to, so a prefix key is read once per tile; the suffix
-// part takes the n_q G rows of one sequence.  A workgroup (NW wavefronts, 32
-// QT rows each) walks a chunk of keys in tiles of KT through LDS, two
-// buffers, copied global -> LDS while the other is used.  Both products run
-// transposed on v_mfma_f32_32x32x16_bf16:
+// head): the prefix part takes them in tiles whatever sequence they belong to,
+// so a prefix key is read once per tile; the suffix part takes the n_q G rows
+// of one sequence.  An item is a row tile and a chunk of the keys, walked in
+// tiles of keys.  Wide items: eight wavefronts of 32 rows share tiles of 64
+// keys, K and V in rings of four LDS slots, copied global -> LDS two steps
+// ahead, one barrier for two steps.  Narrow items: one wavefront of 32 rows,
+// tiles of 32 keys, K fragments straight from memory, V through two LDS slots,
+// no barrier at all.  Both kinds run in one launch, the join in a second.
+// Both products run transposed on v_mfma_f32_32x32x16_bf16:
 //   S^T[key][row] = K Q^T,   O^T[d][row] += V^T P^T,
 // so that a lane owns one row: maximum, sum and rescaling are per-lane
 // (one exchange between the lane's halves), and P^T leaves the first product
@@ -22,8 +25,15 @@
 // is not.  O is rescaled only when a row's maximum has grown by more than
 // 2^8 since the last time (P then stays below 2^8, which costs float32 and
 // bfloat16 no precision).
-#include <type_traits>
-
+//
+// What bounds it.  Wide items: the matrix and the vector unit together, a
+// score costs 4 D operations on the one and an exponential, a fused multiply
+// and add, an addition, a maximum and half a conversion on the other, while
+// every wavefront reads every K and V byte from LDS; 1024 rows of 8 heads over
+// 32768 keys with D = 128 take 150 us, 0.92 PFLOP/s (a large bf16 product of
+// the library: 1.23).  Narrow items with long chunks: HBM, 256 sequences of 512
+// keys each (537 MB) 109 us, 4.9 TB/s.  Short calls: latency, launch, page
+// numbers, first keys, join; 3 sequences over 777 + 100 keys 10.4 us in all.
 #include "oq_internal.h"
 
 namespace oq {
