@@ -244,17 +244,19 @@ __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, c
   // K fragments of a tile in registers (DK): this lane's key row, chunks 2 ks +
   // half; past the end the last key, on a page outside the cache zeros
   v8bf kreg[DK ? KS : 1];
-  auto k_row = [&](int t) -> const uint8_t * {
+  typedef const __attribute__((address_space(1))) uint8_t *Global;  // else they become flat loads, which LDS reads wait for
+  typedef const __attribute__((address_space(1))) v8bf *GlobalFrag;
+  auto k_row = [&](int t) -> Global {
     int key = k0 + t * KT + r32;
     if (key > kend - 1) key = kend - 1;
     const int pg = s_page[(key - k0) >> pl];
     const uint8_t *at = kb + (int64_t)pg * (2 * a.kv.page_stride) + (key & (a.kv.page - 1)) * ROWB;
-    return ((unsigned)pg < (unsigned)a.kv.pages ? at : reinterpret_cast<const uint8_t *>(g_zero_row)) + 16 * half;
+    return (Global)((unsigned)pg < (unsigned)a.kv.pages ? at : reinterpret_cast<const uint8_t *>(g_zero_row)) + 16 * half;
   };
   if (DK) {
-    const uint8_t *at = k_row(0);
+    const Global at = k_row(0);
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) kreg[ks] = *reinterpret_cast<const v8bf *>(at + 32 * ks);
+    for (int ks = 0; ks < KS; ++ks) kreg[ks] = *(GlobalFrag)(at + 32 * ks);
   }
 
   // this lane's row: query fragments, number of places seen
@@ -368,9 +370,9 @@ __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, c
       S[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(DK ? kreg[ks] : k_frag(0, u, ks), qf[ks], S[u], 0, 0, 0);
   }
   if (DK) {
-    const uint8_t *at = k_row(1);
+    const Global at = k_row(1);
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) kreg[ks] = *reinterpret_cast<const v8bf *>(at + 32 * ks);
+    for (int ks = 0; ks < KS; ++ks) kreg[ks] = *(GlobalFrag)(at + 32 * ks);
   }
   max_all(S);
   settle(S, k0);
@@ -389,13 +391,18 @@ __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, c
     int pgk[PIECES], pgv[PIECES];
     if (!DK) pages_of(full_k ? tk : 0, pgk);
     pages_of(full_v ? tv : 0, pgv);
-    const uint8_t *k_next = DK ? k_row(t0 + 2) : nullptr;
+    const Global k_next = DK ? k_row(t0 + 2) : nullptr;
     const float mu = m == -INFINITY ? 0.f : m;
     v8bf pf[2 * SUB], frag[AHEAD + 1];
     auto frag_of = [&](int t) -> v8bf {
       const int u = t / PER, w = t % PER;
       return w < KS ? (DK ? kreg[w] : k_frag(ks_slot, u, w)) : v_frag(v_slot, 2 * u + (w - KS) / DT, (w - KS) % DT);
     };
+    // a wavefront by itself sends them at once, so that they have the whole step
+    if (DK && full_v) {
+#pragma unroll
+      for (int q = 0; q < PIECES; ++q) copy_full(true, true, tv, q, pgv[q]);
+    }
 #pragma unroll
     for (int t = 0; t < AHEAD; ++t) frag[t] = frag_of(t);
 #pragma unroll
@@ -405,7 +412,7 @@ __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, c
       const v8bf f = frag[t % (AHEAD + 1)];
       if (w < KS) {
         Sn[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, qf[w], w == 0 ? (v16f){} : Sn[u], 0, 0, 0);
-        if (DK) kreg[w] = *reinterpret_cast<const v8bf *>(k_next + 32 * w);
+        if (DK) kreg[w] = *(GlobalFrag)(k_next + 32 * w);
       } else {
         const int kk = 2 * u + (w - KS) / DT, d = (w - KS) % DT;
         O[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pf[kk], O[d], 0, 0, 0);
@@ -430,7 +437,7 @@ __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, c
 #pragma unroll
       for (int q = 0; q < PIECES; ++q) {
         if (!DK && t == 2 + 2 * q * (SLOTS - 4) / (2 * PIECES)) copy_full(full_k, false, tk, q, pgk[q]);
-        if (t == 2 + (2 * q + 1) * (SLOTS - 4) / (2 * PIECES)) copy_full(full_v, true, tv, q, pgv[q]);
+        if (!DK && t == 2 + (2 * q + 1) * (SLOTS - 4) / (2 * PIECES)) copy_full(full_v, true, tv, q, pgv[q]);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -473,7 +480,7 @@ __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, c
     if (++t0 == steps) break;
     settle(S, k0 + t0 * KT);
   }
-  wait_vm<0>();  // no copy outlives the item
+  if (!DK) wait_vm<0>();  // no copy outlives the item; one wavefront's have all been used
 
   const int r = r0 + r32;
   const float ls = l[0] + l[1], lt = ls + xhalf(ls);
