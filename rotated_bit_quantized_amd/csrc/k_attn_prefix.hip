@@ -172,16 +172,18 @@ __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, c
   // the chunk's page numbers
   const int pl = __builtin_ctz((unsigned)a.kv.page);
   const int npages = ((kend - 1) >> pl) - (k0 >> pl) + 1;
+  // every wavefront reads all of them and writes what the others write, so that
+  // none has to wait for another
   int bad = 0;
-  for (int i = NW == 1 ? lane : threadIdx.x; i < npages; i += 64 * NW) {
+  for (int i = lane; i < npages; i += 64) {
     const int pg = table[(k0 >> pl) + i];
     s_page[i] = pg;
     bad |= (unsigned)pg >= (unsigned)a.kv.pages;
   }
-  bool any_bad;
-  if (NW > 1) any_bad = __syncthreads_or(bad);
-  else any_bad = __any(bad);
-  meet_lds();
+  const bool any_bad = __any(bad);
+  __builtin_amdgcn_s_waitcnt(0xC07F);
+  __builtin_amdgcn_wave_barrier();
+  asm volatile("" ::: "memory");
   // Copies of tile t, this wavefront's pieces, K or V.  A piece is PROWS key
   // rows of one page, so its source is a scalar base and a fixed offset per
   // lane; the 16-byte chunks of a row are permuted by the row, on the source
