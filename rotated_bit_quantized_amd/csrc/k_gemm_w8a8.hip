@@ -5,7 +5,8 @@
 //   sum of at most 2^31 keeps 24 bits, far more than the bfloat16 output).
 //
 // Both operands are row-major with K contiguous.  Up to 32 tokens the weights
-// have to be read and little else: gemm_w8a8_rows.  Above, gemm_w8a8_tile: a
+// have to be read and little else, and few outputs need k split to fill the chip:
+// gemm_w8a8_rows.  Else gemm_w8a8_tile: a
 // workgroup of WM x WN wavefronts, each TI x TJ tiles of
 // 32 x 32 on v_mfma_i32_32x32x32_i8, accumulated in place (nothing happens
 // between k steps, so the accumulators stay where the MFMA wants them).  k
@@ -300,8 +301,8 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW / 4 * C::RESIDENT) gemm_w8a8
   }
 }
 
-// Up to 16 MT tokens: a workgroup takes 16 weight rows, its 8 wavefronts the k
-// blocks of 64 in turn.  Weight fragments come straight from memory (each byte
+// 16 MT tokens (a group of them: blockIdx.y) times 16 weight rows a workgroup, its
+// 8 wavefronts the k blocks of 64 in turn.  Weight fragments come straight from memory (each byte
 // is used once, so LDS would only add a trip), two batches of 2 loads in flight
 // per wavefront; the activations, which every workgroup reads, go through LDS in
 // chunks of as many k as fit, sent before the first weight loads and with each
@@ -319,7 +320,9 @@ __global__ void __launch_bounds__(512) gemm_w8a8_rows(const GemmArgs g, const in
   const int r16 = lane & 15, kq = lane >> 4;
   const int64_t n = (int64_t)blockIdx.x * 16 + r16;
   const int8_t *wp = g.w + (n < g.N ? n : g.N - 1) * g.ldw + 16 * kq;
-  const int rows = (int)g.M;
+  const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
+  const int8_t *qa = g.qa + m0 * g.lda;
+  const int rows = g.M - m0 < 16 * MT ? (int)(g.M - m0) : 16 * MT;
   v4i acc[MT];
   const uint8_t *arow[MT];  // rows past M are not stored
   int asw[MT];
@@ -357,7 +360,7 @@ __global__ void __launch_bounds__(512) gemm_w8a8_rows(const GemmArgs g, const in
     const int per_row = CH / 1024;
     for (int u = wave; u < rows * per_row; u += NW) {
       const int row = u / per_row, k = 1024 * (u - row * per_row) + 16 * (lane ^ (row & 15));
-      dma_lds16(g.qa + row * g.lda + (k < kn ? k0 + k : 0), lds0 + 1024 * u);
+      dma_lds16(qa + row * g.lda + (k < kn ? k0 + k : 0), lds0 + 1024 * u);
     }
     asm volatile("" ::: "memory");
     v4i W[2][DEPTH];
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(512) gemm_w8a8_rows(const GemmArgs g, const in
     for (int e = 0; e < 4; ++e) part[wave][i * 256 + (4 * kq + e) * 16 + r16] = acc[i][e];
   __syncthreads();
   const int at = threadIdx.x;
-  const int64_t row = at / 16, col = (int64_t)blockIdx.x * 16 + at % 16;
+  const int64_t row = m0 + at / 16, col = (int64_t)blockIdx.x * 16 + at % 16;
   if (at >= MT * 256 || row >= g.M || col >= g.N) return;
   int s = 0;
 #pragma unroll
@@ -414,13 +417,15 @@ hipError_t launch_rows(const GemmArgs &g, hipStream_t stream) {
   // round of workgroups covers N, 128 KiB.  16 tokens, K = 14336, N = 4096: 16.6
   // us with 128 KiB against 17.5; 32 tokens, K = N = 4096: 8.9 against 9.5
   // (both before the wait at the chunk's end, 14.9 and 7.9 since).
-  const int lds = (g.N + 15) / 16 <= device_cus() ? 131072 : 65536;
-  int ch = lds / 1024 / (int)g.M * 1024;
+  const int64_t nt = (g.N + 15) / 16, mt = (g.M + 16 * MT - 1) / (16 * MT);
+  const int lds = nt * mt <= device_cus() ? 131072 : 65536;
+  const int rows = g.M < 16 * MT ? (int)g.M : 16 * MT;
+  int ch = lds / 1024 / rows * 1024;
   if (ch > (g.K + 1023) / 1024 * 1024) ch = (g.K + 1023) / 1024 * 1024;
   static std::atomic<bool> attr_set[64];
   const hipError_t e = lds_limit_once((const void *)gemm_w8a8_rows<MT>, 131072, attr_set);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(gemm_w8a8_rows<MT>, dim3((unsigned)((g.N + 15) / 16)), dim3(512), (size_t)g.M * ch, stream, g, ch);
+  hipLaunchKernelGGL(gemm_w8a8_rows<MT>, dim3((unsigned)nt, (unsigned)mt), dim3(512), (size_t)rows * ch, stream, g, ch);
   return hipGetLastError();
 }
 
@@ -430,17 +435,24 @@ hipError_t launch_gemm_w8a8(const int8_t *qa, int64_t lda, const float *a_scale,
                             int64_t ldw, const float *w_scale, int N, const float *mean, const float *w1,
                             const float *bias, uint16_t *y, int64_t ldy, hipStream_t stream) {
   const GemmArgs g{qa, lda, a_scale, M, K, w, ldw, w_scale, N, mean, w1, bias, y, ldy};
-  if (M <= 16) return launch_rows<1>(g, stream);
+  // Eight wavefronts on the k of 16 x 16 outputs, where those tiles are no more
+  // than the CUs: 100 x 14336 x 500 13.4 us (64 x 64 tiles, whose few workgroups
+  // would each walk all of k: 30), 64 x 4096 x 64 5.3 (10.4), 32 x 14336 x 2048
+  // 14.0 (32 x 16 outputs: 18.7).
+  const int64_t cus = device_cus(), nt = ((int64_t)N + 15) / 16;
+  if (M <= 16 || nt * ((M + 15) / 16) <= cus) return launch_rows<1>(g, stream);
   if (M <= 32) return launch_rows<2>(g, stream);
   // The tile with the least modelled time, rounds of workgroups over the CUs
   // times the measured time of a round at K = 4096 (us; K scales all alike):
   // 256 x 256 59, 128 x 256 34, 128 x 128 20, 64 x 64 7.3 and 4 for the first.
   // Measured with K = 4096, N = 4096: 512 tokens 42.7 / 25.6 / 19.4 / 16.3, 1024
   // 44.2 / 28.5 / 22.1 / 30, 2048 47.4 / 36.2 / 40.6, 4096 63.4 / 67.4 / 77.4.
-  const int64_t cus = device_cus();
+  // Against them gemm_w8a8_rows<2>, 2.8 and 4 for a round of 32 x 16 outputs a CU:
+  // 128 tokens, N = 1024 6.8 (64 x 64 tiles 10.9), N = 2048 10.6 (11.1).
   auto rounds = [&](int64_t bm, int64_t bn) { return (double)(((M + bm - 1) / bm * ((N + bn - 1) / bn) + cus - 1) / cus); };
   const double c256 = 59 * rounds(256, 256), c384 = 34 * rounds(128, 256), c128 = 20 * rounds(128, 128),
-               c64 = 4 + 7.3 * rounds(64, 64);
+               c64 = 4 + 7.3 * rounds(64, 64), c512 = 2.8 + 4 * rounds(32, 16);
+  if (c512 <= c64 && c512 <= c128) return launch_rows<2>(g, stream);
   if (c256 <= c384 && c256 <= c128 && c256 <= c64) return launch_tile<Tile<2, 4, 4, 2, 2>>(g, stream);
   if (c384 <= c128 && c384 <= c64) return launch_tile<Tile<2, 2, 2, 4, 3>>(g, stream);
   if (c128 <= c64) return launch_tile<Tile<2, 1, 2, 4, 3>>(g, stream);

@@ -200,3 +200,19 @@ def test_rotated_layer(kind):
     _check(y, exact.cpu(), (p.abs() + r.abs() + bias.double().abs()).cpu())
     ref = x.double() @ W.double().t() + bias.double()
     assert float((y.double() - ref).norm() / ref.norm()) < 0.03
+
+
+FEW_OUTPUTS = [
+    # more tokens than one group of 16 or 32, few weight rows: k split over the wavefronts
+    (33, 16, 5), (37, 4112, 50), (49, 1008, 16), (100, 14336, 500), (130, 2064, 31), (1000, 8208, 17), (4100, 32, 1), (250, 528, 255),
+    # groups of 32, ragged, one or two rounds
+    (48, 4096, 2000), (65, 272, 1500), (300, 1040, 700), (95, 16400, 1030),
+    # long k, a chunk of which ends inside a KiB
+    (17, 131056, 33), (40, 40016, 100), (64, 15376, 1000),
+]
+
+
+@pytest.mark.parametrize("M,K,N", FEW_OUTPUTS)
+def test_few_outputs(M, K, N):
+    qa, a_s, w, w_s, kw, exact, mag = _case(M, K, N, True, M % 2 == 0, seed=M + N, lda=K + 48, ldw=K + 16)
+    _check(oq.oq_gemm_w8a8(qa, a_s, w, w_s, **kw), exact, mag)
