@@ -28,12 +28,13 @@
 //
 // What bounds it.  Wide items: the matrix and the vector unit together, a
 // score costs 4 D operations on the one and an exponential, a fused multiply
-// and add, an addition, a maximum and half a conversion on the other, while
-// every wavefront reads every K and V byte from LDS; 1024 rows of 8 heads over
-// 32768 keys with D = 128 take 150 us, 0.92 PFLOP/s (a large bf16 product of
-// the library: 1.23).  Narrow items with long chunks: HBM, 256 sequences of 512
-// keys each (537 MB) 109 us, 4.9 TB/s.  Short calls: latency, launch, page
-// numbers, first keys, join; 3 sequences over 777 + 100 keys 10.4 us in all.
+// and add, an addition, half a maximum and half a conversion on the other, while
+// every wavefront reads every K and V byte from LDS, at a clock that the power
+// limits; 1024 rows of 8 heads over 32768 keys with D = 128 take 145 us, 0.95
+// PFLOP/s (a large bf16 product of the library: 1.23).  Narrow items with long
+// chunks: HBM, 256 sequences of 512 keys each (537 MB) 106 us, 5.1 TB/s.  Short
+// calls: latency, launch, page numbers, first keys, join; 3 sequences over
+// 777 + 60 keys 9.7 us in all.
 #include "oq_internal.h"
 
 namespace oq {
@@ -537,7 +538,7 @@ __device__ __forceinline__ float wave_all(float v, F f) {
 // there are few rows: there the first BATCH loads of O leave beside those of the
 // statistics, whatever their weights (what a part without keys has left unwritten
 // is dropped), and with WAVES = 4 four wavefronts share a row, all of 64 parts'
-// loads on their way at once, and their sums meet in LDS.  1 row of 8 heads, 64
+// loads on their way at once, and their sums meet in LDS.  1 sequence, 32 rows, 64
 // parts: 20 us with the parts' kernel, 28 with a wavefront a row.  96 rows, 14
 // parts: 3.8 us against 5.6 without the early loads.  Where there are many rows
 // the traffic counts, and parts without keys are not read (WAVES = 0): 8192 rows
