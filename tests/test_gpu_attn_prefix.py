@@ -318,3 +318,107 @@ def test_many_parts_and_few():
     c.check(*c.run())
     c = Case(700, 1, 1, 8, 64, 32, 40, [b % 4 for b in range(700)], seed=16)
     c.check(*c.run())
+
+
+# Enough rows and keys that wavefronts share the keys (more than 64 rows and 16
+# tiles of 32 rows x 64 keys a CU): the prefix's part, a suffix's, both.
+WIDE = [
+    dict(B=64, n_q=1, Hk=8, G=8, D=128, page=16, prefix=2200, lens=[b % 37 for b in range(64)]),
+    dict(B=64, n_q=1, Hk=8, G=8, D=64, page=64, prefix=2177, lens=[0] * 64),
+    dict(B=43, n_q=3, Hk=8, G=6, D=64, page=32, prefix=1500, lens=[3 + 5 * b for b in range(43)]),
+    dict(B=43, n_q=3, Hk=8, G=6, D=128, page=1024, prefix=1409, lens=[b for b in range(43)]),
+    dict(B=8, n_q=100, Hk=4, G=4, D=128, page=16, prefix=0, lens=[700, 640, 100, 99, 0, 650, 333, 401]),
+    dict(B=8, n_q=100, Hk=4, G=4, D=64, page=64, prefix=700, lens=[660, 641, 100, 37, 0, 650, 512, 449]),
+    dict(B=8, n_q=100, Hk=4, G=4, D=128, page=128, prefix=40, lens=[768, 700, 640, 100, 0, 650, 512, 449]),
+    # chunks that hold as many page numbers as fit
+    dict(B=64, n_q=1, Hk=8, G=32, D=64, page=8, prefix=17003, lens=[b % 11 for b in range(64)]),
+    # more single wavefronts' work than shared work: half of it before, half after
+    dict(B=100, n_q=1, Hk=16, G=2, D=64, page=32, prefix=2500, lens=[700 - 6 * b for b in range(100)]),
+]
+
+
+@pytest.mark.parametrize("n", range(len(WIDE)))
+def test_shared_keys_against_float64(n):
+    c = Case(seed=200 + n, **WIDE[n])
+    c.check(*c.run())
+
+
+def _wide(D=128, prefix=2200, seed=20, q_scale=1.0):
+    return Case(64, 1, 8, 8, D, 16, prefix, [b % 37 for b in range(64)], seed=seed, width=3, q_scale=q_scale)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_scale", [0.0, 60.0])
+def test_shared_keys_flat_and_peaked(D, q_scale):
+    c = _wide(D, q_scale=q_scale)
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("order", ["rising", "falling"])
+def test_shared_keys_running_maximum(order):
+    c = _wide(128, 2208)
+    c.q[:] = 1.0
+    c.q[::2] = -0.5  # half of the rows see it the other way round
+    ramp = (torch.linspace(-1, 1, 2208, device=DEV) * (1 if order == "rising" else -1) * 8.8).to(BF)
+    c.k[c.prefix_table.long()] = ramp.view(-1, 1, 16, 1).expand(-1, 8, 16, 128)
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("fill", [float("nan"), float("inf"), -3e38])
+def test_shared_keys_unseen_places_may_hold_anything(D, fill):
+    c = _wide(D, 2211)
+    want = c.run()
+    seen = torch.zeros(c.pages, c.page, dtype=torch.bool, device=DEV)
+    for b in range(c.B):
+        at = torch.tensor(c.places(b, 0), device=DEV)
+        seen[at[:, 0], at[:, 1]] = True
+    mask = ~seen[:, None, :, None]
+    c.k.masked_fill_(mask, fill)
+    c.v.masked_fill_(mask, fill)
+    o, lse = c.run()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    c.check(o, lse)
+
+
+def test_shared_keys_pages_outside_the_cache():
+    c = _wide()
+    c.prefix_table[3], c.prefix_table[77], c.prefix_table[137] = -1, c.pages, 2 ** 31 - 1
+    c.k[0], c.v[0] = float("nan"), float("nan")  # page 0 is in no table then
+    for t in (c.prefix_table, c.tables):
+        t[t == 0] = -(2 ** 31)
+    c.check(*c.run())
+
+
+def test_shared_keys_strides_streams_and_graph():
+    c = _wide(64)
+    want, wlse = c.run()
+    T, H, D = c.q.shape
+    wide = torch.randn(T, (H + 3) * D, device=DEV).to(BF)
+    wide[:, D : D + H * D] = c.q.flatten(1)
+    q = wide[:, D : D + H * D].unflatten(1, (H, D))
+    out = torch.full((H + 1, T, D + 8), 3.0, dtype=BF, device=DEV)
+    o = out[:H, :, :D].transpose(0, 1)
+    kv = oq.PagedKV(c.k, c.v)
+    ws = torch.full((oq.oq_attn_prefix_ws_bytes(c.B, 1, H, kv, c.prefix, c.S),), 255, dtype=torch.uint8, device=DEV)
+    lse = torch.empty(T, H, device=DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        oq.oq_attn_prefix(q, 1, kv, c.prefix_table, c.prefix, c.tables, c.lens, c.scale, o=o, lse=lse, ws=ws)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(o, want) and torch.equal(lse, wlse)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        oq.oq_attn_prefix(q, 1, kv, c.prefix_table, c.prefix, c.tables, c.lens, c.scale, o=o, lse=lse, ws=ws)
+    for _ in range(3):
+        wide.mul_(-1.25)
+        c.q.mul_(-1.25)
+        c.lens.sub_(5)
+        g.replay()
+        torch.cuda.synchronize()
+        want, wlse = c.run()
+        assert torch.equal(o, want) and torch.equal(lse, wlse)
+    c.check(o.contiguous(), lse)
+    o.fill_(3.0)
+    assert (out == 3.0).all()
