@@ -562,19 +562,24 @@ attn_join_kernel(const AttnArgs a, int rows, int parts, const float *__restrict_
     o.z = __builtin_fmaf(w, v.z, o.z);
     o.w = __builtin_fmaf(w, v.w, o.w);
   };
+  auto stats = [&](int s) { return s < parts ? part_ml[s * all + id] : make_float2(-INFINITY, 0.f); };
+  float2 next = stats(lane);
   for (int s0 = 0; s0 < parts; s0 += 64) {
     const int np = parts - s0 < 64 ? parts - s0 : 64;
     auto read = [&](int s) { return *reinterpret_cast<const float4 *>(part_o + ((s0 + s) * all + id) * D + 4 * gl); };
-    float2 v = make_float2(-INFINITY, 0.f);
-    if (lane < np) v = part_ml[(s0 + lane) * all + id];
     float4 x[BATCH + 1];
+    auto load = [&]() {
 #pragma unroll
-    for (int u = 0; u < BATCH; ++u)
-      if (u * STEP < np) x[u] = read(u * STEP + sub < np ? u * STEP + sub : np - 1);
+      for (int u = 0; u < BATCH; ++u)
+        if (u * STEP < np) x[u] = read(u * STEP + sub < np ? u * STEP + sub : np - 1);
+    };
+    const float2 v = next;
+    if (s0 == 0) load();
+    next = stats(s0 + 64 + lane);
     const float mx = wave_all(v.x, [](float p, float q) { return fmaxf(p, q); });
-    const float mn = fmaxf(m, mx);
-    if (mn == -INFINITY) continue;
-    const float al = exp2f(m - mn);
+    if (mx == -INFINITY) continue;  // no part of these has keys
+    if (s0 > 0) load();
+    const float mn = fmaxf(m, mx), al = exp2f(m - mn);
     m = mn;
     const float w = v.y == 0.f ? 0.f : exp2f(v.x - m);
     l = l * al + wave_all(w * v.y, [](float p, float q) { return p + q; });
