@@ -608,6 +608,8 @@ int oq_kv_append(const uint16_t *k, int64_t k_ld, int64_t k_hs, const uint16_t *
  * page numbers in order; lens int32 [B], at most table_ld * page places are
  * read.  Keys on a page number outside [0, pages) are left out.  Cache places
  * that no query token of a sequence sees may hold anything, NaN included.
+ * NaN in a query, or in a key or value that a row sees, gives NaN there.  A row's
+ * bits do not depend on the contents of other rows.
  * The prefix is read once for all rows of a tile; scores, statistics and sums
  * are float32; softmax numerators enter the value product as bfloat16 (their
  * sum is of the float32 values).

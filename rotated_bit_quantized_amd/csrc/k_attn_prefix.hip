@@ -488,7 +488,8 @@ __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, c
   const int r = r0 + r32;
   const float ls = l[0] + l[1], lt = ls + xhalf(ls);
   if (r >= rend) return;
-  if (half == 0) part_ml[prow + r] = make_float2(m, lt);
+  // a sum that is NaN reaches the output whatever m, which NaN scores do not move
+  if (half == 0) part_ml[prow + r] = make_float2(lt == lt ? m : 0.f, lt);
   float *dst = part_o + (prow + r) * D + 4 * half;
 #pragma unroll
   for (int d = 0; d < DT; ++d)

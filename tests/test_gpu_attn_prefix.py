@@ -422,3 +422,26 @@ def test_shared_keys_strides_streams_and_graph():
     c.check(o.contiguous(), lse)
     o.fill_(3.0)
     assert (out == 3.0).all()
+
+
+@pytest.mark.parametrize("B", [3, 64])
+def test_nan_in_a_query_shows_in_its_row(B):
+    c = Case(B, 1, 8, 8, 64, 16, 2200 if B == 64 else 100, [5 + b for b in range(B)], seed=30)
+    want = c.run()
+    c.q[1, 3, 7] = float("nan")
+    o, lse = c.run()
+    assert torch.isnan(o[1, 3]).all() and torch.isnan(lse[1, 3])
+    keep = torch.ones(B, 64, dtype=torch.bool, device=DEV)
+    keep[1, 3] = False
+    assert torch.equal(o[keep], want[0][keep]) and torch.equal(lse[keep], want[1][keep])
+
+
+def test_nan_in_a_seen_key_shows_in_the_rows_that_see_it():
+    c = Case(3, 1, 2, 4, 128, 16, 100, [5, 20, 9], seed=31)
+    want = c.run()
+    c.k[int(c.tables[1, 0]), 1, 3] = float("nan")
+    o, lse = c.run()
+    assert torch.isnan(o[1, 4:]).all() and torch.isnan(lse[1, 4:]).all()
+    keep = torch.ones(3, 8, dtype=torch.bool, device=DEV)
+    keep[1, 4:] = False
+    assert torch.equal(o[keep], want[0][keep]) and torch.equal(lse[keep], want[1][keep])
