@@ -445,3 +445,42 @@ def test_nan_in_a_seen_key_shows_in_the_rows_that_see_it():
     keep = torch.ones(3, 8, dtype=torch.bool, device=DEV)
     keep[1, 4:] = False
     assert torch.equal(o[keep], want[0][keep]) and torch.equal(lse[keep], want[1][keep])
+
+
+# One part of the keys alone, which writes the output itself: own keys or a
+# prefix, single wavefronts and shared keys, rows without keys among them.
+DIRECT = [
+    dict(B=30, n_q=1, Hk=4, G=4, D=128, page=16, prefix=0, lens=[2 * b % 61 for b in range(30)]),
+    dict(B=17, n_q=3, Hk=2, G=5, D=64, page=32, prefix=0, lens=[3 * b for b in range(17)]),
+    dict(B=3, n_q=1, Hk=2, G=4, D=64, page=64, prefix=40, lens=[0, 0, 0]),
+    dict(B=5, n_q=2, Hk=1, G=40, D=128, page=16, prefix=0, lens=[0, 1, 2, 64, 33]),
+    dict(B=8, n_q=100, Hk=8, G=8, D=128, page=16, prefix=0, lens=[700, 640, 0, 50, 100, 650, 333, 401]),
+    dict(B=8, n_q=100, Hk=8, G=8, D=64, page=64, prefix=0, lens=[0, 641, 700, 37, 0, 650, 512, 449]),
+]
+
+
+@pytest.mark.parametrize("n", range(len(DIRECT)))
+def test_one_part_against_float64(n):
+    c = Case(seed=300 + n, **DIRECT[n])
+    assert oq.oq_attn_prefix_ws_bytes(c.B, c.n_q, c.Hk * c.G, oq.PagedKV(c.k, c.v), c.prefix, c.S) == 0
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("n", [1, 5])
+def test_one_part_strides_and_guard(n):
+    c = Case(seed=310 + n, **DIRECT[n])
+    want, wlse = c.run()
+    T, H, D = c.q.shape
+    out = torch.full((H + 1, T + 1, D + 8), 3.0, dtype=BF, device=DEV)
+    o = out[:H, :T, :D].transpose(0, 1)
+    lse = torch.full((T + 1, H), 5.0, device=DEV)
+    oq.oq_attn_prefix(c.q, c.n_q, oq.PagedKV(c.k, c.v), c.prefix_table, 0, c.tables, c.lens, c.scale, o=o, lse=lse[:T])
+    assert torch.equal(o, want) and torch.equal(lse[:T], wlse) and (lse[T] == 5.0).all()
+    out[:H, :T, :D] = 3.0
+    assert (out == 3.0).all()
+    oq.oq_attn_prefix(c.q, c.n_q, oq.PagedKV(c.k, c.v), c.prefix_table, 0, c.tables, c.lens, c.scale, o=o)
+    assert torch.equal(o, want)
+    c.q[0, 0, 0] = float("nan")
+    c.lens[0] = c.n_q
+    o2, lse2 = c.run()
+    assert torch.isnan(o2[0, 0]).all() and torch.isnan(lse2[0, 0]) and torch.equal(o2[c.n_q :], want[c.n_q :])
