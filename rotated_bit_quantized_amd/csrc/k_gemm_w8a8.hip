@@ -444,13 +444,14 @@ hipError_t launch_gemm_w8a8(const int8_t *qa, int64_t lda, const float *a_scale,
   if (M <= 32) return launch_rows<2>(g, stream);
   // The tile with the least modelled time, rounds of workgroups over the CUs
   // times the measured time of a round at K = 4096 (us; K scales all alike):
-  // 256 x 256 59, 128 x 256 34, 128 x 128 20, 64 x 64 7.3 and 4 for the first.
+  // 256 x 256 59, 128 x 256 34, 128 x 128 22, 64 x 64 7.3 and 4 for the first.
   // Measured with K = 4096, N = 4096: 512 tokens 42.7 / 25.6 / 19.4 / 16.3, 1024
-  // 44.2 / 28.5 / 22.1 / 30, 2048 47.4 / 36.2 / 40.6, 4096 63.4 / 67.4 / 77.4.
+  // 44.2 / 28.5 / 22.1 / 30, 2048 47.4 / 36.2 / 40.6, 4096 63.4 / 67.4 / 77.4;
+  // 1952 x 13984 x 8705 419 / 396 / 431 / 613.
   // Against them gemm_w8a8_rows<2>, 2.8 and 4 for a round of 32 x 16 outputs a CU:
   // 128 tokens, N = 1024 6.8 (64 x 64 tiles 10.9), N = 2048 10.6 (11.1).
   auto rounds = [&](int64_t bm, int64_t bn) { return (double)(((M + bm - 1) / bm * ((N + bn - 1) / bn) + cus - 1) / cus); };
-  const double c256 = 59 * rounds(256, 256), c384 = 34 * rounds(128, 256), c128 = 20 * rounds(128, 128),
+  const double c256 = 59 * rounds(256, 256), c384 = 34 * rounds(128, 256), c128 = 22 * rounds(128, 128),
                c64 = 4 + 7.3 * rounds(64, 64), c512 = 2.8 + 4 * rounds(32, 16);
   if (c512 <= c64 && c512 <= c128) return launch_rows<2>(g, stream);
   if (c256 <= c384 && c256 <= c128 && c256 <= c64) return launch_tile<Tile<2, 4, 4, 2, 2>>(g, stream);
