@@ -108,8 +108,8 @@ __global__ void __launch_bounds__(256) heads_kernel(const HeadArgs a, const int 
   }
   // this lane's cos and sin: element e of a split pair uses index e mod dim/2
   // (8 in a row, sin negated on the a side), element 2i or 2i + 1 of an
-  // interleaved one index i (4 in a row)
-  constexpr int CN = KIND == ROPE_SPLIT ? 8 : 4;
+  // interleaved one index i (4 in a row); otherwise element by element
+  constexpr int CN = KIND == ROPE_PAIRS ? 4 : 8;
   float co[CN], si[CN];
   const bool low = e0 < hd, rot = turn && mine && e0 < dim;
   int partner = lane;  // the lane that holds the other side of this lane's split pairs
@@ -125,6 +125,18 @@ __global__ void __launch_bounds__(256) heads_kernel(const HeadArgs a, const int 
 #pragma unroll
         for (int j = 0; j < 8; ++j) si[j] = low ? -si[j] : si[j];
       }
+    }
+  }
+  if (KIND == ROPE_ANY) {
+#pragma unroll
+    for (int j = 0; j < CN; ++j) {
+      const int e = e0 + j;
+      co[j] = 1.f, si[j] = 0.f;
+      if (!rot || e >= dim) continue;
+      const bool first = a.rope.interleaved ? !(e & 1) : e < hd;
+      const int64_t k = row * hd + (a.rope.interleaved ? e >> 1 : first ? e : e - hd);
+      co[j] = a.rope.cos[k];
+      si[j] = first ? -a.rope.sin[k] : a.rope.sin[k];
     }
   }
 
@@ -173,12 +185,8 @@ __global__ void __launch_bounds__(256) heads_kernel(const HeadArgs a, const int 
         for (int j = 0; j < 8; ++j) {
           const int e = e0 + j;
           if (e >= dim) continue;
-          const bool first = a.rope.interleaved ? !(e & 1) : e < hd;
-          const int k = a.rope.interleaved ? e >> 1 : first ? e : e - hd;
-          const int pe = a.rope.interleaved ? e ^ 1 : first ? e + hd : e - hd;
-          const float cv = a.rope.cos[row * hd + k], sv = a.rope.sin[row * hd + k];
-          const float pv = stage[g * L * 8 + pe];
-          x[j] = first ? x[j] * cv - pv * sv : x[j] * cv + pv * sv;
+          const int pe = a.rope.interleaved ? e ^ 1 : e < hd ? e + hd : e - hd;
+          x[j] = x[j] * co[j] + stage[g * L * 8 + pe] * si[j];
         }
       }
     }
@@ -242,9 +250,11 @@ hipError_t launch_heads(const HeadArgs &a, hipStream_t stream) {
   // heads keep more loads in flight and read the tables less often, fewer give
   // small calls enough wavefronts.  40 heads of 128, one / two / four per group:
   // T = 128 3.3 / 3.5 / 4.9 us, 1024 6.0 / 5.5 / 6.3, 4096 21.7 / 20.1 / 18.6.
+  // No more than a part has: 29681 tokens of 1 + 1 heads 12.2 us, 14.3 with two.
   const int64_t waves = a.T * heads * (a.d <= 64 ? 8 : a.d <= 128 ? 16 : a.d <= 256 ? 32 : 64) / 64;
-  if (waves >= 16384) return launch_h<4>(a, kind, stream);
-  if (waves >= 4096) return launch_h<2>(a, kind, stream);
+  const int most = a.part[0].heads > a.part[1].heads ? a.part[0].heads : a.part[1].heads;
+  if (waves >= 16384 && most > 2) return launch_h<4>(a, kind, stream);
+  if (waves >= 4096 && most > 1) return launch_h<2>(a, kind, stream);
   return launch_h<1>(a, kind, stream);
 }
 
