@@ -232,3 +232,16 @@ def test_streams_and_graph():
         assert torch.equal(eq, qo) and torch.equal(ek, ko)
         assert torch.equal(cache[0][slot // page, :, slot % page], ek)
         assert torch.equal(cache[1][slot // page, :, slot % page], v)
+
+
+@pytest.mark.parametrize("T,hq,hk", [(9000, 5, 3), (3000, 16, 2), (2500, 7, 3), (30000, 1, 1), (12000, 2, 1)])
+@pytest.mark.parametrize("d,dim,inter", [(80, 40, False), (80, 36, True), (128, 20, False), (64, 62, False), (128, 128, False), (64, 32, True)])
+def test_several_heads_of_a_group(T, hq, hk, d, dim, inter):
+    """Token counts at which a lane group takes one, two or four heads, every kind of pairs."""
+    q, k = _x(T, hq, d, 1), _x(T, hk, d, 2)
+    w = 1 + 0.3 * torch.randn(d, generator=torch.Generator(device=DEV).manual_seed(6), device=DEV)
+    pos = torch.randint(0, 200, (T,), generator=torch.Generator(device=DEV).manual_seed(7), device=DEV).int()
+    rope = oq.Rope(*_tables(200, dim), inter)
+    qo, ko = oq.oq_qk_norm_rope(q, k, w, None, EPS, rope, pos)
+    _check(qo, *_exact(q, w, rope, pos))
+    _check(ko, *_exact(k, None, rope, pos))
