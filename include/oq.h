@@ -602,7 +602,7 @@ int oq_kv_append(const uint16_t *k, int64_t k_ld, int64_t k_hs, const uint16_t *
  * token i sees the whole prefix and the suffix places j < lens[b] - n_q + 1 + i.
  *   o[t][h] = sum_j p_j v_j,  p = softmax_j(scale q[t][h] . k_j)
  * over the seen keys of key head h / (heads_q / kv->heads); a row that sees
- * no key gives zeros and lse -inf.  lse (nullable) float32 [B n_q][heads_q]:
+ * no key, or whose every score is -inf, gives zeros and lse -inf.  lse (nullable) float32 [B n_q][heads_q]:
  * log sum_j exp(scale q . k_j).
  * prefix_table int32 [ceil(prefix_len / page)], tables int32 [B][table_ld]:
  * page numbers in order; lens int32 [B], at most table_ld * page places are

@@ -504,16 +504,17 @@ __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, c
   if (r >= rend) return;
   if (lp.direct) {  // what the join of one part would give
     const int tok = r / G, h = hk * G + (r - tok * G);
-    const float inv = lt == 0.f ? 0.f : 1.f / lt;
+    const bool none = lt == 0.f;  // no key has weight: zeros, whatever the values were
+    const float inv = 1.f / lt;
+    auto out = [&](float v) { return (uint32_t)f32_to_bf16_rne(none ? 0.f : v * inv); };
     uint16_t *dst = a.o + tok * a.o_ld + h * a.o_hs + 4 * half;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        *reinterpret_cast<uint2 *>(dst + 32 * d + 8 * e) = make_uint2(
-            (uint32_t)f32_to_bf16_rne(O[d][4 * e] * inv) | ((uint32_t)f32_to_bf16_rne(O[d][4 * e + 1] * inv) << 16),
-            (uint32_t)f32_to_bf16_rne(O[d][4 * e + 2] * inv) | ((uint32_t)f32_to_bf16_rne(O[d][4 * e + 3] * inv) << 16));
-    if (a.lse && half == 0) a.lse[(int64_t)tok * a.heads_q + h] = lt == 0.f ? -INFINITY : LN2 * (m + log2f(lt));
+        *reinterpret_cast<uint2 *>(dst + 32 * d + 8 * e) =
+            make_uint2(out(O[d][4 * e]) | out(O[d][4 * e + 1]) << 16, out(O[d][4 * e + 2]) | out(O[d][4 * e + 3]) << 16);
+    if (a.lse && half == 0) a.lse[(int64_t)tok * a.heads_q + h] = none ? -INFINITY : LN2 * (m + log2f(lt));
     return;
   }
   // a sum that is NaN reaches the output whatever m, which NaN scores do not move

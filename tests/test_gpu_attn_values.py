@@ -1,0 +1,78 @@
+"""oq_attn_prefix where values, keys, queries or the scale are infinite, NaN or
+zero: what a row does not see leaves no trace in it, what it sees arrives,
+whichever plan of parts the sizes select.  Finite outputs within the bound of
+test_gpu_attn_prefix.py."""
+import math
+
+import pytest
+import torch
+
+import rotated_bit_quantized_amd as oq
+from test_gpu_attn_prefix import Case
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+NAN, INF = float("nan"), float("inf")
+
+
+def _exact(c, b, i):
+    """Output, lse, the bound's magnitude and score error of token i of sequence b, float64 [Hk][G][D] (lse [Hk][G])."""
+    at = torch.tensor(c.places(b, i), device=DEV)
+    q = c.q[b * c.n_q + i].double().view(c.Hk, c.G, c.D)
+    k, v = (t[at[:, 0], :, at[:, 1]].double().transpose(0, 1) for t in (c.k, c.v))
+    s = torch.matmul(q, k.transpose(1, 2).contiguous()) * c.scale
+    ds = (c.D + 4) * 2.0 ** -24 * (torch.matmul(q.abs(), k.abs().transpose(1, 2).contiguous()) * abs(c.scale)).amax(-1)
+    z = torch.logsumexp(s, -1)
+    p = torch.exp(s - z[..., None])
+    return torch.matmul(p, v), z, torch.matmul(p, v.abs()), ds
+
+
+def _check(c, o, lse):
+    for b in range(c.B):
+        for i in range(c.n_q):
+            t = b * c.n_q + i
+            if not c.places(b, i):
+                assert (o[t] == 0).all() and (lse[t] == -INF).all(), (b, i)
+                continue
+            y, z, A, ds = _exact(c, b, i)
+            got = o[t].double().view(c.Hk, c.G, c.D)
+            assert torch.equal(torch.isnan(got), torch.isnan(y)), (b, i)
+            big = torch.isinf(y)
+            assert torch.equal(got[big], y[big]), (b, i)
+            ok = torch.isfinite(y)
+            tol = 2.0 ** -8 * y.abs() + A * (1.01 * 2.0 ** -8 + 2 * ds[..., None] + 2.0 ** -18)
+            assert ((got - y).abs()[ok] <= tol[ok]).all(), (b, i)
+            got = lse[t].double().view(c.Hk, c.G)
+            assert ((got - z).abs() <= ds + 2.0 ** -20 * (1 + z.abs())).all(), (b, i)
+
+
+def _own(c, b, j):
+    """(page, offset) of place j of sequence b's own keys."""
+    return int(c.tables[b, j // c.page]), j % c.page
+
+
+@pytest.mark.parametrize("prefix", [0, 211])
+@pytest.mark.parametrize("D", [64, 128])
+def test_tokens_before_the_first_key_give_zeros(prefix, D):
+    """Two of four query tokens stand before their sequence's first key, whose value is not finite."""
+    c = Case(3, 4, 2, 4, D, 16, prefix, [2, 1, 3], seed=40)
+    for b, bad in ((0, NAN), (1, INF), (2, -INF)):
+        p, off = _own(c, b, 0)
+        c.v[p, :, off] = bad
+    o, lse = c.run()
+    if prefix == 0:
+        assert oq.oq_attn_prefix_ws_bytes(3, 4, 8, oq.PagedKV(c.k, c.v), 0, c.S) == 0  # one part writes the output
+        for t in (0, 1, 4, 5, 6, 8):
+            assert (o[t] == 0).all() and (lse[t] == -INF).all(), t
+
+
+@pytest.mark.parametrize("prefix,lens", [(0, [30, 30]), (30, [0, 0]), (30, [30, 30])])
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_keys_without_weight_alone(prefix, lens, bad):
+    """Every key of a row scores -inf and its value is not finite: zeros, as for a row without keys."""
+    c = Case(2, 1, 1, 2, 64, 16, prefix, lens, seed=41, width=2)
+    c.q.abs_().add_(0.1)
+    c.k[..., 0] = -INF
+    c.v[:] = bad
+    o, lse = c.run()
+    assert (o == 0).all() and (lse == -INF).all()
