@@ -223,23 +223,24 @@ __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, c
     const uint32_t dst = ((is_v ? P::VBASE : 0) + t % RING) * TILE + (wave * PIECES + q) * 1024;
     dma_lds16_s((is_v ? vb : kb) + (full ? off : 0), prow_l * ROWB + c, full ? lds0 + dst : spare);
   };
-  // A tile with missing keys: rows past the end repeat the last key, rows on a
-  // page outside the cache are zeros, so that what no row sees, NaN perhaps,
-  // does not meet a zero weight in the value product.
+  // A tile with missing keys: rows past the end and rows on a page outside the
+  // cache are zeros, so that what no row sees, NaN perhaps, does not meet a zero
+  // weight in the value product (nor does a seen infinity a second time).
   auto copy_any = [&](bool is_v, int t) {
     int pg[PIECES], key[PIECES];
 #pragma unroll
     for (int q = 0; q < PIECES; ++q) {
       key[q] = k0 + t * KT + (wave * PIECES + q) * PROWS + prow_l;
-      if (key[q] > kend - 1) key[q] = kend - 1;
-      pg[q] = s_page[(key[q] - k0) >> pl];
+      const int at = key[q] < kend ? key[q] : kend - 1;
+      pg[q] = s_page[(at - k0) >> pl];
     }
 #pragma unroll
     for (int q = 0; q < PIECES; ++q) {
       const int row = (wave * PIECES + q) * PROWS + prow_l;
       const uint32_t c = 16 * (phys_l ^ (is_v ? swz_v<D>(row) : swz_k<D>(row)));
       const uint8_t *at = (is_v ? vb : kb) + (int64_t)pg[q] * (2 * a.kv.page_stride) + (key[q] & (a.kv.page - 1)) * ROWB;
-      dma_lds16(((unsigned)pg[q] < (unsigned)a.kv.pages ? at : reinterpret_cast<const uint8_t *>(g_zero_row)) + c,
+      const bool there = key[q] < kend && (unsigned)pg[q] < (unsigned)a.kv.pages;
+      dma_lds16((there ? at : reinterpret_cast<const uint8_t *>(g_zero_row)) + c,
                 lds0 + ((is_v ? P::VBASE : 0) + t % RING) * TILE + (wave * PIECES + q) * 1024);
     }
   };

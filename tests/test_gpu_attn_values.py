@@ -76,3 +76,19 @@ def test_keys_without_weight_alone(prefix, lens, bad):
     c.v[:] = bad
     o, lse = c.run()
     assert (o == 0).all() and (lse == -INF).all()
+
+
+@pytest.mark.parametrize("prefix,lens", [(37, [0, 0, 0]), (0, [5, 33, 70]), (37, [5, 33, 70]), (2211, [1, 2, 3])])
+@pytest.mark.parametrize("B", [3, 192])
+@pytest.mark.parametrize("D", [64, 128])
+def test_infinite_value_at_the_last_place(prefix, lens, B, D):
+    """The last key of a part ends inside a tile: its infinite value gives infinity, in its place, not NaN."""
+    c = Case(B, 1, 8 if B > 3 else 2, 4, D, 16, prefix, (lens * B)[:B], seed=42, width=5)
+    for bad, d in ((INF, 3), (-INF, 9)):
+        if prefix:
+            c.v[int(c.prefix_table[(prefix - 1) // 16]), 0, (prefix - 1) % 16, d] = bad
+        for b in range(B):
+            if int(c.lens[b]) > 0:
+                p, off = _own(c, b, int(c.lens[b]) - 1)
+                c.v[p, 1, off, d + 1] = bad
+    _check(c, *c.run())
