@@ -607,7 +607,8 @@ int oq_kv_append(const uint16_t *k, int64_t k_ld, int64_t k_hs, const uint16_t *
  * prefix_table int32 [ceil(prefix_len / page)], tables int32 [B][table_ld]:
  * page numbers in order; lens int32 [B], at most table_ld * page places are
  * read.  Keys on a page number outside [0, pages) are left out.  Cache places
- * that no query token of a sequence sees may hold anything, NaN included.
+ * that a row does not see (past its sequence's length, or of a later query
+ * token) may hold anything, NaN included, without a trace in that row.
  * NaN in a query, or in a key or value that a row sees, gives NaN there.  A row's
  * bits do not depend on the contents of other rows.
  * The prefix is read once for all rows of a tile; scores, statistics and sums

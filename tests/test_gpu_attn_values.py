@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import rotated_bit_quantized_amd as oq
-from test_gpu_attn_prefix import Case
+from test_gpu_attn_prefix import DIRECT, WIDE, Case
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -92,3 +92,68 @@ def test_infinite_value_at_the_last_place(prefix, lens, B, D):
                 p, off = _own(c, b, int(c.lens[b]) - 1)
                 c.v[p, 1, off, d + 1] = bad
     _check(c, *c.run())
+
+
+LATER = [
+    # single wavefronts: a prefix beside the own keys, own keys alone, more tokens than one tile holds, tokens before the first key
+    dict(B=3, n_q=4, Hk=2, G=4, D=64, page=16, prefix=211, lens=[4, 61, 33]),
+    dict(B=3, n_q=4, Hk=2, G=4, D=128, page=16, prefix=211, lens=[2, 64, 32]),
+    dict(B=4, n_q=5, Hk=1, G=3, D=64, page=32, prefix=0, lens=[5, 77, 3, 0]),
+    dict(B=3, n_q=4, Hk=1, G=8, D=128, page=8, prefix=0, lens=[2, 40, 129]),
+    dict(B=2, n_q=37, Hk=2, G=1, D=128, page=16, prefix=65, lens=[37, 200]),
+    dict(B=1, n_q=60, Hk=1, G=1, D=64, page=64, prefix=0, lens=[500]),
+    # wavefronts that share the keys, with a prefix and alone
+    WIDE[4], WIDE[5], WIDE[6], DIRECT[4], DIRECT[5],
+]
+
+
+@pytest.mark.parametrize("n", range(len(LATER)))
+@pytest.mark.parametrize("every", [False, True])
+def test_later_tokens_values_stay_out_of_earlier_rows(n, every):
+    """Values that are not finite at the query tokens' own places, a few of them
+    or all: a row shows those that it sees, where they stand, and no others."""
+    c = Case(seed=400 + n, **LATER[n])
+    clean = c.v.clone()
+    want = c.run()
+    g = torch.Generator().manual_seed(n)
+    first_bad = []
+    for b in range(c.B):
+        L = min(int(c.lens[b]), c.S * c.page)
+        own = list(range(max(0, L - c.n_q + 1), L)) or [L - 1] * (L > 0)
+        if not every:
+            own = sorted({own[int(torch.randint(0, len(own), (1,), generator=g))] for _ in range(2)} | set(own[-1:])) if own else []
+        for j in own:
+            p, off = _own(c, b, j)
+            h = int(torch.randint(0, c.Hk, (1,), generator=g))
+            for bad in (NAN, INF, -INF):
+                c.v[p, h, off, int(torch.randint(0, c.D, (1,), generator=g))] = bad
+        first_bad.append(own[0] if own else L)
+    assert not torch.equal(clean.view(torch.int16), c.v.view(torch.int16))
+    o, lse = c.run()
+    assert torch.equal(lse, want[1])  # no value enters it
+    for b in range(c.B):
+        for i in range(c.n_q):
+            if int(c.lens[b]) - c.n_q + 1 + i <= first_bad[b]:
+                t = b * c.n_q + i
+                assert torch.equal(o[t], want[0][t]), (b, i)
+    _check(c, o, lse)
+
+
+@pytest.mark.parametrize("n", [0, 3, 6, 9])
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_whole_later_tokens_not_finite(n, bad):
+    """Keys and values of each sequence's last place: only the last token's rows see them."""
+    c = Case(seed=430 + n, **LATER[n])
+    want = c.run()
+    for b in range(c.B):
+        if 0 < int(c.lens[b]) <= c.S * c.page:
+            p, off = _own(c, b, int(c.lens[b]) - 1)
+            c.k[p, :, off] = bad
+            c.v[p, :, off] = bad
+    o, lse = c.run()
+    for b in range(c.B):
+        last = (b + 1) * c.n_q - 1
+        assert torch.equal(o[b * c.n_q : last], want[0][b * c.n_q : last]), b
+        assert torch.equal(lse[b * c.n_q : last], want[1][b * c.n_q : last]), b
+        if int(c.lens[b]) > 0:
+            assert torch.isnan(o[last]).any(), b
