@@ -609,8 +609,9 @@ int oq_kv_append(const uint16_t *k, int64_t k_ld, int64_t k_hs, const uint16_t *
  * read.  Keys on a page number outside [0, pages) are left out.  Cache places
  * that a row does not see (past its sequence's length, or of a later query
  * token) may hold anything, NaN included, without a trace in that row.
- * NaN in a query, or in a key or value that a row sees, gives NaN there.  A row's
- * bits do not depend on the contents of other rows.
+ * NaN in a query, or in a key or value that a row sees, gives NaN there; an
+ * infinite value gives infinity, or NaN where its weight is too small for
+ * float32.  A row's bits do not depend on the contents of other rows.
  * The prefix is read once for all rows of a tile; scores, statistics and sums
  * are float32; softmax numerators enter the value product as bfloat16 (their
  * sum is of the float32 values).

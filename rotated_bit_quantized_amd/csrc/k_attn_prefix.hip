@@ -672,17 +672,19 @@ attn_join_kernel(const AttnArgs a, int rows, int parts, const float *__restrict_
     if (s0 > 0) load();
     const float mn = fmaxf(m, mx), al = exp2f(m - mn);
     m = mn;
-    const float w = v.y == 0.f ? 0.f : exp2f(v.x - m);
-    l = l * al + wave_all(w * v.y, [](float p, float q) { return p + q; });
+    // -1: without keys, its O unwritten.  A weight that vanishes still takes its
+    // part's O, which may be NaN.
+    const float w = v.y == 0.f ? -1.f : exp2f(v.x - m);
+    l = l * al + wave_all(w < 0.f ? 0.f : w * v.y, [](float p, float q) { return p + q; });
     o.x *= al, o.y *= al, o.z *= al, o.w *= al;
 #pragma unroll
     for (int u = 0; u < BATCH; ++u) {
-      const float ws = __shfl(w, u * STEP + sub);  // lanes past the end have weight zero
-      add(ws, ws == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : x[u]);
+      const float ws = __shfl(w, u * STEP + sub);  // lanes past the end have no keys either
+      add(ws, ws < 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : x[u]);
     }
     for (int s = BATCH * STEP; s < np; s += STEP) {
       const float ws = __shfl(w, s + sub);
-      if (ws != 0.f) add(ws, read(s + sub));
+      if (ws >= 0.f) add(ws, read(s + sub));
     }
   }
 #pragma unroll

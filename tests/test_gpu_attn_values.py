@@ -157,3 +157,18 @@ def test_whole_later_tokens_not_finite(n, bad):
         assert torch.equal(lse[b * c.n_q : last], want[1][b * c.n_q : last]), b
         if int(c.lens[b]) > 0:
             assert torch.isnan(o[last]).any(), b
+
+
+@pytest.mark.parametrize("B,Hk,G", [(1, 1, 1), (1, 8, 4), (40, 8, 4), (192, 8, 4)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_nan_in_a_part_of_vanishing_weight_shows(B, Hk, G, D):
+    """A NaN value among keys whose whole part weighs less than float32 can tell beside another."""
+    c = Case(B, 1, Hk, G, D, 16, 2000, [20] * B, seed=43)
+    c.q[:] = 1.0
+    c.k[c.tables.long()] = 4.0 * math.sqrt(D) * 16 / D  # scores 64, the prefix's below -192 of them
+    c.k[c.prefix_table.long()] = -12.0 * math.sqrt(D) * 16 / D
+    c.v[int(c.prefix_table[3]), Hk - 1, 5, 7] = NAN
+    o, lse = c.run()
+    nan = torch.zeros_like(o, dtype=torch.bool)
+    nan[:, (Hk - 1) * G :, 7] = True
+    assert torch.equal(torch.isnan(o), nan) and torch.isfinite(lse).all()
