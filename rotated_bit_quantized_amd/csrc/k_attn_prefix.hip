@@ -73,7 +73,8 @@ struct Launch {
   int direct;                           // the only part: no join
   int lead, wide_items, narrow_items, waves;  // workgroups of narrow items before the wide ones; wavefronts of a workgroup
   float c;                              // log2(e) |scale|, or 1 where scale == 0
-  uint32_t qand, qxor;                  // on the bits of q pairs: sign of the scale, or zero
+  uint32_t qxor;                        // on the bits of q pairs: sign of the scale
+  int zero;                             // scale == 0: q is taken as 0, NaN where it is not finite
 };
 
 template <int D>
@@ -327,8 +328,15 @@ __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, c
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       u32x4 v = *reinterpret_cast<const u32x4 *>(src + 16 * ks);
+      if (lp.zero) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = (v[e] & lp.qand) ^ lp.qxor;
+        for (int e = 0; e < 4; ++e) {  // an exponent of all ones carries into the sign's place
+          const uint32_t bad = ((v[e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+          v[e] = (bad >> 15) * 0x7fc0u;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] ^= lp.qxor;
       qf[ks] = __builtin_bit_cast(v8bf, v);
     }
   }
@@ -853,8 +861,8 @@ size_t attn_prefix_ws(const AttnArgs &a) {
 hipError_t launch_attn_prefix(const AttnArgs &a, void *ws, hipStream_t stream) {
   Plan p = plan_for(a);
   p.launch.c = a.scale == 0.f ? 1.f : __builtin_fabsf(a.scale) * LOG2E;
-  p.launch.qand = a.scale == 0.f ? 0u : 0xffffffffu;
   p.launch.qxor = a.scale < 0.f ? 0x80008000u : 0u;
+  p.launch.zero = a.scale == 0.f;
   float *po = static_cast<float *>(ws);
   float2 *pm = reinterpret_cast<float2 *>(po + (size_t)p.parts * p.rows_all * a.kv.d);
   return a.kv.d == 64 ? launch_d<64>(a, p, po, pm, stream) : launch_d<128>(a, p, po, pm, stream);

@@ -172,3 +172,22 @@ def test_nan_in_a_part_of_vanishing_weight_shows(B, Hk, G, D):
     nan = torch.zeros_like(o, dtype=torch.bool)
     nan[:, (Hk - 1) * G :, 7] = True
     assert torch.equal(torch.isnan(o), nan) and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+@pytest.mark.parametrize("B,prefix", [(3, 100), (64, 2200)])
+def test_scale_zero_keeps_what_is_not_finite(bad, B, prefix):
+    """0 times a score that is not finite is NaN, for a query's element as for a key's."""
+    c = Case(B, 1, 8, 8, 64, 16, prefix, [5 + b % 30 for b in range(B)], seed=44)
+    c.scale = 0.0
+    want = c.run()
+    c.q[1, 3, 7] = bad
+    c.q[2, 9, 60] = -3e38  # finite: no part in it
+    p, off = _own(c, 2, 4)
+    c.k[p, 7, off, 11] = bad
+    o, lse = c.run()
+    nan = torch.zeros(B, 64, dtype=torch.bool, device=DEV)
+    nan[1, 3] = True
+    nan[2, 56:] = True
+    assert torch.isnan(o[nan]).all() and torch.isnan(lse[nan]).all()
+    assert torch.equal(o[~nan], want[0][~nan]) and torch.equal(lse[~nan], want[1][~nan])
