@@ -73,7 +73,9 @@ int check_attn(const char *fn, const AttnArgs &a) {
   if (a.prefix_len < 0 || a.table_ld < 0) return fail(OQ_ERR_INVALID_ARG, "%s: negative prefix_len or table_ld", fn);
   if ((int64_t)a.table_ld * a.kv.page > 0x7fffffff - 1024 || a.prefix_len > 0x7fffffff - 1024)
     return fail(OQ_ERR_UNSUPPORTED, "%s: more than 2^31 - 1024 places in one sequence", fn);
-  if ((int64_t)a.B * a.n_q * a.heads_q > 0x7fffffff / 2)
+  // one product at a time: that of all three can pass 64 bits
+  const int64_t most = (int64_t)1 << 30, tokens = (int64_t)a.B * a.n_q;
+  if (tokens > most || tokens * a.heads_q > most)
     return fail(OQ_ERR_UNSUPPORTED, "%s: more than 2^30 query rows", fn);
   return OQ_OK;
 }

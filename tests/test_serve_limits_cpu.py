@@ -1,0 +1,15 @@
+"""Refusals of the serving operators at the ends of their argument ranges (CPU only)."""
+import ctypes
+
+import pytest
+
+import rotated_bit_quantized_amd as oq
+from test_serve_cpu import AT, INV, UNS, _call, _kv
+
+
+@pytest.mark.parametrize("B,n_q,heads_q", [(1 << 22, 1 << 21, 1 << 21), (1 << 30, 1 << 30, 8), ((1 << 31) - 1, (1 << 31) - 1, (1 << 31) - 8),
+                                           (1 << 16, 1 << 16, 1 << 30), (1, 1, (1 << 30) + 8)])
+def test_attn_prefix_row_counts_past_64_bits(B, n_q, heads_q):
+    """Products of the three counts that pass 2^30, 2^63 and come back as small numbers modulo 2^64."""
+    assert _call("oq_attn_prefix", AT, dict(B=B, n_q=n_q, heads_q=heads_q)) == UNS
+    assert oq.lib().oq_attn_prefix_ws_bytes(B, n_q, heads_q, _kv(), 60, 2) == 0
