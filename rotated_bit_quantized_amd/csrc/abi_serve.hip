@@ -213,7 +213,7 @@ int oq_attn_prefix(const uint16_t *q, int64_t q_ld, int64_t q_hs, int32_t B, int
                    o, o_ld, o_hs, lse};
   int rc = check_attn(fn, a);
   if (rc) return rc;
-  if (!std::isfinite(scale)) return fail(OQ_ERR_INVALID_ARG, "%s: scale is not finite", fn);
+  if (!std::isfinite(scale * ATTN_LOG2E)) return fail(OQ_ERR_INVALID_ARG, "%s: scale log2(e) is not finite", fn);
   const int64_t T = (int64_t)B * n_q;
   rc = check_heads(fn, "q", q, q_ld, q_hs, heads_q, T, kv->d);
   if (!rc) rc = check_heads(fn, "o", o, o_ld, o_hs, heads_q, T, kv->d);

@@ -48,7 +48,6 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float RESCALE = 8.f;      // log2 growth of a maximum that rescales O
-constexpr float LOG2E = 1.44269504088896340736f;
 constexpr float LN2 = 0.69314718055994530942f;
 
 // what masked key rows are copied from, so that they cannot put NaN into a product
@@ -860,7 +859,7 @@ size_t attn_prefix_ws(const AttnArgs &a) {
 
 hipError_t launch_attn_prefix(const AttnArgs &a, void *ws, hipStream_t stream) {
   Plan p = plan_for(a);
-  p.launch.c = a.scale == 0.f ? 1.f : __builtin_fabsf(a.scale) * LOG2E;
+  p.launch.c = a.scale == 0.f ? 1.f : __builtin_fabsf(a.scale) * ATTN_LOG2E;
   p.launch.qxor = a.scale < 0.f ? 0x80008000u : 0u;
   p.launch.zero = a.scale == 0.f;
   float *po = static_cast<float *>(ws);

@@ -366,6 +366,7 @@ struct AttnArgs {
   int64_t o_ld, o_hs;
   float *lse;
 };
+constexpr float ATTN_LOG2E = 1.44269504088896340736f;  // scores are kept in units of log 2
 size_t attn_prefix_ws(const AttnArgs &a);
 hipError_t launch_attn_prefix(const AttnArgs &a, void *ws, hipStream_t stream);
 

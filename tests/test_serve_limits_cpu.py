@@ -13,3 +13,9 @@ def test_attn_prefix_row_counts_past_64_bits(B, n_q, heads_q):
     """Products of the three counts that pass 2^30, 2^63 and come back as small numbers modulo 2^64."""
     assert _call("oq_attn_prefix", AT, dict(B=B, n_q=n_q, heads_q=heads_q)) == UNS
     assert oq.lib().oq_attn_prefix_ws_bytes(B, n_q, heads_q, _kv(), 60, 2) == 0
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -3.4e38])
+def test_attn_prefix_scale_past_float32(scale):
+    """scale log2(e), by which the kernels multiply, is not finite: a score of 0 would become NaN."""
+    assert _call("oq_attn_prefix", AT, dict(scale=ctypes.c_float(scale))) == INV
