@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(256) heads_kernel(const HeadArgs a, const int 
   // interleaved one index i (4 in a row); otherwise element by element
   constexpr int CN = KIND == ROPE_PAIRS ? 4 : 8;
   float co[CN], si[CN];
-  const bool low = e0 < hd, rot = turn && mine && e0 < dim;
+  const bool low = e0 < hd, rot = turn && mine && e0 < dim;  // others pass: turning an infinity by 0 would make NaN
   int partner = lane;  // the lane that holds the other side of this lane's split pairs
   if (KIND == ROPE_SPLIT || KIND == ROPE_PAIRS) {
 #pragma unroll
@@ -167,13 +167,16 @@ __global__ void __launch_bounds__(256) heads_kernel(const HeadArgs a, const int 
       float p[8];
       unpack8(p, pr);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = x[j] * co[j] + (P.w ? p[j] * r * wp[j] : p[j]) * si[j];
+      for (int j = 0; j < 8; ++j) {
+        const float y = x[j] * co[j] + (P.w ? p[j] * r * wp[j] : p[j]) * si[j];
+        x[j] = rot ? y : x[j];
+      }
     } else if (KIND == ROPE_PAIRS && turn) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float u = x[2 * j], v = x[2 * j + 1];
-        x[2 * j] = u * co[j] - v * si[j];
-        x[2 * j + 1] = v * co[j] + u * si[j];
+        const float u = x[2 * j], v = x[2 * j + 1], y = u * co[j] - v * si[j], z = v * co[j] + u * si[j];
+        x[2 * j] = rot ? y : u;
+        x[2 * j + 1] = rot ? z : v;
       }
     } else if (KIND == ROPE_ANY && P.rope) {
       __syncthreads();
