@@ -392,10 +392,11 @@ __global__ void __launch_bounds__(512) gemm_w8a8_rows(const GemmArgs g, const in
   int s = 0;
 #pragma unroll
   for (int w = 0; w < NW; ++w) s += part[w][at];
-  float v = g.a_scale[row] * g.w_scale[col] * (float)s;
-  if (g.mean) v = __builtin_fmaf(g.mean[row], g.w1[col], v);
-  if (g.bias) v = v + g.bias[col];
-  g.y[row * g.ldy + col] = f32_to_bf16_rne(v);
+  // as in the tiles, zeros stand for what is not given: the sign of a zero too
+  // does not depend on the kernel
+  const float v = g.a_scale[row] * g.w_scale[col] * (float)s;
+  const float r = __builtin_fmaf(g.mean ? g.mean[row] : 0.f, g.mean ? g.w1[col] : 0.f, v);
+  g.y[row * g.ldy + col] = f32_to_bf16_rne(r + (g.bias ? g.bias[col] : 0.f));
 }
 
 template <class C>
