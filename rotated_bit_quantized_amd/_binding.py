@@ -122,7 +122,8 @@ def _p(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without the Stream object (2.9 us)
+# the current stream's handle; the first without the Stream object (2.9 us), where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
 
 
 def _stream():
