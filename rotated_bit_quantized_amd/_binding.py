@@ -130,25 +130,33 @@ def _stream():
     return _raw_stream(torch.cuda.current_device())
 
 
-def _stream_of(t: torch.Tensor):
-    """The current stream of the current device, where `t` has to live."""
-    if not t.is_cuda:
-        raise OQError(OQ_ERR_INVALID_ARG, "tensors must live on the GPU")
-    d = torch.cuda.current_device()
-    if t.get_device() != d:
-        raise OQError(OQ_ERR_INVALID_ARG, f"tensors live on GPU {t.get_device()}, the current device is {d}")
-    return _raw_stream(d)
+def _on(t, dev: int, what: str):
+    """t lives on the current device `dev` (get_device() of a host tensor is -1)."""
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise OQError(OQ_ERR_INVALID_ARG, f"{what} must live on the GPU")
+        raise OQError(OQ_ERR_INVALID_ARG, f"{what} lives on GPU {t.get_device()}, the current device is {dev}")
 
 
-def _vec(t: torch.Tensor, n: int, dtype, what: str):
-    """Address of a contiguous GPU vector of at least n elements of `dtype`."""
-    if t is None or t.dtype is not dtype or not t.is_cuda or t.numel() < n or not t.is_contiguous():
+def _current(t: torch.Tensor, what: str):
+    """The current device, where `t` has to live, and its current stream."""
+    if not t.is_cuda:  # before the runtime is asked
+        raise OQError(OQ_ERR_INVALID_ARG, f"{what} must live on the GPU")
+    dev = torch.cuda.current_device()
+    _on(t, dev, what)
+    return dev, _raw_stream(dev)
+
+
+def _vec(t: torch.Tensor, n: int, dtype, what: str, dev: int):
+    """Address of a contiguous vector of at least n elements of `dtype` on GPU `dev`."""
+    if t is None or t.dtype is not dtype or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
         _need(t, n * dtype.itemsize, what, (dtype,))
+        _on(t, dev, what)
     return t.data_ptr()
 
 
-def _opt(t: Optional[torch.Tensor], n: int, dtype, what: str):
-    return None if t is None else _vec(t, n, dtype, what)
+def _opt(t: Optional[torch.Tensor], n: int, dtype, what: str, dev: int):
+    return None if t is None else _vec(t, n, dtype, what, dev)
 
 
 def _dev(t: torch.Tensor):
@@ -623,7 +631,11 @@ def oq_quant_weight_w8(w, rot: Optional[Rotation] = None, codes=None, scales=Non
     if w.dim() != 2 or w.dtype != torch.float32 or w.stride(1) != 1:
         raise OQError(OQ_ERR_INVALID_ARG, "w must be a float32 matrix with unit column stride")
     N, K = w.shape
-    dev = _dev(w)
+    on, stream = _current(w, "w")
+    dev = w.device
+    for t in () if rot is None else (rot.perm, rot.signs, rot.mats):
+        if t is not None:
+            _on(t, on, "the rotation")
     Kq = rot.width if rot is not None else K
     if codes is None:
         codes = torch.empty((N, Kq), dtype=torch.int8, device=dev)
@@ -634,10 +646,9 @@ def oq_quant_weight_w8(w, rot: Optional[Rotation] = None, codes=None, scales=Non
         scales = torch.empty(N, dtype=torch.float32, device=dev)
     if want_w1 and w1 is None:
         w1 = torch.empty(N, dtype=torch.float32, device=dev)
-    _need(scales, 4 * N, "scales", _F32)
-    _need(w1, 4 * N, "w1", _F32, optional=True)
-    _check(_lib.oq_quant_weight_w8(_p(w), N, K, w.stride(0), _rref(rot), _p(codes), codes.stride(0), _p(scales),
-                                   _p(w1), _stream()))
+    _on(codes, on, "codes")
+    _check(_lib.oq_quant_weight_w8(_p(w), N, K, w.stride(0), _rref(rot), _p(codes), codes.stride(0),
+                                   _vec(scales, N, _F, "scales", on), _opt(w1, N, _F, "w1", on), stream))
     return {"codes": codes, "scales": scales, "w1": w1}
 
 
@@ -649,21 +660,21 @@ def oq_gemm_w8a8(qa, a_scale, w, w_scale, mean=None, w1=None, bias=None, y=None)
     (lda, ca), (ldw, cw) = qa.stride(), w.stride()
     if K != Kw or ca != 1 or cw != 1:
         raise OQError(OQ_ERR_INVALID_ARG, f"qa [M][K] and w [N][K] with unit column strides, got {qa.shape} and {w.shape}")
-    stream = _stream_of(qa)
-    if not w.is_cuda:
-        raise OQError(OQ_ERR_INVALID_ARG, "w must live on the GPU")
+    dev, stream = _current(qa, "qa")
+    _on(w, dev, "w")
     if y is None:
         y = torch.empty((M, N), dtype=torch.bfloat16, device=qa.device)
     elif y.dtype not in _BF16 or y.dim() != 2 or y.shape[0] < M or y.shape[1] < N:
         _out_y(y, M, N, qa.device)
     ldy, cy = y.stride()
-    if cy != 1 or not y.is_cuda:
+    if cy != 1:
         _out_y(y, M, N, qa.device)
+    _on(y, dev, "y")
     # a matrix of one row has no row stride to speak of
-    _check(_lib.oq_gemm_w8a8(qa.data_ptr(), lda if M > 1 else (K + 15) // 16 * 16, _vec(a_scale, M, _F, "a_scale"), M, K,
-                             w.data_ptr(), ldw if N > 1 else (K + 15) // 16 * 16, _vec(w_scale, N, _F, "w_scale"), N,
-                             _opt(mean, M, _F, "mean"), _opt(w1, N, _F, "w1"), _opt(bias, N, _F, "bias"), y.data_ptr(),
-                             ldy if M > 1 else N, stream))
+    _check(_lib.oq_gemm_w8a8(qa.data_ptr(), lda if M > 1 else (K + 15) // 16 * 16, _vec(a_scale, M, _F, "a_scale", dev), M, K,
+                             w.data_ptr(), ldw if N > 1 else (K + 15) // 16 * 16, _vec(w_scale, N, _F, "w_scale", dev), N,
+                             _opt(mean, M, _F, "mean", dev), _opt(w1, N, _F, "w1", dev), _opt(bias, N, _F, "bias", dev),
+                             y.data_ptr(), ldy if M > 1 else N, stream))
     return y
 
 
@@ -686,6 +697,8 @@ class Rope:
             raise OQError(OQ_ERR_INVALID_ARG, "cos and sin must be matrices of one shape")
         for t, what in ((cos, "cos"), (sin, "sin")):
             _need(t, 0, what, _F32)
+        self.dev = cos.get_device()
+        _on(sin, self.dev, "sin")
         self.cos, self.sin, self.interleaved = cos, sin, interleaved
         self.c = oq_rope(cos.data_ptr(), sin.data_ptr(), cos.shape[0], 2 * cos.shape[1], int(interleaved))
         self.ref = ctypes.byref(self.c)
@@ -701,7 +714,8 @@ class PagedKV:
                 raise OQError(OQ_ERR_INVALID_ARG, f"{what} must be a GPU bfloat16 tensor [pages][heads][page][d]")
             if t.stride()[1:] != (t.shape[2] * t.shape[3], t.shape[3], 1):
                 raise OQError(OQ_ERR_INVALID_ARG, f"the pages of {what} must be contiguous")
-        if k.shape != v.shape or k.stride() != v.stride() or k.device != v.device:
+        self.dev = k.get_device()
+        if k.shape != v.shape or k.stride() != v.stride() or v.get_device() != self.dev:
             raise OQError(OQ_ERR_INVALID_ARG, "k and v must have one shape, stride and device")
         self.k, self.v = k, v
         self.pages, self.heads, self.page, self.d = k.shape
@@ -709,9 +723,17 @@ class PagedKV:
         self.ref = ctypes.byref(self.c)
 
 
-def _heads(t: torch.Tensor, shape, what: str):
-    """(address, token stride, head stride) of a GPU bfloat16 tensor [T][heads][d]."""
-    if t.shape != shape or not t.is_cuda or t.dtype not in _BF16:
+def _handle(h, dev: int, what: str):
+    """Reference to the descriptor of a Rope or PagedKV, whose tensors have to live on GPU `dev`."""
+    if h.dev != dev:
+        raise OQError(OQ_ERR_INVALID_ARG, f"{what} lives on GPU {h.dev}, the current device is {dev}")
+    return h.ref
+
+
+def _heads(t: torch.Tensor, shape, what: str, dev: int):
+    """(address, token stride, head stride) of a bfloat16 tensor [T][heads][d] on GPU `dev`."""
+    _on(t, dev, what)
+    if t.shape != shape or t.dtype not in _BF16:
         raise OQError(OQ_ERR_INVALID_ARG, f"{what} must be a GPU bfloat16 tensor of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     ld, hs, es = t.stride()
     if es != 1:
@@ -736,34 +758,35 @@ def oq_qk_norm_rope(q, k, w_q=None, w_k=None, eps: float = 1e-6, rope: Optional[
     if x is None:
         raise OQError(OQ_ERR_INVALID_ARG, "q or k is required")
     T, _, d = _tokens(x, "q" if q is not None else "k")
-    stream = _stream_of(x)
+    dev, stream = _current(x, "q" if q is not None else "k")
     args = [None, 0, 0, 0, None, 0, 0, 0]
     outs = [None, 0, 0, None, 0, 0]
     if q is not None:
         shape = q.shape
         q_out = torch.empty(shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-        args[0:4] = *_heads(q, shape, "q"), shape[1]
-        outs[0:3] = _heads(q_out, shape, "q_out")
+        args[0:4] = *_heads(q, shape, "q", dev), shape[1]
+        outs[0:3] = _heads(q_out, shape, "q_out", dev)
     if k is not None:
         shape = _tokens(k, "k")
         if shape[0] != T or shape[2] != d:
             raise OQError(OQ_ERR_INVALID_ARG, f"q and k differ: {tuple(x.shape)}, {tuple(shape)}")
         k_out = torch.empty(shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
-        args[4:8] = *_heads(k, shape, "k"), shape[1]
-        outs[3:6] = _heads(k_out, shape, "k_out")
-    _check(_lib.oq_qk_norm_rope(*args, T, d, _opt(w_q, d, _F, "w_q"), _opt(w_k, d, _F, "w_k"), eps,
-                                None if rope is None else rope.ref, _opt(pos, T, _I32, "pos"), *outs, stream))
+        args[4:8] = *_heads(k, shape, "k", dev), shape[1]
+        outs[3:6] = _heads(k_out, shape, "k_out", dev)
+    _check(_lib.oq_qk_norm_rope(*args, T, d, _opt(w_q, d, _F, "w_q", dev), _opt(w_k, d, _F, "w_k", dev), eps,
+                                None if rope is None else _handle(rope, dev, "rope"), _opt(pos, T, _I32, "pos", dev), *outs,
+                                stream))
     return q_out, k_out
 
 
 def oq_kv_append(k, v, slot, kv: PagedKV, w_k=None, eps: float = 1e-6, rope: Optional[Rope] = None, pos=None):
     """k, v [T][heads][d] into the places slot (int64 [T], negative: skipped) of the cache."""
     T, d = k.shape[0], kv.d
-    stream = _stream_of(k)
+    dev, stream = _current(k, "k")
     shape = (T, kv.heads, d)
-    _check(_lib.oq_kv_append(*_heads(k, shape, "k"), *_heads(v, shape, "v"), T, _opt(w_k, d, _F, "w_k"), eps,
-                             None if rope is None else rope.ref, _opt(pos, T, _I32, "pos"), _vec(slot, T, _I64, "slot"),
-                             kv.ref, stream))
+    _check(_lib.oq_kv_append(*_heads(k, shape, "k", dev), *_heads(v, shape, "v", dev), T, _opt(w_k, d, _F, "w_k", dev), eps,
+                             None if rope is None else _handle(rope, dev, "rope"), _opt(pos, T, _I32, "pos", dev),
+                             _vec(slot, T, _I64, "slot", dev), _handle(kv, dev, "kv"), stream))
 
 
 def oq_attn_prefix_ws_bytes(B: int, n_q: int, heads_q: int, kv: PagedKV, prefix_len: int, table_ld: int) -> int:
@@ -780,23 +803,23 @@ def oq_attn_prefix(q, n_q: int, kv: PagedKV, prefix_table, prefix_len: int, tabl
     if n_q < 1 or T % n_q or d != kv.d:
         raise OQError(OQ_ERR_INVALID_ARG, f"q of shape {tuple(shape)} for n_q={n_q} and heads of {kv.d}")
     B = T // n_q
-    stream = _stream_of(q)
+    dev, stream = _current(q, "q")
     table_ld, table_at, lens_at = 0, None, None
     if tables is not None:
         if tables.dim() != 2 or tables.shape[0] != B:
             raise OQError(OQ_ERR_INVALID_ARG, f"tables must be a matrix of {B} rows")
         table_ld = tables.shape[1]
-        table_at, lens_at = _vec(tables, 0, _I32, "tables"), _vec(lens, B, _I32, "lens")
+        table_at, lens_at = _vec(tables, 0, _I32, "tables", dev), _vec(lens, B, _I32, "lens", dev)
     if o is None:
         o = torch.empty(shape, dtype=q.dtype, device=q.device)
     if lse is None and want_lse:
         lse = torch.empty((T, heads_q), dtype=_F, device=q.device)
     if ws is None:
         ws = torch.empty(oq_attn_prefix_ws_bytes(B, n_q, heads_q, kv, prefix_len, table_ld), dtype=torch.uint8, device=q.device)
-    elif not ws.is_cuda or not ws.is_contiguous():
-        raise OQError(OQ_ERR_INVALID_ARG, "ws must be a contiguous GPU tensor")
-    prefix_at = _vec(prefix_table, -(-prefix_len // kv.page), _I32, "prefix_table") if prefix_len > 0 else None
-    _check(_lib.oq_attn_prefix(*_heads(q, shape, "q"), B, n_q, heads_q, kv.ref, prefix_at, prefix_len, table_at, table_ld,
-                               lens_at, scale, *_heads(o, shape, "o"), _opt(lse, T * heads_q, _F, "lse"), ws.data_ptr(),
-                               ws.numel() * ws.element_size(), stream))
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise OQError(OQ_ERR_INVALID_ARG, f"ws must be a contiguous tensor on GPU {dev}")
+    prefix_at = _vec(prefix_table, -(-prefix_len // kv.page), _I32, "prefix_table", dev) if prefix_len > 0 else None
+    _check(_lib.oq_attn_prefix(*_heads(q, shape, "q", dev), B, n_q, heads_q, _handle(kv, dev, "kv"), prefix_at, prefix_len,
+                               table_at, table_ld, lens_at, scale, *_heads(o, shape, "o", dev),
+                               _opt(lse, T * heads_q, _F, "lse", dev), ws.data_ptr(), ws.numel() * ws.element_size(), stream))
     return o, lse
