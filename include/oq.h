@@ -535,6 +535,7 @@ int oq_gemm_w8a8(const int8_t *qa, int64_t lda, const float *a_scale, int64_t M,
  * attention over it.  Heads are bfloat16 vectors of d consecutive elements;
  * element (token t, head h) of a tensor starts at base + t ld + h hs
  * (elements; every start 16-byte aligned, so ld, hs and d multiples of 8).
+ * ld and hs are at least d; heads of an output must not overlap.
  */
 
 /*

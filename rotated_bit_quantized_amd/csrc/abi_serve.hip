@@ -11,15 +11,33 @@ namespace {
 
 inline bool al(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// Whether heads of different tokens and different numbers share elements:
+// |i hs - j ld| < d for some 1 <= i < heads, 1 <= j < T.
+bool heads_overlap(int64_t ld, int64_t hs, int heads, int64_t T, int d) {
+  if (heads < 2 || T < 2) return false;
+  if ((hs - d) / ld >= T - 1 || (ld - d) / hs >= heads - 1) return false;  // one inside the other's stride
+  for (int i = 1; i < heads; ++i) {
+    const __int128 at = (__int128)i * hs, j = at / ld;
+    if (j >= T) break;
+    if (j >= 1 && at - j * ld < d) return true;
+    if (j + 1 < T && (j + 1) * ld - at < d) return true;
+  }
+  return false;
+}
+
 // A tensor of head vectors (T tokens, `heads` heads of d): every head must
-// start 16-byte aligned.
-int check_heads(const char *fn, const char *name, const void *x, int64_t ld, int64_t hs, int heads, int64_t T, int d) {
+// start 16-byte aligned, and those of an output have places of their own.
+int check_heads(const char *fn, const char *name, const void *x, int64_t ld, int64_t hs, int heads, int64_t T, int d,
+                bool out) {
   if (heads == 0 || T == 0) return OQ_OK;
   if (!x) return fail(OQ_ERR_INVALID_ARG, "%s: %s is NULL", fn, name);
   if (ld < 0 || hs < 0) return fail(OQ_ERR_INVALID_ARG, "%s: negative stride of %s", fn, name);
   if ((heads > 1 && hs < d) || (T > 1 && ld < d))
     return fail(OQ_ERR_INVALID_ARG, "%s: strides of %s (token %lld, head %lld) overlap heads of %d", fn, name,
                 (long long)ld, (long long)hs, d);
+  if (out && heads_overlap(ld, hs, heads, T, d))
+    return fail(OQ_ERR_INVALID_ARG, "%s: heads of %s overlap (strides: token %lld, head %lld)", fn, name, (long long)ld,
+                (long long)hs);
   if (!al(x, 16) || (T > 1 && ld % 8) || (heads > 1 && hs % 8))  // the stride over a single one is not used
     return fail(OQ_ERR_ALIGNMENT, "%s: every head of %s must start 16-byte aligned", fn, name);
   return OQ_OK;
@@ -137,10 +155,10 @@ int oq_qk_norm_rope(const uint16_t *q, int64_t q_ld, int64_t q_hs, int32_t heads
   int rc = check_head_width(fn, d);
   if (!rc) rc = check_norm(fn, eps);
   if (!rc) rc = check_rope(fn, rope, pos, T, d);
-  if (!rc) rc = check_heads(fn, "q", q, q_ld, q_hs, heads_q, T, d);
-  if (!rc) rc = check_heads(fn, "k", k, k_ld, k_hs, heads_k, T, d);
-  if (!rc) rc = check_heads(fn, "q_out", q_out, qo_ld, qo_hs, heads_q, T, d);
-  if (!rc) rc = check_heads(fn, "k_out", k_out, ko_ld, ko_hs, heads_k, T, d);
+  if (!rc) rc = check_heads(fn, "q", q, q_ld, q_hs, heads_q, T, d, false);
+  if (!rc) rc = check_heads(fn, "k", k, k_ld, k_hs, heads_k, T, d, false);
+  if (!rc) rc = check_heads(fn, "q_out", q_out, qo_ld, qo_hs, heads_q, T, d, true);
+  if (!rc) rc = check_heads(fn, "k_out", k_out, ko_ld, ko_hs, heads_k, T, d, true);
   if (rc) return rc;
   if (!al(w_q, 4) || !al(w_k, 4)) return fail(OQ_ERR_ALIGNMENT, "%s: norm weights misaligned", fn);
   HeadArgs a;
@@ -167,8 +185,8 @@ int oq_kv_append(const uint16_t *k, int64_t k_ld, int64_t k_hs, const uint16_t *
   rc = check_head_width(fn, d);
   if (!rc) rc = check_norm(fn, eps);
   if (!rc) rc = check_rope(fn, rope, pos, T, d);
-  if (!rc) rc = check_heads(fn, "k", k, k_ld, k_hs, kv->heads, T, d);
-  if (!rc) rc = check_heads(fn, "v", v, v_ld, v_hs, kv->heads, T, d);
+  if (!rc) rc = check_heads(fn, "k", k, k_ld, k_hs, kv->heads, T, d, false);
+  if (!rc) rc = check_heads(fn, "v", v, v_ld, v_hs, kv->heads, T, d, false);
   if (rc) return rc;
   if (T > 0 && !slot) return fail(OQ_ERR_INVALID_ARG, "%s: slot is NULL", fn);
   if (!al(slot, 8) || !al(w_k, 4)) return fail(OQ_ERR_ALIGNMENT, "%s: slot or norm weights misaligned", fn);
@@ -215,8 +233,8 @@ int oq_attn_prefix(const uint16_t *q, int64_t q_ld, int64_t q_hs, int32_t B, int
   if (rc) return rc;
   if (!std::isfinite(scale * ATTN_LOG2E)) return fail(OQ_ERR_INVALID_ARG, "%s: scale log2(e) is not finite", fn);
   const int64_t T = (int64_t)B * n_q;
-  rc = check_heads(fn, "q", q, q_ld, q_hs, heads_q, T, kv->d);
-  if (!rc) rc = check_heads(fn, "o", o, o_ld, o_hs, heads_q, T, kv->d);
+  rc = check_heads(fn, "q", q, q_ld, q_hs, heads_q, T, kv->d, false);
+  if (!rc) rc = check_heads(fn, "o", o, o_ld, o_hs, heads_q, T, kv->d, true);
   if (rc) return rc;
   if (B > 0 && prefix_len > 0 && !prefix_table) return fail(OQ_ERR_INVALID_ARG, "%s: prefix_table is NULL", fn);
   if (B > 0 && table_ld > 0 && (!tables || !lens)) return fail(OQ_ERR_INVALID_ARG, "%s: tables or lens is NULL", fn);
