@@ -36,7 +36,7 @@
 // chunks: HBM, 256 sequences of 512 keys each (537 MB) 106 us, 5.1 TB/s.  Short
 // calls: latency, launch, page numbers, first keys, join; 3 sequences over
 // 777 + 60 keys 9.7 us in all.
-#include "oq_internal.h"
+#include "attn_plan.h"
 
 namespace oq {
 namespace {
@@ -52,29 +52,6 @@ constexpr float LN2 = 0.69314718055994530942f;
 
 // what masked key rows are copied from, so that they cannot put NaN into a product
 __device__ const uint4 g_zero_row[16] = {};
-
-// The prefix's or the suffixes' share of the work.
-struct PartPlan {
-  int suffix;     // 0 prefix (one table, rows of all sequences), 1 suffixes (one sequence per item)
-  int wide;       // 1: a workgroup of 8 wavefronts per item, 0: one wavefront
-  int tiles;      // row tiles per key head (prefix) or per sequence and key head (suffix)
-  int splits;     // chunks of the keys
-  int chunk;      // keys per chunk: a multiple of the key tile and of the page (suffixes: the least)
-  int part0;      // number of the first part
-  int rows;       // B n_q G, rows of one key head
-  int swizzle;    // give each XCD a run of items
-  int64_t items;
-};
-
-// One launch: the workgroups of wide items, then those of one-wavefront items.
-struct Launch {
-  PartPlan part[2];
-  int direct;                           // the only part: no join
-  int lead, wide_items, narrow_items, waves;  // workgroups of narrow items before the wide ones; wavefronts of a workgroup
-  float c;                              // log2(e) |scale|, or 1 where scale == 0
-  uint32_t qxor;                        // on the bits of q pairs: sign of the scale
-  int zero;                             // scale == 0: q is taken as 0, NaN where it is not finite
-};
 
 template <int D>
 __device__ __forceinline__ int swz_k(int row) { return D == 128 ? row & 15 : (row >> 1) & 7; }
@@ -100,7 +77,7 @@ struct Part {
   static constexpr int RING = 2 * GRP;              // tile t of K and of V is in their slot t % RING
   static constexpr int TILE = KT * 2 * D;           // bytes of a K or V tile
   static constexpr int VBASE = NW == 1 ? 0 : RING;  // K slots, then V slots; one wavefront has K in registers
-  static constexpr int PAGES_AT = (VBASE + RING) * TILE, PAGES_MAX = NW == 1 ? 256 : 512;
+  static constexpr int PAGES_AT = (VBASE + RING) * TILE, PAGES_MAX = NW == 1 ? NARROW_PAGES : WIDE_PAGES;
   static constexpr int FLAG = PAGES_MAX - 1;        // place after the most page numbers of a chunk: see hide()
   static constexpr int LDS = PAGES_AT + 4 * PAGES_MAX;
 };
@@ -721,99 +698,6 @@ attn_join_kernel(const AttnArgs a, int rows, int parts, const float *__restrict_
   if (a.lse && lane == 0) a.lse[(int64_t)tok * a.heads_q + h] = m == -INFINITY ? -INFINITY : LN2 * (m + log2f(l));
 }
 
-struct Plan {
-  Launch launch;
-  int rows, parts;
-  int64_t rows_all;
-  bool mixed;
-};
-
-int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
-
-Plan plan_for(const AttnArgs &a) {
-  Plan p{};
-  const int G = a.heads_q / a.kv.heads;
-  p.rows = a.B * a.n_q * G;
-  p.rows_all = (int64_t)p.rows * a.kv.heads;
-  const int64_t cus = device_cus();
-  int64_t keys[2], groups[2];
-  double work[2];
-  for (int s = 0; s < 2; ++s) {
-    PartPlan &q = p.launch.part[s];
-    keys[s] = a.kv.pages == 0 ? 0 : s ? (int64_t)a.table_ld * a.kv.page : a.prefix_len;
-    const int group_rows = s ? a.n_q * G : p.rows;
-    q.suffix = s;
-    q.rows = p.rows;
-    // Wavefronts on their own read a key once per 32 rows, but start at once and
-    // go to every CU; eight that share keys through LDS read them once per 256
-    // rows.  Single ones up to 64 rows, or where 16 a CU with 64 keys each are
-    // enough.  Single against shared: 96 rows of 8 heads over 16384
-    // keys 40.9 us (33.4), over 2000 15.9 (21.1); 160 of 8 over 8000 31.7 (28.4);
-    // 256 of 4 over 2000 17.7 (23.9).
-    const int64_t singles = (int64_t)((group_rows + 31) / 32) * a.kv.heads * (s ? a.B : 1) * ((keys[s] + 63) / 64);
-    q.wide = group_rows > 64 && singles > 16 * cus;
-    q.tiles = (group_rows + (q.wide ? 255 : 31)) / (q.wide ? 256 : 32);
-    groups[s] = (int64_t)q.tiles * a.kv.heads * (s ? a.B : 1);
-    // CU microseconds, as measured: 2.0 (d 128) or 1.1 (d 64) for 64 keys of a
-    // wide item, 4 and 1.9 or 1.2 per 32 keys for eight single wavefronts (used
-    // to share the CUs below); suffixes are taken to fill half of their tables
-    const double k = s ? 0.5 * (double)keys[s] : (double)keys[s];
-    work[s] = keys[s] == 0 ? 0
-              : q.wide     ? (double)groups[s] * k / 64 * (a.kv.d == 128 ? 2.0 : 1.1)
-                           : (double)groups[s] / 8 * (4 + k / 32 * (a.kv.d == 128 ? 1.9 : 1.2));
-  }
-  // Chunks that give every CU a workgroup, or eight single wavefronts.  Where
-  // there are both kinds, either wide items leave the single ones a share of the
-  // CUs, at most a quarter, all in one round; or each kind has all CUs, which
-  // costs a second round's start and end, some 6 us.  One round (measured against
-  // two): 24 x 4 sequences over 5000 + 333 keys 16.3 us (21.2), 40 over 2000 + 50
-  // 22 (33), 40 over 8000 + 100 28 (36).  Two: 64 over 16384 + 2048 156 us (275),
-  // 33 over 2000 + 4000 136 (164).
-  const int w = p.launch.part[0].wide ? 0 : 1;
-  int64_t cus_for[2] = {cus, cus};
-  bool mixed = p.launch.part[0].wide != p.launch.part[1].wide && keys[0] > 0 && keys[1] > 0 && groups[1 - w] / 8 < cus / 2;
-  if (mixed) {
-    const double all = work[0] + work[1], share = work[w] < 0.75 * all ? 0.75 : work[w] / all;
-    const double wide_us = work[w] / (share * (double)cus), narrow_us = work[1 - w] / ((1 - share) * (double)cus);
-    mixed = (wide_us > narrow_us ? wide_us : narrow_us) < 6 + all / (double)cus;
-    if (mixed) cus_for[w] = (int64_t)((double)cus * share);
-  }
-  p.mixed = mixed;
-  for (int i = 0; i < 2; ++i) {
-    const int s = i ? 1 - w : w;  // wide items first
-    PartPlan &q = p.launch.part[s];
-    if (keys[s] == 0) continue;
-    const int64_t unit = a.kv.page > 64 ? a.kv.page : 64;  // a part of fewer keys costs more than reading them
-    int64_t splits = (cus_for[s] * (q.wide ? 1 : 8) + (mixed ? groups[s] / 2 : 0)) / groups[s];
-    if (q.wide && splits > 1 && splits * groups[s] > cus) --splits;
-    // Two wavefronts a CU nearly fill the memory's bandwidth; more are for
-    // chunks of 256 keys at least, as each costs a partial O.  One sequence of 8
-    // heads x 4 over 16384 keys: 64 chunks 20 us, 256 24; 16 of them with 8000
-    // keys each: 16 chunks 105 us, 4 121.
-    if (!q.wide && !mixed) {
-      const int64_t two = 2 * cus / groups[s], most = keys[s] / 256;
-      if (splits > most) splits = most;
-      if (splits < two) splits = two;
-    }
-    if (splits < 1) splits = 1;
-    int64_t chunk = round_up((keys[s] + splits - 1) / splits, unit);
-    const int64_t pages = q.wide ? Part<64, 8>::PAGES_MAX : Part<64, 1>::PAGES_MAX;
-    const int64_t most = (pages - 1) * a.kv.page / unit * unit;
-    if (chunk > most) chunk = most;
-    q.splits = (int)((keys[s] + chunk - 1) / chunk);
-    q.chunk = (int)(s ? unit : chunk);
-    q.items = groups[s] * q.splits;
-    if (mixed && q.wide && q.items < cus) cus_for[1 - s] = cus - q.items;
-  }
-  p.launch.part[1].part0 = p.launch.part[0].splits;
-  p.parts = p.launch.part[0].splits + p.launch.part[1].splits;
-  // one part alone writes the output: 64 sequences of up to 60 own keys 7.5 us (10.2
-  // with a join), 256 of up to 512 54.5 (60.4),
-  // 2048 tokens of 32 heads among themselves 68 (94)
-  p.launch.direct = p.parts == 1;
-  return p;
-}
-
 template <int D>
 hipError_t launch_d(const AttnArgs &a, Plan &p, float *po, float2 *pm, hipStream_t stream) {
   Launch &lp = p.launch;
@@ -851,11 +735,6 @@ hipError_t launch_d(const AttnArgs &a, Plan &p, float *po, float2 *pm, hipStream
 }
 
 }  // namespace
-
-size_t attn_prefix_ws(const AttnArgs &a) {
-  const Plan p = plan_for(a);
-  return p.launch.direct ? 0 : (size_t)p.parts * (size_t)p.rows_all * ((size_t)a.kv.d * 4 + 8);
-}
 
 hipError_t launch_attn_prefix(const AttnArgs &a, void *ws, hipStream_t stream) {
   Plan p = plan_for(a);

@@ -4,7 +4,7 @@ import ctypes
 import pytest
 
 import rotated_bit_quantized_amd as oq
-from test_serve_cpu import AT, INV, QK, UNS, _call, _kv
+from test_serve_cpu import AT, INV, QK, UNS, WS, _call, _kv
 
 
 @pytest.mark.parametrize("B,n_q,heads_q", [(1 << 22, 1 << 21, 1 << 21), (1 << 30, 1 << 30, 8), ((1 << 31) - 1, (1 << 31) - 1, (1 << 31) - 8),
@@ -32,3 +32,11 @@ def test_outputs_that_overlap_are_refused(ld, hs):
     assert _call("oq_qk_norm_rope", QK, dict(qo_ld=ld, qo_hs=hs)) == INV
     assert _call("oq_qk_norm_rope", QK, dict(ko_ld=ld, ko_hs=hs)) == INV
     assert _call("oq_attn_prefix", AT, dict(B=10, o_ld=ld, o_hs=hs)) == INV
+
+
+@pytest.mark.parametrize("short", ["none", "empty", "one byte"])
+def test_attn_prefix_workspace_too_small(short):
+    need = oq.lib().oq_attn_prefix_ws_bytes(4, 1, 32, _kv(), 60, 2)
+    assert need > 0
+    change = dict(ws=None) if short == "none" else dict(ws_bytes=0 if short == "empty" else need - 1)
+    assert _call("oq_attn_prefix", AT, change) == WS
