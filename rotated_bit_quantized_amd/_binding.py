@@ -143,8 +143,18 @@ def _current(t: torch.Tensor, what: str):
     if not t.is_cuda:  # before the runtime is asked
         raise OQError(OQ_ERR_INVALID_ARG, f"{what} must live on the GPU")
     dev = torch.cuda.current_device()
-    _on(t, dev, what)
+    if t.get_device() != dev:
+        _on(t, dev, what)
     return dev, _raw_stream(dev)
+
+
+_MAX = 0x7FFFFFFF  # the library takes most sizes in 32 bits, and ctypes would pass the remainder of larger ones
+
+
+def _small(*sizes):
+    for n in sizes:
+        if not -_MAX <= n <= _MAX:
+            raise OQError(OQ_ERR_UNSUPPORTED, f"a size does not fit 32 bits: {sizes}")
 
 
 def _vec(t: torch.Tensor, n: int, dtype, what: str, dev: int):
@@ -631,6 +641,7 @@ def oq_quant_weight_w8(w, rot: Optional[Rotation] = None, codes=None, scales=Non
     if w.dim() != 2 or w.dtype != torch.float32 or w.stride(1) != 1:
         raise OQError(OQ_ERR_INVALID_ARG, "w must be a float32 matrix with unit column stride")
     N, K = w.shape
+    _small(N, K)
     on, stream = _current(w, "w")
     dev = w.device
     for t in () if rot is None else (rot.perm, rot.signs, rot.mats):
@@ -660,8 +671,11 @@ def oq_gemm_w8a8(qa, a_scale, w, w_scale, mean=None, w1=None, bias=None, y=None)
     (lda, ca), (ldw, cw) = qa.stride(), w.stride()
     if K != Kw or ca != 1 or cw != 1:
         raise OQError(OQ_ERR_INVALID_ARG, f"qa [M][K] and w [N][K] with unit column strides, got {qa.shape} and {w.shape}")
+    if K > _MAX or N > _MAX:
+        _small(K, N)
     dev, stream = _current(qa, "qa")
-    _on(w, dev, "w")
+    if w.get_device() != dev:
+        _on(w, dev, "w")
     if y is None:
         y = torch.empty((M, N), dtype=torch.bfloat16, device=qa.device)
     elif y.dtype not in _BF16 or y.dim() != 2 or y.shape[0] < M or y.shape[1] < N:
@@ -669,7 +683,8 @@ def oq_gemm_w8a8(qa, a_scale, w, w_scale, mean=None, w1=None, bias=None, y=None)
     ldy, cy = y.stride()
     if cy != 1:
         _out_y(y, M, N, qa.device)
-    _on(y, dev, "y")
+    if y.get_device() != dev:
+        _on(y, dev, "y")
     # a matrix of one row has no row stride to speak of
     _check(_lib.oq_gemm_w8a8(qa.data_ptr(), lda if M > 1 else (K + 15) // 16 * 16, _vec(a_scale, M, _F, "a_scale", dev), M, K,
                              w.data_ptr(), ldw if N > 1 else (K + 15) // 16 * 16, _vec(w_scale, N, _F, "w_scale", dev), N,
@@ -697,6 +712,7 @@ class Rope:
             raise OQError(OQ_ERR_INVALID_ARG, "cos and sin must be matrices of one shape")
         for t, what in ((cos, "cos"), (sin, "sin")):
             _need(t, 0, what, _F32)
+        _small(2 * cos.shape[1])
         self.dev = cos.get_device()
         _on(sin, self.dev, "sin")
         self.cos, self.sin, self.interleaved = cos, sin, interleaved
@@ -718,6 +734,7 @@ class PagedKV:
         if k.shape != v.shape or k.stride() != v.stride() or v.get_device() != self.dev:
             raise OQError(OQ_ERR_INVALID_ARG, "k and v must have one shape, stride and device")
         self.k, self.v = k, v
+        _small(*k.shape)
         self.pages, self.heads, self.page, self.d = k.shape
         self.c = oq_kv(k.data_ptr(), v.data_ptr(), k.stride(0), self.pages, self.page, self.heads, self.d)
         self.ref = ctypes.byref(self.c)
@@ -732,7 +749,8 @@ def _handle(h, dev: int, what: str):
 
 def _heads(t: torch.Tensor, shape, what: str, dev: int):
     """(address, token stride, head stride) of a bfloat16 tensor [T][heads][d] on GPU `dev`."""
-    _on(t, dev, what)
+    if t.get_device() != dev:
+        _on(t, dev, what)
     if t.shape != shape or t.dtype not in _BF16:
         raise OQError(OQ_ERR_INVALID_ARG, f"{what} must be a GPU bfloat16 tensor of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     ld, hs, es = t.stride()
@@ -757,7 +775,9 @@ def oq_qk_norm_rope(q, k, w_q=None, w_k=None, eps: float = 1e-6, rope: Optional[
     x = q if q is not None else k
     if x is None:
         raise OQError(OQ_ERR_INVALID_ARG, "q or k is required")
-    T, _, d = _tokens(x, "q" if q is not None else "k")
+    T, heads, d = _tokens(x, "q" if q is not None else "k")
+    if heads > _MAX or d > _MAX or (k is not None and _tokens(k, "k")[1] > _MAX):
+        raise OQError(OQ_ERR_UNSUPPORTED, "head counts and widths past 32 bits")
     dev, stream = _current(x, "q" if q is not None else "k")
     args = [None, 0, 0, 0, None, 0, 0, 0]
     outs = [None, 0, 0, None, 0, 0]
@@ -767,7 +787,7 @@ def oq_qk_norm_rope(q, k, w_q=None, w_k=None, eps: float = 1e-6, rope: Optional[
         args[0:4] = *_heads(q, shape, "q", dev), shape[1]
         outs[0:3] = _heads(q_out, shape, "q_out", dev)
     if k is not None:
-        shape = _tokens(k, "k")
+        shape = k.shape
         if shape[0] != T or shape[2] != d:
             raise OQError(OQ_ERR_INVALID_ARG, f"q and k differ: {tuple(x.shape)}, {tuple(shape)}")
         k_out = torch.empty(shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
@@ -790,6 +810,7 @@ def oq_kv_append(k, v, slot, kv: PagedKV, w_k=None, eps: float = 1e-6, rope: Opt
 
 
 def oq_attn_prefix_ws_bytes(B: int, n_q: int, heads_q: int, kv: PagedKV, prefix_len: int, table_ld: int) -> int:
+    _small(B, n_q, heads_q, prefix_len, table_ld)
     return int(_lib.oq_attn_prefix_ws_bytes(B, n_q, heads_q, kv.ref, prefix_len, table_ld))
 
 
@@ -803,12 +824,16 @@ def oq_attn_prefix(q, n_q: int, kv: PagedKV, prefix_table, prefix_len: int, tabl
     if n_q < 1 or T % n_q or d != kv.d:
         raise OQError(OQ_ERR_INVALID_ARG, f"q of shape {tuple(shape)} for n_q={n_q} and heads of {kv.d}")
     B = T // n_q
+    if T > _MAX or heads_q > _MAX or prefix_len > _MAX:
+        _small(B, n_q, heads_q, prefix_len)
     dev, stream = _current(q, "q")
     table_ld, table_at, lens_at = 0, None, None
     if tables is not None:
         if tables.dim() != 2 or tables.shape[0] != B:
             raise OQError(OQ_ERR_INVALID_ARG, f"tables must be a matrix of {B} rows")
         table_ld = tables.shape[1]
+        if table_ld > _MAX:
+            _small(table_ld)
         table_at, lens_at = _vec(tables, 0, _I32, "tables", dev), _vec(lens, B, _I32, "lens", dev)
     if o is None:
         o = torch.empty(shape, dtype=q.dtype, device=q.device)

@@ -26,7 +26,7 @@ def test_import_without_the_raw_stream_symbol():
 
 
 class OnGpu(torch.Tensor):
-    """A host tensor that says it lives on GPU `where`."""
+    """A tensor without memory that says it lives on GPU `where`."""
 
     where = 0
     is_cuda = property(lambda self: self.where >= 0)
@@ -36,7 +36,7 @@ class OnGpu(torch.Tensor):
 
 
 def gpu(*shape, dtype=torch.bfloat16, where=0):
-    t = torch.zeros(*shape, dtype=dtype).as_subclass(OnGpu)
+    t = torch.empty(*shape, dtype=dtype, device="meta").as_subclass(OnGpu)
     t.where = where
     return t
 
@@ -53,6 +53,8 @@ TENSORS = {  # entry point: its tensor arguments, as (shape, dtype)
     "oq_attn_prefix": dict(q=((4, 2, 64),), k_cache=((5, 1, 16, 64),), v_cache=((5, 1, 16, 64),), prefix_table=((2,), I32),
                            tables=((4, 1), I32), lens=((4,), I32), o=((4, 2, 64),), lse=((4, 2), F32), ws=((1 << 20,), U8)),
 }
+
+SCALARS = {"oq_attn_prefix": dict(n_q=1, prefix_len=20, scale=0.1)}
 
 
 def _call(entry, where, monkeypatch):
@@ -72,9 +74,7 @@ def _call(entry, where, monkeypatch):
         t["rope"] = oq.Rope(t.pop("cos"), t.pop("sin"))
     if "k_cache" in t:
         t["kv"] = oq.PagedKV(t.pop("k_cache"), t.pop("v_cache"))
-    if entry == "oq_attn_prefix":
-        t.update(n_q=1, prefix_len=20, scale=0.1)
-    getattr(oq, entry)(**t)
+    getattr(oq, entry)(**t, **SCALARS.get(entry, {}))
     return reached
 
 
@@ -96,3 +96,45 @@ def test_every_tensor_has_to_live_on_the_current_gpu(entry, name, where, monkeyp
 def test_a_whole_handle_of_another_gpu(entry, pair, monkeypatch):
     with pytest.raises(oq.OQError):
         _call(entry, dict.fromkeys(pair, 1), monkeypatch)
+
+
+HUGE = (1 << 32) + 64  # 64 in 32 bits
+LARGE = {
+    "oq_quant_weight_w8": [dict(w=((1, HUGE), F32), codes=((1, HUGE), I8)), dict(w=((HUGE, 64), F32), codes=((HUGE, 64), I8), scales=((HUGE,), F32), w1=((HUGE,), F32))],
+    "oq_gemm_w8a8": [dict(qa=((4, HUGE), I8), w=((8, HUGE), I8)),
+                     dict(w=((HUGE, 64), I8), w_scale=((HUGE,), F32), w1=((HUGE,), F32), bias=((HUGE,), F32), y=((4, HUGE), torch.bfloat16))],
+    "oq_qk_norm_rope": [dict(q=((4, HUGE, 64),), q_out=((4, HUGE, 64),)), dict(k=((4, HUGE, 64),), k_out=((4, HUGE, 64),)),
+                        {n: (s[:-1] + (HUGE,),) for n, s in dict(q=(4, 2, 0), k=(4, 1, 0), q_out=(4, 2, 0), k_out=(4, 1, 0)).items()}
+                        | dict(w_q=((HUGE,), F32), w_k=((HUGE,), F32))],
+    "oq_kv_append": [dict(k=((4, HUGE, 64),), v=((4, HUGE, 64),), k_cache=((5, HUGE, 16, 64),), v_cache=((5, HUGE, 16, 64),)),
+                     dict(k_cache=((HUGE, 1, 16, 64),), v_cache=((HUGE, 1, 16, 64),)), dict(cos=((9, HUGE // 2), F32), sin=((9, HUGE // 2), F32))],
+    "oq_attn_prefix": [dict(prefix_len=HUGE, prefix_table=((HUGE // 16,), I32)), dict(tables=((4, HUGE), I32)),
+                       dict(q=((4, HUGE, 64),), o=((4, HUGE, 64),), lse=((4, HUGE), F32)), dict(n_q=HUGE, q=((HUGE, 2, 64),), o=((HUGE, 2, 64),), tables=((1, 1), I32), lens=((1,), I32), lse=((HUGE, 2), F32)),
+                       dict(q=((HUGE, 2, 64),), o=((HUGE, 2, 64),), tables=((HUGE, 1), I32), lens=((HUGE,), I32), lse=((HUGE, 2), F32))],
+}
+
+
+@pytest.mark.parametrize("entry,n", [(e, n) for e, a in LARGE.items() for n in range(len(a))])
+def test_sizes_past_32_bits_are_refused(entry, n, monkeypatch):
+    """The library's sizes are 32 bits: what they cannot hold must not arrive as its remainder."""
+    change = dict(LARGE[entry][n])
+    scalars = {k: change.pop(k) for k in list(change) if not isinstance(change[k], tuple)}
+    monkeypatch.setitem(TENSORS, entry, {**TENSORS[entry], **change})
+    monkeypatch.setitem(SCALARS, entry, {**SCALARS.get(entry, {}), **scalars})
+    with pytest.raises(oq.OQError):
+        _call(entry, {}, monkeypatch)
+
+
+@pytest.mark.parametrize("at", range(5))
+def test_workspace_sizes_past_32_bits_are_refused(at, monkeypatch):
+    args = [4, 1, 32, 60, 2]
+    args[at] = HUGE
+    kv = oq.PagedKV(gpu(5, 1, 16, 64), gpu(5, 1, 16, 64))
+    with pytest.raises(oq.OQError):
+        oq.oq_attn_prefix_ws_bytes(*args[:3], kv, *args[3:])
+
+
+def test_keys_of_another_rank_are_refused(monkeypatch):
+    monkeypatch.setitem(TENSORS, "oq_qk_norm_rope", {**TENSORS["oq_qk_norm_rope"], "k": ((64,),)})
+    with pytest.raises(oq.OQError):
+        _call("oq_qk_norm_rope", {}, monkeypatch)
