@@ -520,7 +520,7 @@ int oq_quant_weight_w8(const float *w, int32_t N, int32_t K, int64_t ldw, const 
  *   acc = exact int32 sum over K, converted to float32 with one rounding.
  * qa int8 [M][lda]; a_scale float32 [M]; w int8 [N][ldw]; w_scale float32 [N];
  * mean and w1 both NULL or both set; bias nullable; y bf16 [M][ldy].
- * Any M, N >= 0 (zero enqueues nothing); K a multiple of 16, 16 <= K <=
+ * 0 <= M <= 2^30, any N >= 0 (zero enqueues nothing); K a multiple of 16, 16 <= K <=
  * 131056 (the int32 sum cannot overflow, codes of -128 included); lda, ldw
  * multiples of 16, at most 2^23; qa and w 16-byte aligned.  No scratch.  The result does
  * not depend on the tile that the library picks from M, N, K and the CU count.
@@ -626,7 +626,10 @@ int oq_attn_prefix(const uint16_t *q, int64_t q_ld, int64_t q_hs, int32_t B, int
                    float *lse, void *ws, size_t ws_bytes, hipStream_t stream);
 
 /* Scratch bytes of oq_attn_prefix (0 for arguments it refuses).  Pure host
- * function of the sizes and the device's CU count. */
+ * function of the sizes and the device's CU count.  It does not grow with the
+ * arguments: the number of parts follows from how the work fills the CUs, so a
+ * shorter prefix can take more than a longer one.  A caller whose sizes change
+ * asks for each, or keeps the largest of those that come. */
 size_t oq_attn_prefix_ws_bytes(int32_t B, int32_t n_q, int32_t heads_q, const oq_kv *kv, int32_t prefix_len,
                                int32_t table_ld);
 

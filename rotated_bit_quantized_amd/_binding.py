@@ -810,6 +810,7 @@ def oq_kv_append(k, v, slot, kv: PagedKV, w_k=None, eps: float = 1e-6, rope: Opt
 
 
 def oq_attn_prefix_ws_bytes(B: int, n_q: int, heads_q: int, kv: PagedKV, prefix_len: int, table_ld: int) -> int:
+    """Scratch bytes of one call; a shorter prefix can take more than a longer one."""
     _small(B, n_q, heads_q, prefix_len, table_ld)
     return int(_lib.oq_attn_prefix_ws_bytes(B, n_q, heads_q, kv.ref, prefix_len, table_ld))
 

@@ -346,7 +346,7 @@ struct HeadArgs {
   const int32_t *pos = nullptr;
   const int64_t *slot = nullptr;  // set: outputs go to the slots of a cache of these dimensions
   int64_t page_stride = 0, slots = 0;
-  int page_log2 = 0, cache_heads = 0;
+  int page_log2 = 0;
 };
 hipError_t launch_heads(const HeadArgs &a, hipStream_t stream);
 
