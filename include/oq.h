@@ -615,7 +615,7 @@ int oq_kv_append(const uint16_t *k, int64_t k_ld, int64_t k_hs, const uint16_t *
  * float32.  A row's bits do not depend on the contents of other rows.
  * The prefix is read once for all rows of a tile; scores, statistics and sums
  * are float32; softmax numerators enter the value product as bfloat16 (their
- * sum is of the float32 values).
+ * sum is of the float32 values), an error of about the output's own rounding.
  * d (kv->d) 64 or 128; heads_q a multiple of kv->heads; scale log2(e) finite.
  * ws: device scratch of oq_attn_prefix_ws_bytes(B, n_q, heads_q, kv,
  * prefix_len, table_ld) bytes, 16-byte aligned (may be 0).

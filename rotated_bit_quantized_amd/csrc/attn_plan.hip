@@ -43,9 +43,8 @@ Plan plan_for(const AttnArgs &a) {
   // there are both kinds, either wide items leave the single ones a share of the
   // CUs, at most a quarter, all in one round; or each kind has all CUs, which
   // costs a second round's start and end, some 6 us.  One round (measured against
-  // two): 24 x 4 sequences over 5000 + 333 keys 16.3 us (21.2), 40 over 2000 + 50
-  // 22 (33), 40 over 8000 + 100 28 (36).  Two: 64 over 16384 + 2048 156 us (275),
-  // 33 over 2000 + 4000 136 (164).
+  // two): 24 x 4 sequences over 5000 + 333 keys 24.5 us (28.9), 40 over 8000 + 100
+  // 28 (40).  Two (against one): 64 over 16384 + 2048 152 us (244).
   const int w = p.launch.part[0].wide ? 0 : 1;
   int64_t cus_for[2] = {cus, cus};
   bool mixed = p.launch.part[0].wide != p.launch.part[1].wide && keys[0] > 0 && keys[1] > 0 && groups[1 - w] / 8 < cus / 2;

@@ -22,10 +22,16 @@
 // (one exchange between the lane's halves), and P^T leaves the first product
 // in the layout that the second takes, up to an order of the keys that the
 // V^T fragments (transposing LDS reads) follow.  The scale is applied to the
-// float32 scores; P is rounded to bfloat16 for the second product, its sum l
-// is not.  O is rescaled only when a row's maximum has grown by more than
-// 2^8 since the last time (P then stays below 2^8, which costs float32 and
-// bfloat16 no precision).
+// float32 scores; P is rounded to bfloat16 for the second product, which takes
+// both operands in V's type, its sum l is not.  That is the one place with fewer
+// than 32 bits before the output's own rounding, and costs about as much as that:
+// off by 0.0022 to 0.0024 of the norm against 64 bits, 0.0017 with P as two
+// bfloat16 terms (and for exact results rounded once).  Two terms are half as
+// many products again: 256 sequences over 32768 + 512 keys 214 -> 268 us, 8192
+// tokens among themselves 556 -> 759.
+// O is rescaled only when a row's maximum has grown by more than 2^8 since the
+// last time (P then stays below 2^8, which costs float32 and bfloat16 no
+// precision).
 //
 // What bounds it.  Wide items: the matrix and the vector unit together, a
 // score costs 4 D operations on the one and an exponential, a fused multiply
@@ -33,9 +39,9 @@
 // every wavefront reads every K and V byte from LDS, at a clock that the power
 // limits; 1024 rows of 8 heads over 32768 keys with D = 128 take 145 us, 0.95
 // PFLOP/s (a large bf16 product of the library: 1.23).  Narrow items with long
-// chunks: HBM, 256 sequences of 512 keys each (537 MB) 106 us, 5.1 TB/s.  Short
+// chunks: HBM, 16 sequences of 8000 keys each (524 MB) 103 us, 5.1 TB/s.  Short
 // calls: latency, launch, page numbers, first keys, join; 3 sequences over
-// 777 + 60 keys 9.7 us in all.
+// 777 + 60 keys 9.8 us in all.
 #include "attn_plan.h"
 
 namespace oq {
@@ -112,7 +118,7 @@ __device__ __forceinline__ void part_body(const AttnArgs &a, const Launch &lp, c
   // keys (the row tiles of one chunk) are consecutive, so give each XCD a run.
   if (p.swizzle) item = (item & 7) * (int)(p.items >> 3) + (item >> 3);
   // A suffix's last rows see the most keys: they go first, so that what ends last
-  // is short (8192 tokens among themselves 602 -> 537 us, 4096 180 -> 146).
+  // is short (8192 tokens among themselves 602 -> 537 us, 4096 180 -> 146, before hide() below).
   const int tile = p.suffix ? p.tiles - 1 - item % p.tiles : item % p.tiles;
   item /= p.tiles;
   const int split = item % p.splits;
@@ -617,7 +623,7 @@ __device__ __forceinline__ float wave_all(float v, F f) {
 // parts: 20 us with the parts' kernel, 28 with a wavefront a row.  96 rows, 14
 // parts: 3.8 us against 5.6 without the early loads.  Where there are many rows
 // the traffic counts, and parts without keys are not read (WAVES = 0): 8192 rows
-// 10.3 us, 11.4 with early loads.
+// 9.7 us, 11.4 with early loads.
 template <int D, int WAVES>
 __global__ void __launch_bounds__(256)
 attn_join_kernel(const AttnArgs a, int rows, int parts, const float *__restrict__ part_o, const float2 *__restrict__ part_ml) {

@@ -18,11 +18,12 @@
 // MFMAs of the current ones.
 //
 // What bounds it.  The 256 x 256 tile: the matrix unit at the clock that the
-// operands' bits allow, 8192 x 4096 -> 14336 takes 434 us, 2.2 POP/s (a large
-// int8 product of the library: 2.16; the instruction alone 4.7).  The smaller
+// operands' bits allow, 8192 x 4096 -> 14336 takes 432 to 463 us on one card and
+// another, 2.1 to 2.2 POP/s (a large int8 product of the library: 2.16; the
+// instruction alone 4.7).  The smaller
 // tiles: copies into LDS (64 bytes a clock and CU, so 556 clocks for a stage of
 // the 128 x 128 tile against 512 of products) and products overlap to seven
-// tenths; 512 x 4096 -> 4096 takes 16.5 us, 333 x 1920 -> 7680 10.5.
+// tenths; 512 x 4096 -> 4096 takes 16.8 us, 333 x 1920 -> 7680 10.4.
 #include "oq_internal.h"
 
 namespace oq {
@@ -307,9 +308,11 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW / 4 * C::RESIDENT) gemm_w8a8
 // per wavefront; the activations, which every workgroup reads, go through LDS in
 // chunks of as many k as fit, sent before the first weight loads and with each
 // row's 16-byte pieces permuted by the row against bank conflicts.  The
-// wavefronts' int32 sums meet in LDS.  Measured: 1 x 4096 x 6144 7.7 us (batches
-// of 4 7.8, of 8 11), 16 x 1920 x 7680 6.1 (7.3, 10.8), 32 x 4096 x 14336 19.7
-// (3.0 TB/s of weights).
+// wavefronts' int32 sums meet in LDS.  Measured: 1 x 4096 x 6144 7.8 us (batches
+// of 4 7.8, of 8 11), 16 x 1920 x 7680 5.8 (7.3, 10.8), 32 x 4096 x 14336 19.8
+// (3.0 TB/s of weights).  A chunk's copies and first weights start when the last
+// one has been used, and the epilogue's vectors are asked for after the sums have
+// met: both are trips to memory that nothing hides.
 template <int MT>
 __global__ void __launch_bounds__(512) gemm_w8a8_rows(const GemmArgs g, const int CH) {
   constexpr int NW = 8, DEPTH = 2;
@@ -444,8 +447,10 @@ hipError_t launch_gemm_w8a8(const int8_t *qa, int64_t lda, const float *a_scale,
   if (M <= 16 || nt * ((M + 15) / 16) <= cus) return launch_rows<1>(g, stream);
   if (M <= 32) return launch_rows<2>(g, stream);
   // The tile with the least modelled time, rounds of workgroups over the CUs
-  // times the measured time of a round at K = 4096 (us; K scales all alike):
-  // 256 x 256 59, 128 x 256 34, 128 x 128 22, 64 x 64 7.3 and 4 for the first.
+  // times the measured time of a round at K = 4096 (us): 256 x 256 59, 128 x 256
+  // 34, 128 x 128 22, 64 x 64 7.3 and 4 for the first.  K scales a round, not the
+  // fixed part of a call, so the choice is the measured one at K = 4096 and is
+  // taken for every K.
   // Measured with K = 4096, N = 4096: 512 tokens 42.7 / 25.6 / 19.4 / 16.3, 1024
   // 44.2 / 28.5 / 22.1 / 30, 2048 47.4 / 36.2 / 40.6, 4096 63.4 / 67.4 / 77.4;
   // 1952 x 13984 x 8705 419 / 396 / 431 / 613.

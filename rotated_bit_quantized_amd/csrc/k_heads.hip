@@ -12,8 +12,8 @@
 // used, and the token's cos and sin, four times the bytes of a head, are
 // loaded once for all of them.  A workgroup is 256 / L tokens of the same
 // heads, so which tensor and which heads is scalar.
-// Measured: 32768 tokens of 32 + 8 heads of 128 142 us, 4.8 TB/s (a large copy:
-// 5.2); into the cache, 8 + 8 heads, 65.5 us, 4.4 TB/s.
+// Measured: 32768 tokens of 32 + 8 heads of 128 145 us, 4.8 TB/s (a large copy:
+// 5.2); into the cache, 8 + 8 heads, 66 us, 4.3 TB/s.
 #include "oq_internal.h"
 
 namespace oq {
