@@ -28,7 +28,7 @@
 // off by 0.0022 to 0.0024 of the norm against 64 bits, 0.0017 with P as two
 // bfloat16 terms (and for exact results rounded once).  Two terms are half as
 // many products again: 256 sequences over 32768 + 512 keys 214 -> 268 us, 8192
-// tokens among themselves 556 -> 759.
+// tokens among themselves 568 -> 763.
 // O is rescaled only when a row's maximum has grown by more than 2^8 since the
 // last time (P then stays below 2^8, which costs float32 and bfloat16 no
 // precision).
