@@ -634,6 +634,170 @@ size_t oq_attn_prefix_ws_bytes(int32_t B, int32_t n_q, int32_t heads_q, const oq
                                int32_t table_ld);
 
 /*
+ * The feed-forward half of a sparse (mixture-of-experts) layer on int8 codes,
+ * and the answer behind the last layer: routing, the experts' products, the
+ * residual stream with its norms, log probabilities.  An entry i = t k + j is
+ * the j-th choice of token t; entries are the rows of everything that the
+ * experts compute.
+ */
+
+/* element types of logits and of the residual stream */
+enum { OQ_F32 = 1, OQ_BF16 = 2 };
+
+/* scores of a router */
+enum { OQ_SCORE_SOFTMAX = 1, OQ_SCORE_SIGMOID = 2 };
+
+/*
+ * A router (host struct, bias device float32 [experts] or NULL).  For the
+ * logits l of a token: s = softmax(l) or sigmoid(l), element by element;
+ *   c = s + bias (without a bias experts are compared by l itself);
+ *   the experts lie in `groups` equal runs; a run's score is the sum of its
+ *   group_best (1 or 2) best c (without a bias: of the best l, or of the two best
+ *   s), and the top_groups best runs are open (groups 1: all);
+ *   chosen are the k best c of the open runs, in falling order;
+ *   weight = factor s, divided by the sum of the chosen s if renorm is not 0.
+ * Equal ones go to the lowest index, runs and experts alike.  Choices are those
+ * of the exact values: where float32 cannot tell neighbours apart, float64
+ * decides.  A NaN ranks below all numbers (in a run's score it counts as -inf);
+ * ids are valid whatever the logits hold, weights follow the formula.
+ * 1 <= experts <= 1024 (512 with groups); groups <= 64 divides experts; group_best <= experts /
+ * groups; 1 <= k <= 32, k <= top_groups experts / groups; factor finite.
+ */
+typedef struct {
+  const float *bias;
+  int32_t experts;
+  int32_t k;
+  int32_t score;
+  int32_t groups;
+  int32_t top_groups;
+  int32_t group_best;
+  int32_t renorm;
+  float factor;
+} oq_router;
+
+/*
+ * oq_route -- logits [T][ld] (dtype OQ_F32 or OQ_BF16, ld >= experts) to
+ * ids int32 [T][k], weights float32 [T][k] and, where offsets and order are
+ * given (both or neither), the lists that oq_gemm_w8a8_experts reads: order
+ * int32 [T k] holds the entries by expert, those of one expert in rising
+ * order, expert e's at offsets[e] .. offsets[e + 1] - 1 (int32 [experts + 1]).
+ * mask uint8 [T] (nullable): a token of 0 gets ids -1 and weights 0 and is in
+ * no list; places of order behind offsets[experts] get -1.
+ * T k <= 2^30.  ws: device scratch of oq_route_ws_bytes(T, r) bytes, 16-byte
+ * aligned (not read without lists; may be 0).
+ */
+int oq_route(const void *logits, int dtype, int64_t ld, int64_t T, const uint8_t *mask, const oq_router *r, int32_t *ids,
+             float *weights, int32_t *offsets, int32_t *order, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* Scratch bytes of oq_route (0 for arguments it refuses).  Pure host function. */
+size_t oq_route_ws_bytes(int64_t T, const oq_router *r);
+
+/* what the experts' product does with its outputs */
+enum { OQ_ACT_NONE = 0, OQ_ACT_SWIGLU = 1 };
+
+/*
+ * oq_gemm_w8a8_experts -- the product of oq_gemm_w8a8 for every entry with the
+ * weights of its expert: for entry i = order[p], offsets[e] <= p < offsets[e + 1],
+ * on activation row i / per,
+ *   v[o] = a_scale[row] * w_scale[e][o] * acc + mean[row] * w1[e][o] + bias[e][o]
+ *   y[i][o] = bf16_RNE(v[o])                                  OQ_ACT_NONE, N outputs
+ *   y[i][o] = bf16_RNE(v[o] / (1 + exp(-v[o])) * v[N/2 + o])  OQ_ACT_SWIGLU, N/2 outputs
+ * (N even; the first half of the weight rows is the gate).
+ * per = k: entries of a token share its activation row (up projections); per =
+ * 1: every entry has a row of its own (down projections).
+ * qa int8 [rows][lda], a_scale and mean float32 [rows]; w int8 [E][N][ldw], an
+ * expert's rows w_stride bytes behind the last one's; w_scale, w1, bias float32
+ * [E][N]; mean and w1 both NULL or both set, bias nullable; offsets int32 [E + 1]
+ * and order int32 [n] as from oq_route; y bf16 [n][ldy].
+ * An entry may be in the lists once; rows of y whose entry is in no list stay
+ * as they are.  List values outside their range are ignored (offsets are cut to
+ * 0 .. n, an order outside 0 .. n - 1 has no row).
+ * 0 <= n <= 2^30, per >= 1, rows >= ceil(n / per); 1 <= E <= 1024; K, lda, ldw,
+ * alignment as oq_gemm_w8a8, w_stride a multiple of 16 and at least N ldw.
+ * N <= 2^20.  No scratch.  A row's bits do not depend on the other entries.
+ */
+int oq_gemm_w8a8_experts(const int8_t *qa, int64_t lda, const float *a_scale, int64_t rows, int32_t K, const int8_t *w,
+                         int64_t ldw, int64_t w_stride, const float *w_scale, int32_t N, int32_t E,
+                         const int32_t *offsets, const int32_t *order, int64_t n, int32_t per, int act,
+                         const float *mean, const float *w1, const float *bias, uint16_t *y, int64_t ldy,
+                         hipStream_t stream);
+
+/*
+ * A norm over the d elements of a row (host struct; w, b device float32 [d] or
+ * NULL):  OQ_NORM_RMS    x / sqrt(mean(x^2) + eps) * w + b
+ *         OQ_NORM_LAYER  (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps) * w + b
+ */
+enum { OQ_NORM_RMS = 1, OQ_NORM_LAYER = 2 };
+typedef struct {
+  const float *w;
+  const float *b;
+  int32_t kind;
+  float eps;
+} oq_norm;
+
+/*
+ * Modulation (host struct, device arrays): gate, scale, shift bfloat16
+ * [rows][ld] (each nullable; they may be columns of one table); token t uses
+ * row row[t] (int32 [T]; NULL: row 0 of a single one, else row t).  A row
+ * outside [0, rows) gives NaN in that token's outputs.
+ */
+typedef struct {
+  const uint16_t *gate;
+  const uint16_t *scale;
+  const uint16_t *shift;
+  const int32_t *row;
+  int64_t ld;
+  int64_t rows;
+} oq_mod;
+
+/*
+ * oq_residual_norm -- from the end of one block to the start of the next, one
+ * pass over each row:
+ *   u = sum_j weights[t][j] y[t k + j]    (weights NULL: k = 1 and u = y[t])
+ *   R = r_scale r + y_scale gate post(u)  (r NULL: without it; post, gate: as given)
+ *   h = pre(R) (1 + scale) + shift        (pre, scale, shift: as given)
+ * Stored are r_out = R and h, each nullable, each rounded once from float32; h
+ * is formed of R before its rounding.  y NULL: R = r_scale r (no post, no gate).
+ * A row of y whose weight is 0 is not read (an entry that has no expert, say).
+ * y, h bf16; r, r_out of type r_type (OQ_F32 or OQ_BF16).  r_out may be r (same
+ * ld); other outputs must not overlap inputs or each other.
+ * d a multiple of 8, 8 <= d <= 16384; 1 <= k <= 64; T k < 2^31; every row
+ * 16-byte aligned; y_scale, r_scale finite; eps finite, >= 0.
+ */
+int oq_residual_norm(const uint16_t *y, int64_t y_ld, int32_t k, const float *weights, float y_scale, const void *r,
+                     int64_t r_ld, float r_scale, int r_type, int64_t T, int32_t d, const oq_norm *post,
+                     const oq_norm *pre, const oq_mod *mod, void *r_out, int64_t ro_ld, uint16_t *h, int64_t h_ld,
+                     hipStream_t stream);
+
+/*
+ * oq_logprobs -- of each row x of logits [T][ld] (dtype OQ_F32 or OQ_BF16, V
+ * wide), with p = softmax(scale x):
+ *   logprob[t][i] = log p[tokens[t][i]]      (n tokens a row, int32 [T][n])
+ *   rank[t][i]    = how many of the row come before that token (0: the first)
+ *   entropy[t]    = -sum_v p log p,  lse[t] = log sum_v exp(scale x)
+ *   top_id[t][j], top_logprob[t][j], j < top: the first `top` of the row
+ * The order is that of falling logits, equal ones by rising index; NaN comes
+ * behind all numbers.  A token outside [0, V) (padding) gives NaN and rank -1.
+ * Masked logits (-inf) take no part and no time of their own; a row of nothing
+ * else has lse -inf and NaN elsewhere, as has a row with NaN or +inf (whose lse
+ * is NaN too); ranks and top_id are in order there as well.
+ * Sums are float32; values are off by about 1e-7 of lse - scale x, absolute.
+ * Each output nullable but logprob and rank with n > 0, and the top pair with
+ * top > 0.  Rows need the alignment of their element only.
+ * 1 <= V <= 2^22, 0 <= n <= 64, 0 <= top <= 32, top <= V, scale > 0 and its
+ * product with log2(e) finite.
+ * ws: device scratch of oq_logprobs_ws_bytes(T, V, n, top) bytes, 16-byte
+ * aligned (may be 0).
+ */
+int oq_logprobs(const void *logits, int dtype, int64_t ld, int64_t T, int32_t V, float scale, const int32_t *tokens,
+                int32_t n, int32_t top, float *logprob, int32_t *rank, float *entropy, float *lse, int32_t *top_id,
+                float *top_logprob, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* Scratch bytes of oq_logprobs for either dtype (0 for arguments it refuses).
+ * Pure host function of the sizes and the device's CU count; not monotonic. */
+size_t oq_logprobs_ws_bytes(int64_t T, int32_t V, int32_t n, int32_t top);
+
+/*
  * oq_probe_mfma -- measurement helper, not part of the layer: the rate one
  * matrix-core instruction sustains on the calling device at its current clock
  * (a roofline denominator beside the published dense peak, which assumes the

@@ -16,6 +16,8 @@ from ._binding import (  # noqa: F401
     oq_quant_weight_asym, oq_prepack_w4_asym, oq_quant_act_gsum, oq_gemm_w4a4_asym, oq_kron_plan,
     oq_quant_weight_w8, oq_gemm_w8a8,
     Rope, PagedKV, oq_qk_norm_rope, oq_kv_append, oq_attn_prefix, oq_attn_prefix_ws_bytes,
+    Router, Norm, oq_route, oq_route_ws_bytes, oq_gemm_w8a8_experts, oq_residual_norm, oq_logprobs, oq_logprobs_ws_bytes,
+    OQ_F32, OQ_BF16, OQ_SCORE_SOFTMAX, OQ_SCORE_SIGMOID, OQ_ACT_NONE, OQ_ACT_SWIGLU, OQ_NORM_RMS, OQ_NORM_LAYER,
     oq_linear_fused_noalloc, OQ_NOALLOC_SCRATCH_BYTES,
     oq_probe_mfma, OQ_PROBE_FP6, OQ_PROBE_FP4, OQ_PROBE_FP8, OQ_PROBE_I8, OQ_PROBE_BF16, OQ_PROBE_F16,
     OQ_PROBE_FP6_UPDATE,

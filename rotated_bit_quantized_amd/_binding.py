@@ -25,6 +25,10 @@ OQ_W4, OQ_W_MXFP4 = 4, 0x104
 OQ_OP_GEMM_W4A8, OQ_OP_GEMM_W4A4, OQ_OP_LINEAR, OQ_OP_GEMM_LM = 1, 2, 3, 4
 OQ_TILED = 0x10000
 OQ_SCALE_PCTL = 0x20000
+OQ_F32, OQ_BF16 = 1, 2
+OQ_SCORE_SOFTMAX, OQ_SCORE_SIGMOID = 1, 2
+OQ_ACT_NONE, OQ_ACT_SWIGLU = 0, 1
+OQ_NORM_RMS, OQ_NORM_LAYER = 1, 2
 
 
 class OQError(RuntimeError):
@@ -91,6 +95,14 @@ def _load():
         "oq_attn_prefix": ([vp, i64, i64, i32, i32, i32, vp, vp, i32, vp, i32, vp, f32, vp, i64, i64, vp, vp, sz, vp],
                            ctypes.c_int),
         "oq_attn_prefix_ws_bytes": ([i32, i32, i32, vp, i32, i32], sz),
+        "oq_route": ([vp, ctypes.c_int, i64, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
+        "oq_route_ws_bytes": ([i64, vp], sz),
+        "oq_gemm_w8a8_experts": ([vp, i64, vp, i64, i32, vp, i64, i64, vp, i32, i32, vp, vp, i64, i32, ctypes.c_int, vp, vp, vp,
+                                  vp, i64, vp], ctypes.c_int),
+        "oq_residual_norm": ([vp, i64, i32, vp, f32, vp, i64, f32, ctypes.c_int, i64, i32, vp, vp, vp, vp, i64, vp, i64, vp],
+                             ctypes.c_int),
+        "oq_logprobs": ([vp, ctypes.c_int, i64, i64, i32, f32, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
+        "oq_logprobs_ws_bytes": ([i64, i32, i32, i32], sz),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -106,7 +118,8 @@ EXPORTED = ("oq_last_error", "oq_center", "oq_rotate", "oq_quant_act", "oq_quant
             "oq_tiled_f16_bytes", "oq_quant_act_lm", "oq_prepack_w16", "oq_gemm_lm", "oq_quant_weight_asym",
             "oq_prepack_w4_asym", "oq_quant_act_gsum", "oq_gemm_w4a4_asym", "oq_kron_plan",
             "oq_linear_fused_noalloc", "oq_probe_mfma", "oq_probe_sink_elems", "oq_quant_weight_w8", "oq_gemm_w8a8",
-            "oq_qk_norm_rope", "oq_kv_append", "oq_attn_prefix", "oq_attn_prefix_ws_bytes")
+            "oq_qk_norm_rope", "oq_kv_append", "oq_attn_prefix", "oq_attn_prefix_ws_bytes", "oq_route", "oq_route_ws_bytes",
+            "oq_gemm_w8a8_experts", "oq_residual_norm", "oq_logprobs", "oq_logprobs_ws_bytes")
 
 
 def lib():
@@ -849,3 +862,249 @@ def oq_attn_prefix(q, n_q: int, kv: PagedKV, prefix_table, prefix_len: int, tabl
                                table_at, table_ld, lens_at, scale, *_heads(o, shape, "o", dev),
                                _opt(lse, T * heads_q, _F, "lse", dev), ws.data_ptr(), ws.numel() * ws.element_size(), stream))
     return o, lse
+
+
+# ---------------------------------------------------------------- sparse layers, residual stream, answers
+class oq_router(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("experts", ctypes.c_int32), ("k", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32), ("group_best", ctypes.c_int32), ("renorm", ctypes.c_int32),
+                ("factor", ctypes.c_float)]
+
+
+class oq_norm(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("b", ctypes.c_void_p), ("kind", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class oq_mod(ctypes.Structure):
+    _fields_ = [("gate", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("shift", ctypes.c_void_p), ("row", ctypes.c_void_p),
+                ("ld", ctypes.c_int64), ("rows", ctypes.c_int64)]
+
+
+_SCORES = {"softmax": OQ_SCORE_SOFTMAX, "sigmoid": OQ_SCORE_SIGMOID}
+
+
+class Router:
+    """How tokens choose k of `experts`: scores ("softmax" or "sigmoid"), a balance
+    bias (float32 [experts], kept alive here), groups of which the best top_groups are
+    open (by the sum of their group_best best), weights renormalised over the chosen
+    or not, and a factor on them."""
+
+    def __init__(self, experts: int, k: int, score: str = "softmax", bias: Optional[torch.Tensor] = None, groups: int = 1,
+                 top_groups: Optional[int] = None, group_best: int = 1, renorm: bool = True, factor: float = 1.0):
+        if score not in _SCORES:
+            raise OQError(OQ_ERR_INVALID_ARG, f"score must be one of {tuple(_SCORES)}, got {score!r}")
+        top_groups = groups if top_groups is None else top_groups
+        _small(experts, k, groups, top_groups, group_best)
+        self.dev = None
+        if bias is not None:
+            _need(bias, 4 * experts, "bias", _F32)
+            self.dev = bias.get_device()
+        self.experts, self.k, self.bias = experts, k, bias
+        self.c = oq_router(None if bias is None else bias.data_ptr(), experts, k, _SCORES[score], groups, top_groups, group_best,
+                           int(renorm), factor)
+        self.ref = ctypes.byref(self.c)
+
+
+class Norm:
+    """An RMS or layer norm (OQ_NORM_RMS, OQ_NORM_LAYER) of rows of d with weights
+    and bias (float32 [d], kept alive here; each may be None)."""
+
+    def __init__(self, kind: int, d: int, eps: float = 1e-6, w: Optional[torch.Tensor] = None, b: Optional[torch.Tensor] = None):
+        self.dev = None
+        for t, what in ((w, "w"), (b, "b")):
+            if t is None:
+                continue
+            _need(t, 4 * d, what, _F32)
+            if self.dev is not None:
+                _on(t, self.dev, what)
+            self.dev = t.get_device()
+        self.d, self.w, self.b = d, w, b
+        self.c = oq_norm(None if w is None else w.data_ptr(), None if b is None else b.data_ptr(), kind, eps)
+        self.ref = ctypes.byref(self.c)
+
+
+def _wide(h, dev: int, what: str):
+    """Reference to a Router's or Norm's descriptor, whose tensors (if any) have to live on GPU `dev`."""
+    if h.dev is not None and h.dev != dev:
+        raise OQError(OQ_ERR_INVALID_ARG, f"{what} lives on GPU {h.dev}, the current device is {dev}")
+    return h.ref
+
+
+_TYPES = {torch.float32: OQ_F32, torch.bfloat16: OQ_BF16}
+
+
+def _matrix(t: torch.Tensor, shape, dtypes, what: str, dev: int):
+    """(address, row stride) of a matrix of `shape` with unit column stride on GPU `dev`."""
+    if t.get_device() != dev:
+        _on(t, dev, what)
+    if t.dim() != 2 or tuple(t.shape) != tuple(shape) or t.dtype not in dtypes or (t.stride(1) != 1 and shape[1] > 1):
+        raise OQError(OQ_ERR_INVALID_ARG, f"{what} must be a matrix of shape {tuple(shape)} and type {dtypes} with unit column stride, "
+                      f"got {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]  # a matrix of one row has no row stride to speak of
+
+
+def _logits(t: torch.Tensor, what: str):
+    """(type, address, row stride) of logits [T][V] on the current device."""
+    dev, stream = _current(t, what)
+    if t.dim() != 2 or t.dtype not in _TYPES:
+        raise OQError(OQ_ERR_INVALID_ARG, f"{what} must be a float32 or bfloat16 matrix, got {t.dtype} {tuple(t.shape)}")
+    return dev, stream, _TYPES[t.dtype], *_matrix(t, t.shape, _TYPES, what, dev)
+
+
+def _scratch(ws, nbytes: int, dev: int, device):
+    """(address, bytes) of a workspace, allocated where none is given."""
+    if ws is None:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise OQError(OQ_ERR_INVALID_ARG, f"ws must be a contiguous tensor on GPU {dev}")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def oq_route_ws_bytes(T: int, router: Router) -> int:
+    """Scratch bytes of one call with lists."""
+    return int(_lib.oq_route_ws_bytes(T, router.ref))
+
+
+def oq_route(logits, router: Router, mask=None, ids=None, weights=None, offsets=None, order=None, ws=None, lists: bool = True):
+    """logits float32 or bfloat16 [T][experts]; mask uint8 or bool [T] (0: a token
+    without experts); returns (ids int32 [T][k], weights float32 [T][k], offsets int32
+    [experts + 1], order int32 [T k]), the last two None without lists."""
+    dev, stream, dtype, at, ld = _logits(logits, "logits")
+    T, E, k = logits.shape[0], router.experts, router.k
+    if logits.shape[1] != E:
+        raise OQError(OQ_ERR_INVALID_ARG, f"logits of {logits.shape[1]} columns for {E} experts")
+    if ids is None:
+        ids = torch.empty((T, k), dtype=_I32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((T, k), dtype=_F, device=logits.device)
+    if lists:
+        if offsets is None:
+            offsets = torch.empty(E + 1, dtype=_I32, device=logits.device)
+        if order is None:
+            order = torch.empty(T * k, dtype=_I32, device=logits.device)
+    elif offsets is not None or order is not None:
+        raise OQError(OQ_ERR_INVALID_ARG, "offsets or order with lists=False")
+    ws, ws_at, ws_bytes = _scratch(ws, oq_route_ws_bytes(T, router) if lists else 0, dev, logits.device)
+    mask_at = None
+    if mask is not None:
+        if mask.dtype not in (torch.uint8, torch.bool):
+            raise OQError(OQ_ERR_INVALID_ARG, f"mask must be uint8 or bool, got {mask.dtype}")
+        mask_at = _vec(mask, T, mask.dtype, "mask", dev)
+    _check(_lib.oq_route(at, dtype, ld, T, mask_at, _wide(router, dev, "the router"), _vec(ids, T * k, _I32, "ids", dev),
+                         _vec(weights, T * k, _F, "weights", dev), _opt(offsets, E + 1, _I32, "offsets", dev),
+                         _opt(order, T * k, _I32, "order", dev), ws_at, ws_bytes, stream))
+    return ids, weights, offsets, order
+
+
+def oq_gemm_w8a8_experts(qa, a_scale, w, w_scale, offsets, order, per: int = 1, act: int = OQ_ACT_NONE, mean=None, w1=None,
+                         bias=None, y=None):
+    """qa int8 [rows][K], a_scale and mean float32 [rows]; w int8 [E][N][K], w_scale,
+    w1 and bias float32 [E][N]; offsets int32 [E + 1] and order int32 [n] from
+    oq_route; entry i uses activation row i / per and writes row i of y bfloat16 [n][N]
+    ([n][N / 2] with OQ_ACT_SWIGLU)."""
+    if qa.dim() != 2 or w.dim() != 3 or qa.dtype != torch.int8 or w.dtype != torch.int8:
+        raise OQError(OQ_ERR_INVALID_ARG, "qa must be an int8 matrix and w an int8 tensor [E][N][K]")
+    (rows, K), (E, N, Kw) = qa.shape, w.shape
+    if K != Kw or qa.stride(1) != 1 or w.stride(2) != 1:
+        raise OQError(OQ_ERR_INVALID_ARG, f"qa [rows][K] and w [E][N][K] with unit column strides, got {tuple(qa.shape)} and {tuple(w.shape)}")
+    _small(K, N, E, per)
+    dev, stream = _current(qa, "qa")
+    _on(w, dev, "w")
+    n = order.numel()
+    out = N // 2 if act == OQ_ACT_SWIGLU else N
+    if y is None:
+        y = torch.empty((n, out), dtype=torch.bfloat16, device=qa.device)
+    y_at, ldy = _matrix(y, (n, out), _BF16, "y", dev)
+    pad = (K + 15) // 16 * 16
+    ldw = w.stride(1) if N > 1 else pad
+    _check(_lib.oq_gemm_w8a8_experts(qa.data_ptr(), qa.stride(0) if rows > 1 else pad, _vec(a_scale, rows, _F, "a_scale", dev), rows, K,
+                                     w.data_ptr(), ldw, w.stride(0) if E > 1 else N * ldw, _vec(w_scale, E * N, _F, "w_scale", dev),
+                                     N, E, _vec(offsets, E + 1, _I32, "offsets", dev), _vec(order, n, _I32, "order", dev), n, per, act,
+                                     _opt(mean, rows, _F, "mean", dev), _opt(w1, E * N, _F, "w1", dev),
+                                     _opt(bias, E * N, _F, "bias", dev), y_at, ldy, stream))
+    return y
+
+
+def oq_residual_norm(y, r=None, weights=None, post: Optional[Norm] = None, pre: Optional[Norm] = None, gate=None, scale=None,
+                     shift=None, row=None, y_scale: float = 1.0, r_scale: float = 1.0, r_out=None, h=None, want_r: bool = True,
+                     want_h: bool = True, r_dtype=torch.bfloat16):
+    """y bfloat16 [T k][d] (None: no block output) with weights float32 [T][k] (None:
+    k = 1); r float32 or bfloat16 [T][d] (None: no residual yet, r_out is of r_dtype);
+    gate, scale, shift bfloat16 [rows][d] of one row stride, row int32 [T]; returns
+    (r_out, h), None where not wanted.  Passing r as r_out works in place."""
+    x = y if y is not None else r
+    if x is None or x.dim() != 2:
+        raise OQError(OQ_ERR_INVALID_ARG, "y or r, a matrix, is required")
+    d = x.shape[1]
+    dev, stream = _current(x, "y" if y is not None else "r")
+    k = 1
+    if weights is not None:
+        if weights.dim() != 2 or y is None or weights.shape[0] * weights.shape[1] != y.shape[0]:
+            raise OQError(OQ_ERR_INVALID_ARG, "weights must be a matrix of as many elements as y has rows")
+        k = weights.shape[1]
+        T = weights.shape[0]
+    else:
+        T = x.shape[0]
+    _small(d, k)
+    r_type = r.dtype if r is not None else r_out.dtype if r_out is not None else r_dtype
+    if r_type not in _TYPES:
+        raise OQError(OQ_ERR_INVALID_ARG, f"r and r_out must be float32 or bfloat16, got {r_type}")
+    if want_r and r_out is None:
+        r_out = torch.empty((T, d), dtype=r_type, device=x.device)
+    if want_h and h is None:
+        h = torch.empty((T, d), dtype=torch.bfloat16, device=x.device)
+    none = (None, 0)
+    y_at, y_ld = none if y is None else _matrix(y, (T * k, d), _BF16, "y", dev)
+    r_at, r_ld = none if r is None else _matrix(r, (T, d), (r_type,), "r", dev)
+    ro_at, ro_ld = none if not want_r else _matrix(r_out, (T, d), (r_type,), "r_out", dev)
+    h_at, h_ld = none if not want_h else _matrix(h, (T, d), _BF16, "h", dev)
+    for n, what in ((post, "post"), (pre, "pre")):
+        if n is not None and n.d != d:
+            raise OQError(OQ_ERR_INVALID_ARG, f"{what} is a norm of {n.d}, rows have {d}")
+    mod = None
+    parts = [t for t in (gate, scale, shift) if t is not None]
+    if parts:
+        rows = parts[0].shape[0]
+        lds = [_matrix(t, (rows, d), _BF16, "gate, scale or shift", dev)[1] for t in parts]
+        if len(set(lds)) > 1:
+            raise OQError(OQ_ERR_INVALID_ARG, f"gate, scale and shift must have one row stride, got {lds}")
+        mod = ctypes.byref(oq_mod(*(None if t is None else t.data_ptr() for t in (gate, scale, shift)),
+                                  _opt(row, T, _I32, "row", dev), lds[0], rows))
+    _check(_lib.oq_residual_norm(y_at, y_ld, k, _opt(weights, T * k, _F, "weights", dev), y_scale, r_at, r_ld, r_scale, _TYPES[r_type],
+                                 T, d, None if post is None else _wide(post, dev, "post"),
+                                 None if pre is None else _wide(pre, dev, "pre"), mod, ro_at, ro_ld, h_at, h_ld, stream))
+    return (r_out if want_r else None), (h if want_h else None)
+
+
+def oq_logprobs_ws_bytes(T: int, V: int, n: int, top: int) -> int:
+    """Scratch bytes of one call; fewer rows can take more than more do."""
+    _small(V, n, top)
+    return int(_lib.oq_logprobs_ws_bytes(T, V, n, top))
+
+
+def oq_logprobs(logits, tokens=None, top: int = 0, scale: float = 1.0, logprob=None, rank=None, entropy=None, lse=None, top_id=None,
+                top_logprob=None, ws=None):
+    """logits float32 or bfloat16 [T][V]; tokens int32 [T][n] (None: n = 0); returns
+    (logprob [T][n], rank [T][n], entropy [T], lse [T], top_id [T][top], top_logprob [T][top])."""
+    dev, stream, dtype, at, ld = _logits(logits, "logits")
+    T, V = logits.shape
+    n = 0
+    if tokens is not None:
+        if tokens.dim() != 2 or tokens.shape[0] != T:
+            raise OQError(OQ_ERR_INVALID_ARG, f"tokens must be a matrix of {T} rows")
+        n = tokens.shape[1]
+    _small(V, n, top)
+
+    def out(t, *shape, dtype=_F):
+        return torch.empty(shape, dtype=dtype, device=logits.device) if t is None else t
+
+    top_n = max(top, 0)
+    logprob, rank, entropy, lse = out(logprob, T, n), out(rank, T, n, dtype=_I32), out(entropy, T), out(lse, T)
+    top_id, top_logprob = out(top_id, T, top_n, dtype=_I32), out(top_logprob, T, top_n)
+    ws, ws_at, ws_bytes = _scratch(ws, oq_logprobs_ws_bytes(T, V, n, top), dev, logits.device)
+    _check(_lib.oq_logprobs(at, dtype, ld, T, V, scale, _opt(tokens, T * n, _I32, "tokens", dev), n, top,
+                            _vec(logprob, T * n, _F, "logprob", dev), _vec(rank, T * n, _I32, "rank", dev),
+                            _vec(entropy, T, _F, "entropy", dev), _vec(lse, T, _F, "lse", dev),
+                            _vec(top_id, T * top_n, _I32, "top_id", dev), _vec(top_logprob, T * top_n, _F, "top_logprob", dev),
+                            ws_at, ws_bytes, stream))
+    return logprob, rank, entropy, lse, top_id, top_logprob

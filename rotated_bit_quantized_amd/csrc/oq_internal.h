@@ -370,6 +370,76 @@ constexpr float ATTN_LOG2E = 1.44269504088896340736f;  // scores are kept in uni
 size_t attn_prefix_ws(const AttnArgs &a);
 hipError_t launch_attn_prefix(const AttnArgs &a, void *ws, hipStream_t stream);
 
+// Routing (arguments as oq_route, already validated).
+struct RouteArgs {
+  const void *logits;
+  int64_t ld, T;
+  const uint8_t *mask;
+  oq_router r;
+  int32_t *ids;
+  float *weights;
+  int32_t *offsets, *order;  // both NULL: no lists
+};
+size_t route_ws(int64_t T, const oq_router &r);
+hipError_t launch_route(const RouteArgs &a, bool bf16, void *ws, hipStream_t stream);
+
+// The experts' int8 products (arguments as oq_gemm_w8a8_experts, validated, n > 0 and N > 0).
+struct ExpertArgs {
+  const int8_t *qa;
+  int64_t lda;
+  const float *a_scale;
+  int K;
+  const int8_t *w;
+  int64_t ldw, w_stride;
+  const float *w_scale;
+  int N, E;
+  const int32_t *offsets, *order;
+  int64_t n;
+  int per;
+  const float *mean, *w1, *bias;
+  uint16_t *y;
+  int64_t ldy;
+};
+hipError_t launch_gemm_experts(const ExpertArgs &a, int act, hipStream_t stream);
+
+// Residual stream and norms (arguments as oq_residual_norm, validated).
+struct NormArgs {
+  const uint16_t *y;
+  int64_t y_ld;
+  int k;
+  const float *weights;
+  float y_scale;
+  const void *r;
+  int64_t r_ld;
+  float r_scale;
+  int64_t T;
+  int d;
+  oq_norm post, pre;  // kind 0: none
+  oq_mod mod;
+  void *r_out;
+  int64_t ro_ld;
+  uint16_t *h;
+  int64_t h_ld;
+};
+hipError_t launch_residual_norm(const NormArgs &a, bool r_bf16, hipStream_t stream);
+
+// Log probabilities (arguments as oq_logprobs, validated, T > 0).
+struct LogprobArgs {
+  const void *logits;
+  int64_t ld, T;
+  int V;
+  float scale;
+  const int32_t *tokens;
+  int n, top;
+  float *logprob;
+  int32_t *rank;
+  float *entropy, *lse;
+  int32_t *top_id;
+  float *top_logprob;
+};
+size_t logprobs_ws(int64_t T, int V, int n, int top);
+hipError_t launch_logprobs(const LogprobArgs &a, bool bf16, void *ws, hipStream_t stream);
+
 // Compute units of the current device (cached per device).
 int device_cus();
 // Matrix-core rate probe (oq_probe_mfma): launches it and returns the number
