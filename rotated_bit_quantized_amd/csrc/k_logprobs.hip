@@ -27,7 +27,7 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int WAVES = 8, THREADS = 64 * WAVES, LIST = 512;
+constexpr int LIST = 512;
 constexpr float LN2 = 0.693147180559945309417f;
 
 // What is known of a row or a part of it: sums over 2^(z(x)).
@@ -46,10 +46,6 @@ __device__ __forceinline__ Part about(float top, float c) {
   const float ref = top == -INFINITY ? 0.f : top;
   return Part{ref, ref * c, 0.f, 0.f};
 }
-
-struct Plan {
-  int nv, parts;
-};
 
 struct Scratch {
   Part *part;      // [T][parts]
@@ -84,15 +80,6 @@ __device__ __forceinline__ float wave_sum(float v) {
   for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
   return v;
 }
-__device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) {
-    const uint64_t w = (uint64_t)__shfl_xor((unsigned long long)v, o);
-    v = v > w ? v : w;
-  }
-  return v;
-}
-
 template <class T>
 __device__ __forceinline__ float logit(const T *row, int i) {
   if constexpr (sizeof(T) == 2) return __uint_as_float((uint32_t)row[i] << 16);
@@ -118,14 +105,60 @@ __device__ __forceinline__ void token_outputs(const LogprobArgs &a, const T *row
   a.rank[t * a.n + i] = in ? rank : -1;
 }
 
+// The largest of two float32 or four times two bfloat16 numbers at a time; the
+// latter as whole numbers: signed ones order all but negative bfloat16 among
+// themselves, of which the smallest unsigned one is the largest.
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+
 template <class T, int NV>
-__global__ void __launch_bounds__(THREADS) logprobs_part(const LogprobArgs a, const Scratch ws, const int parts) {
+__device__ __forceinline__ float largest(const u32x4 (&raw)[NV]) {
+  float m = -INFINITY;
+  if constexpr (sizeof(T) == 2) {
+    s16x2 hi = {-32768, -32768};
+    u16x2 lo = {65535, 65535};
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t w = raw[v][j];
+        hi = __builtin_elementwise_max(hi, __builtin_bit_cast(s16x2, w));
+        lo = __builtin_elementwise_min(lo, __builtin_bit_cast(u16x2, w));
+      }
+    const int h = hi.x > hi.y ? hi.x : hi.y;
+    const uint32_t l = lo.x < lo.y ? lo.x : lo.y;
+    m = __uint_as_float((h < 0 ? l : (uint32_t)h) << 16);
+    if (m == m) return m;
+    m = -INFINITY;  // a NaN is there: it is passed over
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m = fmaxf(m, fmaxf(bf16_lo(raw[v][j]), bf16_hi(raw[v][j])));
+  } else {
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m = fmaxf(m, __uint_as_float(raw[v][j]));  // passes NaN over
+  }
+  return m;
+}
+
+// Pieces part * each .. (part + 1) * each - 1 of a row, NV a thread at most, by WAVES
+// wavefronts.  Of 8 wavefronts three workgroups fit a CU, whose loads run under each
+// other's arithmetic (2048 x 131072: 133 us; four of them, with 64 registers a
+// thread, spill: 163).
+template <class T, int NV, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, WAVES == 8 ? 6 : 4) logprobs_part(const LogprobArgs a, const Scratch ws, const int parts, const int each) {
+  constexpr int THREADS = 64 * WAVES;
   constexpr int VE = 16 / sizeof(T);  // elements of a piece
+  constexpr int HELD = 64;            // threads whose pieces go to LDS for their candidates
+  __shared__ u32x4 s_held[HELD * NV];
+  __shared__ int s_first[HELD];
   __shared__ uint32_t s_max[WAVES * 64];
   __shared__ float s_sum[2 * WAVES];
   __shared__ uint64_t s_list[LIST];
   __shared__ int s_rank[64];
-  __shared__ int s_count[2];
+  __shared__ int s_count[3];  // listed candidates, a count, threads held
   __shared__ uint32_t s_limit;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = blockIdx.x / parts;
@@ -133,46 +166,51 @@ __global__ void __launch_bounds__(THREADS) logprobs_part(const LogprobArgs a, co
   const T *row = static_cast<const T *>(a.logits) + t * a.ld;
   // pieces lie on 16-byte boundaries: the first one may begin before the row
   const int lead = (int)(reinterpret_cast<uintptr_t>(row) & 15) / (int)sizeof(T);
-  const int first = (part * NV * THREADS + (int)threadIdx.x) * VE - lead;  // element of this thread's first piece
-  constexpr int STEP = THREADS * VE;
+  const int begin = part * each * VE - lead > 0 ? part * each * VE - lead : 0;  // elements of the part
+  const int end = (part + 1) * each * VE - lead < a.V ? (part + 1) * each * VE - lead : a.V;
+  const int p0 = part * each + (int)threadIdx.x;  // this thread's pieces: p0, p0 + THREADS, ..
   constexpr uint32_t NONE = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;  // -inf
+  const u32x4 *pieces = reinterpret_cast<const u32x4 *>(row - lead) + p0;
+  const int whole = (end + lead) / VE;                                   // the part's pieces up to here are whole
+  const int nv = whole > p0 ? (whole - p0 + THREADS - 1) / THREADS : 0;  // and so many of this thread
+  const bool cut = p0 == 0 && lead > 0;                                  // the row begins inside the first one
   u32x4 raw[NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int i = first + v * STEP;
     raw[v] = (u32x4){NONE, NONE, NONE, NONE};
-    if (i >= 0 && i + VE <= a.V) {
-      raw[v] = *reinterpret_cast<const u32x4 *>(row + i);
-    } else if (i + VE > 0 && i < a.V) {  // a piece that the row fills in part
+    if (v < nv && !(v == 0 && cut)) raw[v] = pieces[v * THREADS];
+  }
+  // a row's first and last piece, which it may fill in part
+  auto partial = [&](int i) {
+    u32x4 piece = {NONE, NONE, NONE, NONE};
 #pragma unroll
-      for (int j = 0; j < VE; ++j) {
-        if (i + j < 0 || i + j >= a.V) continue;
-        if constexpr (sizeof(T) == 2) {
-          const uint32_t w = raw[v][j / 2], e = row[i + j];
-          raw[v][j / 2] = j & 1 ? (w & 0xFFFFu) | e << 16 : (w & 0xFFFF0000u) | e;
-        } else {
-          raw[v][j] = __float_as_uint(row[i + j]);
-        }
+    for (int j = 0; j < VE; ++j) {
+      if (i + j < 0 || i + j >= end) continue;
+      if constexpr (sizeof(T) == 2) {
+        const uint32_t w = piece[j / 2], e = row[i + j];
+        piece[j / 2] = j & 1 ? (w & 0xFFFFu) | e << 16 : (w & 0xFFFF0000u) | e;
+      } else {
+        piece[j] = __float_as_uint(row[i + j]);
       }
     }
+    return piece;
+  };
+  if (cut) raw[0] = partial(-lead);
+  if (whole * VE - lead < end && whole >= p0 && (whole - p0) % THREADS == 0 && !(whole == 0 && cut)) {
+    const u32x4 piece = partial(whole * VE - lead);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) raw[v] = v == nv ? piece : raw[v];
   }
   auto at = [&](int v, int j) {
     if constexpr (sizeof(T) == 2) return j & 1 ? bf16_hi(raw[v][j / 2]) : bf16_lo(raw[v][j / 2]);
     else return __uint_as_float(raw[v][j]);
   };
-  // what was unpacked for one pass over the registers is not kept for the next
-  auto forget = [&]() {
-#pragma unroll
-    for (int v = 0; v < NV; ++v) asm volatile("" : "+v"(raw[v]));
-  };
+  // what was unpacked of a piece for one pass over the registers is not kept for the next
+  auto forget = [&](int v) { asm volatile("" : "+v"(raw[v])); };
   if (threadIdx.x < 64) s_rank[threadIdx.x] = 0;
-  if (threadIdx.x < 2) s_count[threadIdx.x] = 0;
+  if (threadIdx.x < 3) s_count[threadIdx.x] = 0;
 
-  float mine = -INFINITY;
-#pragma unroll
-  for (int v = 0; v < NV; ++v)
-#pragma unroll
-    for (int j = 0; j < VE; ++j) mine = fmaxf(mine, at(v, j));  // passes NaN over
+  const float mine = largest<T, NV>(raw);
   s_max[threadIdx.x] = order_of(mine);
   __syncthreads();
   uint32_t group = 0;  // the largest over the threads of this lane number
@@ -184,61 +222,6 @@ __global__ void __launch_bounds__(THREADS) logprobs_part(const LogprobArgs a, co
   const float top = value_of(wave_max(group)), c = a.scale * ATTN_LOG2E;
   Part stat = about(top, c);
 
-  float s = 0.f, sum_t = 0.f;
-  auto sums = [&](auto z_at) {
-    forget();
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-      for (int j = 0; j < VE; ++j) {
-        const float z = z_at(at(v, j)), e = __builtin_amdgcn_exp2f(z);
-        s += e;
-        sum_t = __builtin_fmaf(e, fmaxf(z, -1024.f), sum_t);  // 2^-inf takes no part
-      }
-  };
-  if (fabsf(stat.m) < INFINITY) sums([&](float x) { return __builtin_fmaf(x, c, -stat.m); });
-  else sums([&](float x) { return (x - stat.top) * c; });
-  s = wave_sum(s);
-  sum_t = wave_sum(sum_t);
-  if (lane == 0) s_sum[wave] = s, s_sum[WAVES + wave] = sum_t;
-
-  // ranks: elements above the token's, and equal ones before it.  A piece before
-  // the token counts from its value on, one behind it from the next value on.
-  for (int i = 0; i < a.n; ++i) {
-    const int tok = a.tokens[t * a.n + i];
-    if (tok < 0 || tok >= a.V) continue;
-    const float xt = logit(row, tok);
-    int count = 0;
-    forget();
-    if (xt > -INFINITY) {
-      const float above = value_of(order_of(xt) + 1);
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const int i0 = first + v * STEP;
-        const float limit = i0 + VE <= tok ? xt : above;
-#pragma unroll
-        for (int j = 0; j < VE; ++j) count += __popcll(__ballot(at(v, j) >= limit));
-        if (i0 <= tok && tok < i0 + VE) {  // one thread of the row: equal ones in the token's own piece
-          int equal = 0;
-#pragma unroll
-          for (int j = 0; j < VE; ++j) equal += i0 + j < tok && at(v, j) == xt;
-          atomicAdd(s_rank + i, equal);
-        }
-      }
-    } else {  // -inf or NaN: places outside the row would count too
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int j = 0; j < VE; ++j) {
-          const int at_i = first + v * STEP + j;
-          const float x = at(v, j);
-          const uint32_t o = order_of(x), ot = order_of(xt);
-          count += __popcll(__ballot(at_i >= 0 && at_i < a.V && (o > ot || (o == ot && at_i < tok))));
-        }
-    }
-    if (lane == 0 && count) atomicAdd(s_rank + i, count);
-  }
-
   // the threshold: the top-th largest of the 64 group maxima
   if (a.top > 0 && wave == 0) {
     uint32_t left = group, limit = 0;
@@ -248,6 +231,61 @@ __global__ void __launch_bounds__(THREADS) logprobs_part(const LogprobArgs a, co
       if (lane == win) left = 0;
     }
     if (lane == 0) s_limit = limit;
+  }
+
+  float s = 0.f, sum_t = 0.f;
+  auto sums = [&](auto z_at) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      forget(v);
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        const float z = z_at(at(v, j)), e = __builtin_amdgcn_exp2f(z);
+        s += e;
+        sum_t = __builtin_fmaf(e, fmaxf(z, -1024.f), sum_t);  // 2^-inf takes no part
+      }
+    }
+  };
+  if (fabsf(stat.m) < INFINITY) sums([&](float x) { return __builtin_fmaf(x, c, -stat.m); });
+  else sums([&](float x) { return (x - stat.top) * c; });
+  s = wave_sum(s);
+  sum_t = wave_sum(sum_t);
+  if (lane == 0) s_sum[wave] = s, s_sum[WAVES + wave] = sum_t;
+
+  // ranks: elements above the token's, and equal ones before it.  A piece before
+  // the token's counts from its value on, that one and those behind it from the
+  // next value on.  A wavefront whose largest is below the token has nothing to count.
+#pragma unroll 1
+  for (int i = 0; i < a.n; ++i) {
+    const int tok = a.tokens[t * a.n + i];
+    if (tok < 0 || tok >= a.V) continue;
+    const float xt = logit(row, tok);
+    int count = 0;
+    if (xt > -INFINITY) {
+      const int own = (tok + lead) / VE;  // the token's piece; equal ones in it:
+      if (own >= part * each && own < (part + 1) * each && (int)threadIdx.x < VE) {
+        const int e = own * VE - lead + (int)threadIdx.x;
+        if (e >= 0 && e < tok && logit(row, e) == xt) atomicAdd(s_rank + i, 1);
+      }
+      if (__ballot(mine >= xt) == 0) continue;
+      const float above = value_of(order_of(xt) + 1);
+      const int before = own > p0 ? (own - p0 + THREADS - 1) / THREADS : 0;  // pieces of this thread before it
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        forget(v);
+        const float limit = v < before ? xt : above;
+#pragma unroll
+        for (int j = 0; j < VE; ++j) count += __popcll(__ballot(at(v, j) >= limit));
+      }
+    } else {  // -inf or NaN: no value in the registers stands for places outside the row
+      const uint32_t ot = order_of(xt);
+      for (int e = begin + (int)threadIdx.x; e < end; e += THREADS) {
+        const uint32_t o = order_of(logit(row, e));
+        count += o > ot || (o == ot && e < tok);
+      }
+      for (int o = 32; o; o >>= 1) count += __shfl_xor(count, o);
+    }
+    if (lane == 0 && count) atomicAdd(s_rank + i, count);
   }
   __syncthreads();
 #pragma unroll
@@ -260,87 +298,90 @@ __global__ void __launch_bounds__(THREADS) logprobs_part(const LogprobArgs a, co
       const int n = atomicAdd(s_count, 1);
       if (n < LIST) s_list[n] = key_of(x, i);
     };
-    auto collect = [&](uint32_t from) {  // every number of order `from` on, from > lowest
-      const float v0 = value_of(from);
-      forget();
+    // the threads that hold a candidate hand their pieces to all; of masked rows
+    // every number is one
+    const float v0 = value_of(limit > lowest ? limit : lowest + 1);
+    if (mine >= v0) {
+      const int at_held = atomicAdd(s_count + 2, 1);
+      if (at_held < HELD) {
+        s_first[at_held] = p0 * VE - lead;
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int j = 0; j < VE; ++j)
-          if (at(v, j) >= v0) add(at(v, j), first + v * STEP + j);
-    };
-    auto count_from = [&](uint32_t from, int slot) {  // how many numbers of order `from` on, from > lowest
-      const float v0 = value_of(from);
-      forget();
-      int count = 0;
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int j = 0; j < VE; ++j) count += __popcll(__ballot(at(v, j) >= v0));
-      __syncthreads();
-      if (threadIdx.x == 0) s_count[slot] = 0;
-      __syncthreads();
-      if (lane == 0) atomicAdd(s_count + slot, count);
-      __syncthreads();
-      return s_count[slot];
-    };
-    // the first `want` elements of order o in this wavefront, by index
-    auto collect_first = [&](uint32_t o, int want) {
-      for (int v = 0; v < NV && want > 0; ++v) {
-        uint32_t hit = 0;
-        forget();
-#pragma unroll
-        for (int w = 0; w < NV; ++w)  // raw[] stays in registers
-          if (w == v) {
-#pragma unroll
-            for (int j = 0; j < VE; ++j) {
-              const int i = first + w * STEP + j;
-              hit |= (uint32_t)(i >= 0 && i < a.V && order_of(at(w, j)) == o) << j;
-            }
-          }
-        int before = 0, all = 0;
-#pragma unroll
-        for (int j = 0; j < VE; ++j) {
-          const uint64_t b = __ballot(hit >> j & 1);
-          before += __popcll(b & ((1ull << lane) - 1));
-          all += __popcll(b);
-        }
-        const float x = value_of(o);
-#pragma unroll
-        for (int j = 0; j < VE; ++j)
-          if (hit >> j & 1 && before++ < want) add(x, first + v * STEP + j);
-        want -= all;
+        for (int v = 0; v < NV; ++v) s_held[at_held * NV + v] = raw[v];
       }
-    };
-    bool listed = false;
-    if (limit > lowest) {
-      collect(limit);
+    }
+    __syncthreads();
+    const int held = s_count[2];
+    bool listed = held <= HELD;
+    if (listed) {
+      for (int e = threadIdx.x; e < held * (NV * VE); e += THREADS) {
+        const int h = e / (NV * VE), r = e - h * (NV * VE);
+        float x;
+        if constexpr (sizeof(T) == 2) x = __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(s_held)[e] << 16);
+        else x = reinterpret_cast<const float *>(s_held)[e];
+        if (x >= v0) add(x, s_first[h] + r / VE * (THREADS * VE) + r % VE);
+      }
       __syncthreads();
       listed = s_count[0] <= LIST;
       __syncthreads();
     }
+    // What is left is rare and reads the part again, element by element.
+    // the first `want` elements of order o among this wavefront's, by index
+    auto collect_first = [&](uint32_t o, int want) {
+      for (int i0 = begin + 64 * wave; i0 < end && want > 0; i0 += THREADS) {
+        const int i = i0 + lane;
+        const bool hit = i < end && order_of(logit(row, i)) == o;
+        const uint64_t hits = __ballot(hit);
+        if (hit && __popcll(hits & ((1ull << lane) - 1)) < want) add(value_of(o), i);
+        want -= __popcll(hits);
+      }
+    };
     if (!listed) {
       // too many: the exact top-th value, unless fewer are above the limit
-      int above = count_from(limit + 1, 1);
+      auto count_from = [&](uint32_t from) {  // how many numbers of order `from` on
+        const float least = value_of(from);
+        int count = 0;
+#pragma unroll 8
+        for (int i = begin + (int)threadIdx.x; i < end; i += THREADS) count += logit(row, i) >= least;
+        for (int o = 32; o; o >>= 1) count += __shfl_xor(count, o);
+        __syncthreads();
+        if (threadIdx.x == 0) s_count[1] = 0;
+        __syncthreads();
+        if (lane == 0) atomicAdd(s_count + 1, count);
+        __syncthreads();
+        return s_count[1];
+      };
+      int above = count_from(limit + 1);
       if (above >= a.top) {
         uint32_t lo = limit + 1, hi = order_of(top) + 1;  // count(lo) >= top, count(hi) = 0
         while (hi - lo > 1) {
           const uint32_t mid = lo + (hi - lo) / 2;
-          if (count_from(mid, 1) >= a.top) lo = mid;
+          if (count_from(mid) >= a.top) lo = mid;
           else hi = mid;
         }
         limit = lo;
-        above = count_from(limit + 1, 1);
+        above = count_from(limit + 1);
       }
       __syncthreads();
       if (threadIdx.x == 0) s_count[0] = 0;
       __syncthreads();
-      if (above > 0) collect(limit + 1);
-      collect_first(limit, a.top - above);
+      if (above > 0) {
+        const float least = value_of(limit + 1);
+        for (int i = begin + (int)threadIdx.x; i < end; i += THREADS) {
+          const float x = logit(row, i);
+          if (x >= least) add(x, i);
+        }
+      }
       __syncthreads();
-      const int n = s_count[0];
+    }
+    // fewer than wanted: the first ones equal to the limit, then NaN
+    int have = s_count[0];
+    __syncthreads();
+    if (have < a.top) {
+      collect_first(limit, a.top - have);
       __syncthreads();
-      if (limit == lowest && n < a.top) collect_first(1, a.top - n);  // fewer numbers than that: NaN
+      have = s_count[0];
+      __syncthreads();
+      if (have < a.top) collect_first(1, a.top - have);
       __syncthreads();
     }
     const int n = s_count[0];
@@ -367,6 +408,8 @@ __global__ void __launch_bounds__(THREADS) logprobs_part(const LogprobArgs a, co
   }
 }
 
+// A wavefront joins a row's parts.  Everything it reads is asked for before it is
+// used, but a token's logit.
 template <class T>
 __global__ void __launch_bounds__(64) logprobs_join(const LogprobArgs a, const Scratch ws, const int parts) {
   extern __shared__ uint64_t s_keys[];  // [parts][top]
@@ -374,10 +417,20 @@ __global__ void __launch_bounds__(64) logprobs_join(const LogprobArgs a, const S
   const int64_t t = blockIdx.x;
   const T *row = static_cast<const T *>(a.logits) + t * a.ld;
   const int total = parts * a.top;
+  const int tok = lane < a.n ? a.tokens[t * a.n + lane] : -1;
+  const bool in = tok >= 0 && tok < a.V;
+  const float xt = in ? logit(row, tok) : 0.f;
+  int rank = 0;
+  if (lane < a.n) {
+#pragma unroll 8
+    for (int p = 0; p < parts; ++p) rank += ws.ranks[(t * parts + p) * a.n + lane];
+  }
+#pragma unroll 4
   for (int i = lane; i < total; i += 64) s_keys[i] = ws.keys[t * total + i];
   // parts of nothing but -inf (s = 0) have no maximum
-  float top = -INFINITY;
-  for (int p = lane; p < parts; p += 64) {
+  Part mine = lane < parts ? ws.part[t * parts + lane] : Part{0.f, 0.f, 0.f, 0.f};
+  float top = mine.s != 0.f ? mine.top : -INFINITY;
+  for (int p = lane + 64; p < parts; p += 64) {
     const Part q = ws.part[t * parts + p];
     if (q.s != 0.f) top = fmaxf(top, q.top);
   }
@@ -386,7 +439,7 @@ __global__ void __launch_bounds__(64) logprobs_join(const LogprobArgs a, const S
   const float c = a.scale * ATTN_LOG2E;
   Part stat = about(top, c);
   for (int p = lane; p < parts; p += 64) {
-    const Part q = ws.part[t * parts + p];
+    const Part q = p == lane ? mine : ws.part[t * parts + p];
     if (q.s == 0.f) continue;
     const bool far = !(fabsf(q.m) < INFINITY && fabsf(stat.m) < INFINITY);
     const float down = fmaxf(far ? (q.top - stat.top) * c : q.m - stat.m, -1024.f), f = __builtin_amdgcn_exp2f(down);
@@ -396,50 +449,83 @@ __global__ void __launch_bounds__(64) logprobs_join(const LogprobArgs a, const S
   stat.s = wave_sum(stat.s);
   stat.t = wave_sum(stat.t);
   if (lane == 0) row_outputs(a, t, stat);
-  for (int i = lane; i < a.n; i += 64) {
-    int rank = 0;
-    for (int p = 0; p < parts; ++p) rank += ws.ranks[(t * parts + p) * a.n + i];
-    token_outputs(a, row, t, i, stat, rank);
+  if (lane < a.n) {
+    a.logprob[t * a.n + lane] = in ? log_prob(xt, a.scale, stat) : NAN;
+    a.rank[t * a.n + lane] = in ? rank : -1;
   }
   if (a.top == 0) return;
   __syncthreads();
-  // the parts' sorted lists are merged: every lane the best of its parts' heads,
-  // packed behind the key's index as nothing but the place in LDS
-  int mine = -1;  // place of the best head of parts lane, lane + 64, ..
+  // The parts' sorted lists are merged: every lane the best of the heads of parts
+  // lane, lane + 64, ..; a head that was taken is 0.  Where a lane has one list
+  // alone, it also holds the next key of it.
+  int place = -1;
   auto find = [&]() {
     uint64_t best = 0;
-    mine = -1;
+    place = -1;
     for (int p = lane; p < parts; p += 64)
-      for (int j = 0; j < a.top; ++j) {  // heads that were taken are 0
+      for (int j = 0; j < a.top; ++j) {
         const uint64_t k = s_keys[p * a.top + j];
         if (k == 0) continue;
-        if (k > best) best = k, mine = p * a.top + j;
+        if (k > best) best = k, place = p * a.top + j;
         break;
       }
     return best;
   };
-  uint64_t head = find();
+  const bool single = parts <= 64;
+  const int list_end = (lane + 1) * a.top;
+  uint64_t head = 0, next = 0, best_key = 0;
+  if (single) {
+    place = lane * a.top + 1;
+    if (lane < parts) head = s_keys[place - 1];
+    if (lane < parts && place < list_end) next = s_keys[place];
+  } else {
+    head = find();
+  }
   for (int j = 0; j < a.top; ++j) {
-    const uint64_t best = wave_max64(head);
-    if (head == best && best) {
-      a.top_id[t * a.top + j] = (int32_t)~(uint32_t)best;
-      a.top_logprob[t * a.top + j] = log_prob(value_of((uint32_t)(best >> 32)), a.scale, stat);
-      s_keys[mine] = 0;
-      head = find();
+    // the largest value, of equal ones the largest key behind it
+    const uint32_t value = wave_max((uint32_t)(head >> 32));
+    const uint64_t equal = __ballot((uint32_t)(head >> 32) == value);
+    int win = __ffsll((long long)equal) - 1;
+    if (equal & (equal - 1)) {
+      const uint32_t low = wave_max((uint32_t)(head >> 32) == value ? (uint32_t)head : 0u);
+      win = __ffsll((long long)__ballot((uint32_t)(head >> 32) == value && (uint32_t)head == low)) - 1;
     }
+    const uint64_t best = (uint64_t)value << 32 | (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)head, win);
+    if (lane == j) best_key = best;
+    if (lane == win && best) {
+      if (single) {
+        head = next;
+        next = ++place < list_end ? s_keys[place] : 0;
+      } else {
+        s_keys[place] = 0;
+        head = find();
+      }
+    }
+  }
+  if (lane < a.top && best_key) {
+    a.top_id[t * a.top + lane] = (int32_t)~(uint32_t)best_key;
+    a.top_logprob[t * a.top + lane] = log_prob(value_of((uint32_t)(best_key >> 32)), a.scale, stat);
   }
 }
 
-// Pieces a thread and parts a row: as many pieces as there are, up to 8, while the parts of
-// all rows still are two workgroups a CU.
-Plan plan_for(int64_t T, int V, int bytes) {
+// Wavefronts of a workgroup, pieces a thread and parts a row.  lead: elements by
+// which rows begin inside a piece.
+struct Plan {
+  int waves, nv, parts, each;  // each: pieces of a part
+};
+Plan plan_for(int64_t T, int V, int bytes, int lead) {
   const int ve = 16 / bytes;
-  const int64_t pieces = ((int64_t)V + 2 * (ve - 1)) / ve;  // a row that begins inside a piece has one more
-  Plan p{8, 1};
+  const int pieces = (V + lead + ve - 1) / ve;
+  // Few rows that 16 wavefronts can hold: one launch.  Else as many pieces a thread
+  // as there are, up to 8, while the parts of all rows still are two workgroups a CU.
+  if (T <= 2 * device_cus() && pieces <= 1024 * 8 && pieces > 512) return Plan{16, 8, 1, pieces};
+  Plan p{8, 8, 1, 0};
   for (;; p.nv /= 2) {
-    p.parts = (int)((pieces + (int64_t)THREADS * p.nv - 1) / ((int64_t)THREADS * p.nv));
-    if (p.nv == 1 || T * p.parts >= 2 * device_cus()) return p;
+    p.parts = (pieces + 512 * p.nv - 1) / (512 * p.nv);
+    if (p.nv == 1 || T * p.parts >= 2 * device_cus()) break;
   }
+  p.each = (pieces + p.parts - 1) / p.parts;
+  return p;
 }
 
 size_t round16(size_t n) { return (n + 15) & ~(size_t)15; }
@@ -451,17 +537,20 @@ size_t scratch_bytes(int64_t T, int parts, int n, int top) {
 
 template <class T>
 hipError_t launch(const LogprobArgs &a, void *ws, hipStream_t stream) {
-  const Plan p = plan_for(a.T, a.V, sizeof(T));
+  const int ve = 16 / sizeof(T), lead = (int)(reinterpret_cast<uintptr_t>(a.logits) & 15) / (int)sizeof(T);
+  const Plan p = plan_for(a.T, a.V, sizeof(T), a.T == 1 || a.ld % ve == 0 ? lead : ve - 1);
   const size_t rows = (size_t)a.T * p.parts;
   if (rows > 0x7fffffff) return hipErrorInvalidConfiguration;
   char *base = static_cast<char *>(ws);
   const Scratch w{reinterpret_cast<Part *>(base), reinterpret_cast<uint64_t *>(base + rows * sizeof(Part)),
                   reinterpret_cast<int32_t *>(base + rows * sizeof(Part) + round16(rows * a.top * 8))};
-#define PART(NV) hipLaunchKernelGGL((logprobs_part<T, NV>), dim3((unsigned)rows), dim3(THREADS), 0, stream, a, w, p.parts)
-  if (p.nv == 8) PART(8);
-  else if (p.nv == 4) PART(4);
-  else if (p.nv == 2) PART(2);
-  else PART(1);
+#define PART(NV, WAVES) \
+  hipLaunchKernelGGL((logprobs_part<T, NV, WAVES>), dim3((unsigned)rows), dim3(64 * WAVES), 0, stream, a, w, p.parts, p.each)
+  if (p.waves == 16) PART(8, 16);
+  else if (p.nv == 8) PART(8, 8);
+  else if (p.nv == 4) PART(4, 8);
+  else if (p.nv == 2) PART(2, 8);
+  else PART(1, 8);
 #undef PART
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.parts == 1) return e;
@@ -472,8 +561,13 @@ hipError_t launch(const LogprobArgs &a, void *ws, hipStream_t stream) {
 }  // namespace
 
 size_t logprobs_ws(int64_t T, int V, int n, int top) {
-  const size_t b = scratch_bytes(T, plan_for(T, V, 2).parts, n, top), f = scratch_bytes(T, plan_for(T, V, 4).parts, n, top);
-  return b > f ? b : f;
+  size_t most = 0;
+  for (int bytes = 2; bytes <= 4; bytes += 2)
+    for (int lead = 0; lead < 16 / bytes; ++lead) {  // a piece more can choose another plan
+      const size_t b = scratch_bytes(T, plan_for(T, V, bytes, lead).parts, n, top);
+      most = b > most ? b : most;
+    }
+  return most;
 }
 
 hipError_t launch_logprobs(const LogprobArgs &a, bool bf16, void *ws, hipStream_t stream) {
