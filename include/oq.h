@@ -683,7 +683,7 @@ typedef struct {
  * order, expert e's at offsets[e] .. offsets[e + 1] - 1 (int32 [experts + 1]).
  * mask uint8 [T] (nullable): a token of 0 gets ids -1 and weights 0 and is in
  * no list; places of order behind offsets[experts] get -1.
- * T k <= 2^30.  ws: device scratch of oq_route_ws_bytes(T, r) bytes, 16-byte
+ * T k <= 2^28.  ws: device scratch of oq_route_ws_bytes(T, r) bytes, 16-byte
  * aligned (not read without lists; may be 0).
  */
 int oq_route(const void *logits, int dtype, int64_t ld, int64_t T, const uint8_t *mask, const oq_router *r, int32_t *ids,
@@ -712,7 +712,7 @@ enum { OQ_ACT_NONE = 0, OQ_ACT_SWIGLU = 1 };
  * An entry may be in the lists once; rows of y whose entry is in no list stay
  * as they are.  List values outside their range are ignored (offsets are cut to
  * 0 .. n, an order outside 0 .. n - 1 has no row).
- * 0 <= n <= 2^30, per >= 1, rows >= ceil(n / per); 1 <= E <= 1024; K, lda, ldw,
+ * 0 <= n <= 2^28, per >= 1, rows >= ceil(n / per); 1 <= E <= 1024; K, lda, ldw,
  * alignment as oq_gemm_w8a8, w_stride a multiple of 16 and at least N ldw.
  * N <= 2^20.  No scratch.  A row's bits do not depend on the other entries.
  */

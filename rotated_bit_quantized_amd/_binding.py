@@ -951,10 +951,10 @@ def _logits(t: torch.Tensor, what: str):
     return dev, stream, _TYPES[t.dtype], *_matrix(t, t.shape, _TYPES, what, dev)
 
 
-def _scratch(ws, nbytes: int, dev: int, device):
-    """(address, bytes) of a workspace, allocated where none is given."""
+def _scratch(ws, nbytes, dev: int, device):
+    """(tensor, address, bytes) of a workspace; where none is given, one of nbytes() is allocated."""
     if ws is None:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws = torch.empty(nbytes(), dtype=torch.uint8, device=device)
     elif ws.get_device() != dev or not ws.is_contiguous():
         raise OQError(OQ_ERR_INVALID_ARG, f"ws must be a contiguous tensor on GPU {dev}")
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
@@ -984,7 +984,7 @@ def oq_route(logits, router: Router, mask=None, ids=None, weights=None, offsets=
             order = torch.empty(T * k, dtype=_I32, device=logits.device)
     elif offsets is not None or order is not None:
         raise OQError(OQ_ERR_INVALID_ARG, "offsets or order with lists=False")
-    ws, ws_at, ws_bytes = _scratch(ws, oq_route_ws_bytes(T, router) if lists else 0, dev, logits.device)
+    ws, ws_at, ws_bytes = _scratch(ws, lambda: oq_route_ws_bytes(T, router) if lists else 0, dev, logits.device)
     mask_at = None
     if mask is not None:
         if mask.dtype not in (torch.uint8, torch.bool):
@@ -1101,7 +1101,7 @@ def oq_logprobs(logits, tokens=None, top: int = 0, scale: float = 1.0, logprob=N
     top_n = max(top, 0)
     logprob, rank, entropy, lse = out(logprob, T, n), out(rank, T, n, dtype=_I32), out(entropy, T), out(lse, T)
     top_id, top_logprob = out(top_id, T, top_n, dtype=_I32), out(top_logprob, T, top_n)
-    ws, ws_at, ws_bytes = _scratch(ws, oq_logprobs_ws_bytes(T, V, n, top), dev, logits.device)
+    ws, ws_at, ws_bytes = _scratch(ws, lambda: oq_logprobs_ws_bytes(T, V, n, top), dev, logits.device)
     _check(_lib.oq_logprobs(at, dtype, ld, T, V, scale, _opt(tokens, T * n, _I32, "tokens", dev), n, top,
                             _vec(logprob, T * n, _F, "logprob", dev), _vec(rank, T * n, _I32, "rank", dev),
                             _vec(entropy, T, _F, "entropy", dev), _vec(lse, T, _F, "lse", dev),

@@ -36,7 +36,7 @@ int check_router(const char *fn, const oq_router *r, int64_t T) {
     return fail(OQ_ERR_INVALID_ARG, "%s: k=%d of %d open experts", fn, r->k, r->top_groups * each);
   if (!std::isfinite(r->factor)) return fail(OQ_ERR_INVALID_ARG, "%s: factor is not finite", fn);
   if (!al(r->bias, 4)) return fail(OQ_ERR_ALIGNMENT, "%s: bias misaligned", fn);
-  if (T > ((int64_t)1 << 30) / r->k) return fail(OQ_ERR_UNSUPPORTED, "%s: more than 2^30 entries", fn);
+  if (T > ((int64_t)1 << 28) / r->k) return fail(OQ_ERR_UNSUPPORTED, "%s: more than 2^28 entries", fn);
   return OQ_OK;
 }
 
@@ -115,7 +115,7 @@ int oq_gemm_w8a8_experts(const int8_t *qa, int64_t lda, const float *a_scale, in
   if (E > 1024 || N > (1 << 20)) return fail(OQ_ERR_UNSUPPORTED, "%s: E=%d exceeds 1024 or N=%d exceeds 2^20", fn, E, N);
   if ((mean == nullptr) != (w1 == nullptr)) return fail(OQ_ERR_INVALID_ARG, "%s: mean and w1 must be given together", fn);
   if (n == 0 || N == 0) return OQ_OK;
-  if (n > ((int64_t)1 << 30)) return fail(OQ_ERR_UNSUPPORTED, "%s: n=%lld exceeds 2^30", fn, (long long)n);
+  if (n > ((int64_t)1 << 28)) return fail(OQ_ERR_UNSUPPORTED, "%s: n=%lld exceeds 2^28", fn, (long long)n);
   if (rows < (n + per - 1) / per)
     return fail(OQ_ERR_INVALID_ARG, "%s: %lld activation rows for %lld entries, %d a row", fn, (long long)rows, (long long)n, per);
   if (!qa || !a_scale || !w || !w_scale || !offsets || !order || !y) return fail(OQ_ERR_INVALID_ARG, "%s: NULL operand", fn);

@@ -18,11 +18,15 @@ namespace oq {
 namespace {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v16i __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 template <int C>
 __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt(0x0F70 | (C & 0xF) | ((C >> 4) << 14));
 }
+
+__device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0xC07F); }
 
 // x / d for a divisor whose reciprocal r = floor(2^32 / d) + 1 the host has
 // formed: the high product is the quotient or one more.
@@ -36,18 +40,51 @@ __device__ __forceinline__ uint32_t div_of(uint32_t x, Div v) {
   return q * v.d > x ? q - 1 : q;
 }
 
-// Entries order[p0] .. order[p0 + rows - 1] of expert e; rows 0: no such tile.
-struct RowTile {
-  int e, p0, rows;
+// Entries order[p0] .. order[p0 + rows - 1] of expert e, against column tile tn;
+// rows 0: no such tile.
+struct Place {
+  int e, p0, rows, tn;
 };
 
-// Row tile `tile` of the lists, TM entries a tile.  The same in every lane.
+// An address that all lanes share, in scalar registers.
+__device__ __forceinline__ const int8_t *scalar(const int8_t *p) {
+  const uint64_t a = (uint64_t)p;
+  return (const int8_t *)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32)) << 32 |
+                          (uint32_t)__builtin_amdgcn_readfirstlane((int)a));
+}
+
+// Row tiles of the lanes up to and with this one, of which it has `tiles`.  Lists as
+// oq_route makes them have no more than n / TM + E; of others the sum stays in 32
+// bits all the same (n <= 2^28).
 template <int TM>
-__device__ __forceinline__ RowTile find_tile(const ExpertArgs &g, int tile) {
+__device__ __forceinline__ int tiles_below(const ExpertArgs &g, int tiles) {
+  const int lane = threadIdx.x & 63, most = (int)g.n / TM + g.E;
+  int sum = tiles > most ? most : tiles;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(sum, o);
+    if (lane >= o) sum += u;
+  }
+  return sum;
+}
+
+// Tiles of an XCD's run: an eighth of them (2^28 at most, so that places in all runs have 32 bits;
+// the grid's size says that those of oq_route's lists are fewer).
+__device__ __forceinline__ int run_of(int rows, int nt) {
+  const int64_t run = ((int64_t)rows * nt + 7) / 8;
+  return run < 1 << 28 ? (int)run : 1 << 28;
+}
+
+// Tile of this workgroup, TM entries a row tile, nt column tiles.  Workgroups go to
+// the 8 XCDs in turn; each XCD takes a run of tiles, the columns of a row tile one
+// after the other, so that what it has in flight are the tiles of one expert or two,
+// whose rows and weights its L2 holds.  The same in every lane.
+template <int TM>
+__device__ __forceinline__ Place find_tile(const ExpertArgs &g, int nt) {
   const int lane = threadIdx.x & 63, n = (int)g.n, each = (g.E + 63) / 64;
   auto cut = [&](int v) { return v < 0 ? 0 : v < n ? v : n; };
   const int e0 = lane * each, e1 = e0 + each < g.E ? e0 + each : g.E;
-  int tiles = 0;
+  int tiles = 0;  // 16 experts of 2^28 entries at most
   if (e0 < e1) {
     int at = cut(g.offsets[e0]);
     for (int e = e0; e < e1; ++e) {
@@ -56,16 +93,14 @@ __device__ __forceinline__ RowTile find_tile(const ExpertArgs &g, int tile) {
       at = next;
     }
   }
-  int sum = tiles;  // up to and with this lane
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(sum, o);
-    if (lane >= o) sum += u;
-  }
-  const uint64_t past = __ballot(sum > tile);
-  RowTile r{0, 0, 0};
-  if (past == 0) return r;
-  const int win = __ffsll((long long)past) - 1;
+  const int sum = tiles_below<TM>(g, tiles);  // up to and with this lane
+  Place r{0, 0, 0, 0};
+  const int rows = __builtin_amdgcn_readlane(sum, 63), run = run_of(rows, nt);
+  const int in_run = blockIdx.x >> 3, id = (blockIdx.x & 7) * run + in_run;
+  const int tile = __builtin_amdgcn_readfirstlane((int)((uint32_t)id / (uint32_t)nt));
+  if (in_run >= run || tile >= rows) return r;
+  r.tn = id - tile * nt;
+  const int win = __ffsll((long long)__ballot(sum > tile)) - 1;
   int left = tile - __builtin_amdgcn_readlane(sum - tiles, win);
   const int f0 = win * each, f1 = f0 + each < g.E ? f0 + each : g.E;
   int at = cut(g.offsets[f0]);
@@ -83,7 +118,11 @@ __device__ __forceinline__ RowTile find_tile(const ExpertArgs &g, int tile) {
   return r;
 }
 
-__device__ __forceinline__ float silu_mul(float gate, float up) { return gate / (1.f + expf(-gate)) * up; }
+// silu(gate) up.  The exponential of gate log2(e) and the reciprocal are the
+// instructions', good to some 2^-22 (1 + |gate|), far below the bfloat16 result.
+__device__ __forceinline__ float silu_mul(float gate, float up) {
+  return gate * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(gate * -1.44269504088896340736f)) * up;
+}
 
 // Up to 16 MT entries times 32 (8 / KS) weight rows a workgroup: wavefront w takes
 // weight rows of block w / KS and the k blocks of 128 that are w % KS modulo KS.
@@ -98,13 +137,12 @@ __global__ void __launch_bounds__(512) gemm_experts_rows(const ExpertArgs g, con
   constexpr int NW = 8, TM = 16 * MT, GROUPS = NW / KS, DEPTH = 2;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tile = blockIdx.x / nt, tn = blockIdx.x - tile * nt;
-  const RowTile rt = find_tile<TM>(g, tile);
+  const Place rt = find_tile<TM>(g, nt);
   if (rt.rows == 0) return;
   const uint32_t lds0 = lds_addr_of(smem);
   const int r16 = lane & 15, kq = lane >> 4, ks = wave % KS;
   const int half = ACT ? g.N / 2 : g.N;
-  const int n0 = (tn * GROUPS + wave / KS) * (ACT ? 16 : 32);  // first output of this wavefront
+  const int n0 = (rt.tn * GROUPS + wave / KS) * (ACT ? 16 : 32);  // first output of this wavefront
   // weight rows of this lane's column in both blocks; rows past the end re-read the last one
   const int c0 = n0 + r16, c1 = ACT ? c0 : c0 + 16;
   const int q0 = c0 < half ? c0 : half - 1, q1 = ACT ? half + q0 : c1 < half ? c1 : half - 1;
@@ -216,15 +254,364 @@ __global__ void __launch_bounds__(512) gemm_experts_rows(const ExpertArgs g, con
     }
 }
 
+// Tiles of BM entries x BN weight rows: WM x WN wavefronts, each TI x TJ blocks of 32 x 32 on
+// v_mfma_i32_32x32x32_i8, k in stages of 128 through a ring of NSLOT LDS slots.
+template <int TI_, int TJ_, int WM_, int WN_, int NSLOT_>
+struct Tile {
+  static constexpr int TI = TI_, TJ = TJ_, WM = WM_, WN = WN_, NSLOT = NSLOT_;
+  static constexpr int NW = WM * WN, BM = 32 * TI * WM, BN = 32 * TJ * WN;
+  static constexpr int STAGE = (BM + BN) * 128;
+  static constexpr int PER = STAGE / 1024 / NW;  // copies per wavefront and stage
+  static constexpr int PER_A = BM / 8 / NW;      // of which the first are activation rows
+  static constexpr int RING = NSLOT * STAGE;
+  // behind the ring: w_scale, w1, bias of the columns, a_scale, mean of the rows, the rows' entries of
+  // this tile and the next, the experts' first places and tiles (MAX_E + 1 and MAX_E of them)
+  static constexpr int MAX_E = 1024;
+  static constexpr int AT_ROWS = RING + 3 * BN * 4, AT_ENTRY = AT_ROWS + 2 * BM * 4, AT_LISTS = AT_ENTRY + 2 * BM * 4;
+  static constexpr int LDS = AT_LISTS + (2 * MAX_E + 1) * 4;
+  static constexpr int MIN_STAGES = NSLOT + 1;  // of a tile: the next one's entries are there before its first copies
+  static_assert(PER * NW * 1024 == STAGE, "every wavefront copies the same share");
+  static_assert(BM % (8 * NW) == 0 && NW % 4 == 0, "a round of copies is all activations or all weights");
+  static_assert(NSLOT == 3, "vectors sent behind a stage's barrier are older than all that the next one leaves open");
+  static_assert(BN <= 64 * NW && BM <= 64 * NW, "one thread per column and row");
+  static_assert(TJ % 2 == 0, "gate and up blocks of a wavefront in turn");
+  static_assert(LDS <= 160 * 1024, "LDS");
+};
+
+// A persistent kernel, one workgroup a CU: the ring does not end with a tile.  Under
+// the last stages of one the first stages of the next one are copied, and what else
+// the next one needs (its entries, scales) comes through LDS as well, so that its
+// main loop starts at full pace.  Where a workgroup took one tile, 8192 x 8 entries
+// of 128 experts, 2048 -> 1536, took 313 us: 8 of a tile's 23 us passed before its
+// first product and behind its last.
+template <class C, bool ACT>
+__global__ void __launch_bounds__(64 * C::NW, C::NW / 4) gemm_experts_tile(const ExpertArgs g, const int nt, const Div per) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  constexpr int TI = C::TI, TJ = C::TJ, OUT = ACT ? C::BN / 2 : C::BN;
+  const uint32_t lds0 = lds_addr_of(smem);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 31, half = lane >> 5;
+  const int outs = ACT ? g.N / 2 : g.N;
+  float *s_ws = reinterpret_cast<float *>(smem + C::RING), *s_w1 = s_ws + C::BN, *s_b = s_w1 + C::BN;
+  float *s_al = reinterpret_cast<float *>(smem + C::AT_ROWS), *s_mu = s_al + C::BM;
+  int *s_entry = reinterpret_cast<int *>(smem + C::AT_ENTRY);  // [2][BM]
+  int *s_off = reinterpret_cast<int *>(smem + C::AT_LISTS), *s_sum = s_off + C::MAX_E + 1;
+
+  // the experts' first places, and the tiles up to and with each of them
+  const int each = (g.E + 63) / 64;
+  if (wave == 0) {
+    const int n = (int)g.n;
+    auto cut = [&](int v) { return v < 0 ? 0 : v < n ? v : n; };
+    for (int e = lane; e <= g.E; e += 64) s_off[e] = cut(g.offsets[e]);
+    const int e0 = lane * each, e1 = e0 + each < g.E ? e0 + each : g.E;
+    int tiles = 0;  // 16 experts of 2^28 entries at most
+    for (int e = e0; e < e1; ++e) {
+      const int rows = s_off[e + 1] - s_off[e];
+      tiles += rows > 0 ? (rows + C::BM - 1) / C::BM : 0;
+      s_sum[e] = tiles;
+    }
+    const int below = tiles_below<C::BM>(g, tiles) - tiles;
+    for (int e = e0; e < e1; ++e) s_sum[e] += below;
+  }
+  // what is not given is zero
+  for (int i = threadIdx.x; i < 2 * C::BN; i += 64 * C::NW) s_w1[i] = 0.f;
+  for (int i = threadIdx.x; i < C::BM; i += 64 * C::NW) s_mu[i] = 0.f;
+  __syncthreads();
+  const int tiles = __builtin_amdgcn_readfirstlane(s_sum[g.E - 1]), run = __builtin_amdgcn_readfirstlane(run_of(tiles, nt));
+  // tile `it` of this workgroup, in the order described at find_tile
+  auto find = [&](int it) {
+    Place p{0, 0, 0, 0};
+    const int in_run = (blockIdx.x >> 3) + it * (gridDim.x >> 3), id = (blockIdx.x & 7) * run + in_run;
+    const int tile = __builtin_amdgcn_readfirstlane((int)((uint32_t)id / (uint32_t)nt));
+    if (in_run >= run || tile >= tiles) return p;
+    p.tn = id - tile * nt;
+    const int last = lane * each + each - 1;
+    const uint64_t past = __ballot(s_sum[last < g.E ? last : g.E - 1] > tile);
+    const int first = (__ffsll((long long)past) - 1) * each, mine = first + (lane < each ? lane : each - 1);
+    const uint64_t in = __ballot(s_sum[mine < g.E ? mine : g.E - 1] > tile);
+    p.e = __builtin_amdgcn_readfirstlane(first + __ffsll((long long)in) - 1);
+    const int left = __builtin_amdgcn_readfirstlane(tile - (p.e ? s_sum[p.e - 1] : 0));
+    const int start = __builtin_amdgcn_readfirstlane(s_off[p.e]), end = __builtin_amdgcn_readfirstlane(s_off[p.e + 1]);
+    const int64_t at = start + (int64_t)left * C::BM;
+    if (left < 0 || at >= end) return p;  // not with oq_route's lists
+    p.p0 = (int)at;
+    p.rows = end - p.p0 < C::BM ? end - p.p0 : C::BM;
+    return p;
+  };
+  Place rt = find(0), nx = rt;
+  if (rt.rows <= 0) return;
+  auto checked = [&](int i) { return i >= 0 && i < g.n ? i : -1; };  // an entry from a list; -1: none
+  auto entry = [&](const Place &p, const int *list, int row) { return row < p.rows ? checked(list[row]) : -1; };
+  auto from = [&](int i) { return (int64_t)(i < 0 ? 0 : div_of(i, per)); };
+  // weight row of column c of the tile (with SwiGLU its blocks of 32 are gate and up rows in turn),
+  // relative to the first gate or up row; past the end the last one
+  auto weight_row = [&](const Place &p, int c) {
+    const int o = ACT ? (c >> 6) * 32 + (c & 31) : c, last = outs - p.tn * OUT - 1;
+    return o < last ? o : last;
+  };
+  auto is_up = [&](int c) { return ACT && (c >> 5 & 1); };
+
+  // This wavefront's copies: unit u = wave + NW q covers rows 8 u + lane / 8 of the
+  // stage (the tile's BM activation rows, then its BN weight rows), 1 KiB at 1024 u
+  // of the slot.  Activation rows have addresses of their own, weight rows an offset
+  // below a scalar base.  Slot `fill` takes stage `next` of the tile.
+  const int S = (g.K + 127) / 128, last_k = g.K - 128 * (S - 1);  // k of the last stage
+  int next = 0, fill = 0;
+  const int piece = 16 * ((lane & 7) ^ ((lane >> 4) | (wave & 1) << 2));  // of its row: every row of a lane has this (row >> 1) & 7
+  const int8_t *arow[C::PER_A], *base_w, *base_up;
+  uint32_t voff[C::PER - C::PER_A];
+  auto aim = [&](const Place &p, const int *list) {
+    base_w = g.w + p.e * g.w_stride + (int64_t)p.tn * OUT * g.ldw;
+    base_up = base_w + (ACT ? (int64_t)outs * g.ldw : 0);
+#pragma unroll
+    for (int q = 0; q < C::PER; ++q) {
+      const int row = 8 * (wave + C::NW * q) + (lane >> 3);
+      if (q < C::PER_A) arow[q] = g.qa + from(entry(p, list, row)) * g.lda + piece;
+      else voff[q - C::PER_A] = (uint32_t)weight_row(p, row - C::BM) * (uint32_t)g.ldw + piece;
+    }
+  };
+  const int8_t *now_w, *now_up;  // the bases of the stage whose copies are being sent
+  auto settle = [&]() { now_w = scalar(base_w), now_up = scalar(base_up); };
+  auto issue = [&](int q) {
+    const uint32_t to = lds0 + fill * C::STAGE + 1024 * wave + 1024 * C::NW * q;
+    if (q < C::PER_A) dma_lds16(arow[q], to);
+    else dma_lds16_s(is_up(8 * (wave + C::NW * q) - C::BM) ? now_up : now_w, voff[q - C::PER_A], to);
+  };
+  // what lies past K in the last stage is copied from the row's first piece of
+  // the stage and cleared in LDS (clear_tail)
+  auto tail_offsets = [&]() {
+    if (piece < last_k) return;
+#pragma unroll
+    for (int q = 0; q < C::PER_A; ++q) arow[q] -= piece;
+#pragma unroll
+    for (int q = C::PER_A; q < C::PER; ++q) voff[q - C::PER_A] -= piece;
+  };
+  // Behind the last stage of the last tile the loop goes on copying 16 bytes all
+  // over slots that nobody reads, so that it has no special stages.
+  int flip = 0;  // which entries are this tile's
+  auto advance = [&]() {
+    ++next;
+    fill = fill == C::NSLOT - 1 ? 0 : fill + 1;
+    if (next < S) {
+#pragma unroll
+      for (int q = 0; q < C::PER_A; ++q) arow[q] += 128;
+      base_w += 128;
+      base_up += 128;
+      if (next == S - 1) tail_offsets();
+    } else if (next == S) {
+      if (nx.rows > 0) {
+        aim(nx, s_entry + (flip ^ 1) * C::BM);
+        next = 0;
+      } else {
+#pragma unroll
+        for (int q = 0; q < C::PER_A; ++q) arow[q] = base_w;
+#pragma unroll
+        for (int q = C::PER_A; q < C::PER; ++q) voff[q - C::PER_A] = 0;
+      }
+    }
+  };
+  auto clear_tail = [&](int slot) {  // activations past K become zeros, each wavefront clearing what it copied
+    if (piece < last_k) return;
+#pragma unroll
+    for (int q = 0; q < C::PER_A; ++q)
+      *reinterpret_cast<v4i *>(smem + slot * C::STAGE + 1024 * (wave + C::NW * q) + 16 * lane) = (v4i){};
+  };
+  // A tile's vectors and the next one's entries, sent once every wavefront is done with the last
+  // tile's and read a barrier later.  64 columns or rows a wavefront at a time.
+  auto send_vectors = [&]() {
+    for (int u = wave; u < C::BN / 64; u += C::NW) {
+      const int c = 64 * u + lane;
+      const int64_t at = (int64_t)rt.e * g.N + rt.tn * OUT + weight_row(rt, c) + (is_up(c) ? outs : 0);
+      dma_lds4(g.w_scale + at, lds0 + C::RING + 256 * u);
+      if (g.mean) dma_lds4(g.w1 + at, lds0 + C::RING + 4 * C::BN + 256 * u);
+      if (g.bias) dma_lds4(g.bias + at, lds0 + C::RING + 8 * C::BN + 256 * u);
+    }
+    for (int u = C::NW - 1 - wave; u < C::BM / 64; u += C::NW) {
+      const int row = 64 * u + lane;
+      const int64_t at = from(entry(rt, s_entry + flip * C::BM, row));
+      dma_lds4(g.a_scale + at, lds0 + C::AT_ROWS + 256 * u);
+      if (g.mean) dma_lds4(g.mean + at, lds0 + C::AT_ROWS + 4 * C::BM + 256 * u);
+      if (nx.rows > 0)
+        dma_lds4(g.order + nx.p0 + (row < nx.rows ? row : nx.rows - 1), lds0 + C::AT_ENTRY + (flip ^ 1) * C::BM * 4 + 256 * u);
+    }
+  };
+
+  if (threadIdx.x < C::BM) s_entry[threadIdx.x] = threadIdx.x < rt.rows ? g.order[rt.p0 + threadIdx.x] : -1;
+  __syncthreads();
+  aim(rt, s_entry);
+#pragma unroll
+  for (int p = 0; p < C::NSLOT - 1; ++p) {
+    settle();
+#pragma unroll
+    for (int q = 0; q < C::PER; ++q) issue(q);
+    advance();  // not to another tile: MIN_STAGES
+  }
+
+  // fragment of 32 rows, k 32 kc + 16 half of the stage: row r of the block,
+  // piece 2 kc + half in the row's order
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  const uint8_t *fa = smem + (wm * 32 * TI + r) * 128, *fb = smem + (C::BM + wn * 32 * TJ + r) * 128;
+  const int sw = (r >> 1) & 7;  // (row >> 1) & 7 of every row that is r modulo 32
+  v16i acc[TI][TJ];
+  // One chunk of 32 k: the MFMAs of each row block under the reads of the next
+  // chunk's fragments and this wavefront's share of the next copies, spread over
+  // the first half of a stage's MFMAs.  The product is formed transposed (rows:
+  // weights), so that a lane holds one entry and four outputs in a row.
+  constexpr int GROUPS = 2 * TI;
+  auto chunk = [&](const v4i (&a)[TI], const v4i (&b)[TJ], v4i (&an)[TI], v4i (&bn)[TJ], int slot, int kc, int part) {
+    const int at = slot * C::STAGE + 16 * ((2 * kc + half) ^ sw);
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      an[i] = *reinterpret_cast<const v4i *>(fa + at + i * 4096);
+#pragma unroll
+      for (int j = i * TJ / TI; j < (i + 1) * TJ / TI; ++j) bn[j] = *reinterpret_cast<const v4i *>(fb + at + j * 4096);
+      if (part < 2) {
+#pragma unroll
+        for (int q = (part * TI + i) * C::PER / GROUPS; q < (part * TI + i + 1) * C::PER / GROUPS; ++q) issue(q);
+      }
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[j], a[i], acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  const bool vec_ok = (reinterpret_cast<uintptr_t>(g.y) & 15) == 0 && g.ldy % 8 == 0;
+  int slot = 0;
+  for (int it = 1;; ++it) {
+    nx = find(it);
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) acc[i][j] = (v16i){};
+    // The loop is turned by one chunk: when the last chunk of stage s - 1 is in
+    // registers, nobody needs its slot any more.  So there the wavefronts wait for
+    // their copies of stage s, meet, run that chunk while the fragments of stage s
+    // come in, and send the copies of stage s + NSLOT - 1 to the slot.
+    v4i a[2][TI], b[2][TJ];
+#pragma unroll
+    for (int i = 0; i < TI; ++i) a[0][i] = (v4i){};  // the chunk before stage 0
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) b[0][j] = (v4i){};
+    for (int s = 0; s < S; ++s) {
+      if (s > 0 || it == 1) wait_vm<(C::NSLOT - 2) * C::PER>();
+      asm volatile("" ::: "memory");
+      if (s == S - 1 && last_k < 128) clear_tail(slot);
+      wait_lgkm0();
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      settle();
+      if (s == 0) send_vectors();  // older than the stage's copies: there when the next barrier opens
+      chunk(a[0], b[0], a[1], b[1], slot, 0, 0);
+      chunk(a[1], b[1], a[0], b[0], slot, 1, 1);
+      advance();
+      chunk(a[0], b[0], a[1], b[1], slot, 2, 2);
+      chunk(a[1], b[1], a[0], b[0], slot, 3, 3);
+      slot = slot == C::NSLOT - 1 ? 0 : slot + 1;
+    }
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[0][j], a[0][i], acc[i][j], 0, 0, 0);
+
+    // the next tile's first stage, before stores that would have to be waited for with it
+    wait_vm<(C::NSLOT - 2) * C::PER>();
+    asm volatile("" ::: "memory");
+    // Epilogue, straight from the registers: of the four outputs that a lane has of
+    // every eight, the wavefront's halves exchange two fours, so that each stores 16
+    // bytes in a row.  Without a mean or bias their zeros are added.
+    constexpr int BLOCKS = ACT ? TJ / 2 : TJ;  // of 32 outputs a wavefront
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const int row = 32 * (wm * TI + i) + r;
+      const int en = entry(rt, s_entry + flip * C::BM, row);
+      const float al = s_al[row], mu = s_mu[row];
+      auto values = [&](int j, int e4, float (&v)[4]) {
+        const int c = 32 * (wn * TJ + j) + 8 * e4 + 4 * half;
+        const float4 s4 = *reinterpret_cast<const float4 *>(s_ws + c);
+        const float4 w4 = *reinterpret_cast<const float4 *>(s_w1 + c);
+        const float4 b4 = *reinterpret_cast<const float4 *>(s_b + c);
+        v[0] = __builtin_fmaf(mu, w4.x, al * s4.x * (float)acc[i][j][4 * e4]) + b4.x;
+        v[1] = __builtin_fmaf(mu, w4.y, al * s4.y * (float)acc[i][j][4 * e4 + 1]) + b4.y;
+        v[2] = __builtin_fmaf(mu, w4.z, al * s4.z * (float)acc[i][j][4 * e4 + 2]) + b4.z;
+        v[3] = __builtin_fmaf(mu, w4.w, al * s4.w * (float)acc[i][j][4 * e4 + 3]) + b4.w;
+      };
+#pragma unroll
+      for (int k = 0; k < BLOCKS; ++k) {
+#pragma unroll
+        for (int e8 = 0; e8 < 2; ++e8) {
+          uint32_t w[2][2];  // outputs 8 (2 e8 + x) + 4 half ..
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float v[4];
+            if constexpr (ACT) {
+              float up[4];
+              values(2 * k, 2 * e8 + x, v);
+              values(2 * k + 1, 2 * e8 + x, up);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) v[y] = silu_mul(v[y], up[y]);
+            } else {
+              values(k, 2 * e8 + x, v);
+            }
+            w[x][0] = (uint32_t)f32_to_bf16_rne(v[0]) | ((uint32_t)f32_to_bf16_rne(v[1]) << 16);
+            w[x][1] = (uint32_t)f32_to_bf16_rne(v[2]) | ((uint32_t)f32_to_bf16_rne(v[3]) << 16);
+          }
+          u32x4 o;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {  // lower lanes: outputs 16 e8 .. + 7, upper lanes the next eight
+            const auto sw2 = __builtin_amdgcn_permlane32_swap(w[0][y], w[1][y], false, false);
+            o[y] = sw2[0];
+            o[2 + y] = sw2[1];
+          }
+          if (en < 0) continue;
+          const int col = rt.tn * OUT + 32 * (wn * BLOCKS + k) + 16 * e8 + 8 * half;
+          uint16_t *dst = g.y + en * g.ldy + col;
+          if (vec_ok && col + 8 <= outs) {
+            *reinterpret_cast<u32x4 *>(dst) = o;
+          } else {
+            for (int y = 0; y < 8 && col + y < outs; ++y) dst[y] = (uint16_t)(o[y >> 1] >> (16 * (y & 1)));
+          }
+        }
+      }
+    }
+    if (nx.rows <= 0) break;
+    rt = nx;
+    flip ^= 1;
+  }
+  wait_vm<0>();  // copies into LDS that nobody waited for
+}
+
+// Most workgroups that n entries of E experts can need: row tiles times column
+// tiles, in 8 runs.
+template <int TM>
+int64_t most_tiles(const ExpertArgs &g, int64_t nt) {
+  return (nt * (g.n / TM + (g.E < g.n ? g.E : g.n)) + 7) / 8 * 8;
+}
+
+// Tiles need more than NSLOT stages.
+template <class C, bool ACT>
+hipError_t launch_tile(const ExpertArgs &g, hipStream_t stream) {
+  static std::atomic<bool> attr_set[64];
+  const hipError_t e = lds_limit_once((const void *)gemm_experts_tile<C, ACT>, C::LDS, attr_set);
+  if (e != hipSuccess) return e;
+  const int64_t nt = ((ACT ? g.N / 2 : g.N) + (ACT ? C::BN / 2 : C::BN) - 1) / (ACT ? C::BN / 2 : C::BN);
+  int64_t grid = most_tiles<C::BM>(g, nt);
+  if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
+  if (grid > device_cus() / 8 * 8) grid = device_cus() / 8 * 8;
+  hipLaunchKernelGGL((gemm_experts_tile<C, ACT>), dim3((unsigned)grid), dim3(64 * C::NW), C::LDS, stream, g, (int)nt, div_by((uint32_t)g.per));
+  return hipGetLastError();
+}
+
 template <int MT, int KS, bool ACT>
 hipError_t launch_rows(const ExpertArgs &g, hipStream_t stream) {
   constexpr int TM = 16 * MT, OUT = (ACT ? 16 : 32) * (8 / KS), PART = 8 * MT * 2 * 1024;
-  const int64_t nt = ((ACT ? g.N / 2 : g.N) + OUT - 1) / OUT, mt = g.n / TM + (g.E < g.n ? g.E : g.n);
-  if (nt * mt > 0x7fffffff) return hipErrorInvalidConfiguration;
+  const int64_t nt = ((ACT ? g.N / 2 : g.N) + OUT - 1) / OUT, grid = most_tiles<TM>(g, nt);
+  if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
   int ch = 65536 / TM / 1024 * 1024;
   if (ch > (g.K + 1023) / 1024 * 1024) ch = (g.K + 1023) / 1024 * 1024;
   const size_t lds = (size_t)TM * ch > PART || KS == 1 ? (size_t)TM * ch : PART;
-  hipLaunchKernelGGL((gemm_experts_rows<MT, KS, ACT>), dim3((unsigned)(nt * mt)), dim3(512), lds, stream, g, ch, (int)nt,
+  hipLaunchKernelGGL((gemm_experts_rows<MT, KS, ACT>), dim3((unsigned)grid), dim3(512), lds, stream, g, ch, (int)nt,
                      div_by((uint32_t)g.per));
   return hipGetLastError();
 }
@@ -232,7 +619,10 @@ hipError_t launch_rows(const ExpertArgs &g, hipStream_t stream) {
 template <bool ACT>
 hipError_t launch(const ExpertArgs &g, hipStream_t stream) {
   if (g.n <= 8 * (int64_t)g.E) return launch_rows<1, 2, ACT>(g, stream);
-  return launch_rows<4, 1, ACT>(g, stream);
+  if (g.n <= 32 * (int64_t)g.E) return launch_rows<4, 1, ACT>(g, stream);
+  using Big = Tile<2, 2, 2, 4, 3>;
+  if (g.K <= 128 * (Big::MIN_STAGES - 1)) return launch_rows<4, 1, ACT>(g, stream);
+  return launch_tile<Big, ACT>(g, stream);
 }
 
 }  // namespace

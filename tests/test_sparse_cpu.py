@@ -31,7 +31,7 @@ ROUTE = dict(logits=P, dtype=oq.OQ_F32, ld=64, T=100, mask=None, r=_router(), id
     (dict(r=_router(groups=8, top_groups=8, group_best=3)), INV), (dict(r=_router(groups=64, top_groups=8, group_best=2)), INV),
     (dict(r=_router(groups=8, top_groups=2, k=17)), INV), (dict(r=_router(experts=1024, groups=2, top_groups=1)), UNS),
     (dict(r=_router(factor=float("nan"))), INV), (dict(r=_router(factor=float("inf"))), INV), (dict(r=_router(bias=0x100001)), ALN),
-    (dict(r=_router(k=65)), UNS), (dict(r=_router(experts=3, k=4)), INV), (dict(T=(1 << 28) + 1), UNS), (dict(T=(1 << 63) - 1), UNS),
+    (dict(r=_router(k=65)), UNS), (dict(r=_router(experts=3, k=4)), INV), (dict(T=(1 << 26) + 1), UNS), (dict(T=(1 << 63) - 1), UNS),
     (dict(dtype=0), INV), (dict(dtype=3), INV), (dict(offsets=None), INV), (dict(order=None), INV), (dict(logits=None), INV), (dict(ids=None), INV),
     (dict(weights=None), INV), (dict(ld=63), INV), (dict(ld=(1 << 63) - 1), UNS), (dict(logits=P1), ALN), (dict(logits=P2), ALN), (dict(ids=P2), ALN),
     (dict(weights=P2), ALN), (dict(offsets=P2), ALN), (dict(order=P2), ALN), (dict(ws=P4), ALN), (dict(ws=None), WS), (dict(ws_bytes=0), WS)])
@@ -54,7 +54,7 @@ EX = dict(qa=P, lda=1024, a_scale=P, rows=10, K=1024, w=P, ldw=1024, w_stride=64
 @pytest.mark.parametrize("change,code", [
     (dict(rows=-1), INV), (dict(n=-1), INV), (dict(N=-1), INV), (dict(E=0), INV), (dict(per=0), INV), (dict(act=2), INV), (dict(act=-1), INV),
     (dict(act=oq.OQ_ACT_SWIGLU, N=63), INV), (dict(K=0), UNS), (dict(K=8), UNS), (dict(K=1000), UNS), (dict(K=131072, lda=131072, ldw=131072), UNS),
-    (dict(E=1025), UNS), (dict(N=(1 << 20) + 2), UNS), (dict(mean=P), INV), (dict(w1=P), INV), (dict(n=(1 << 30) + 1, rows=1 << 30), UNS),
+    (dict(E=1025), UNS), (dict(N=(1 << 20) + 2), UNS), (dict(mean=P), INV), (dict(w1=P), INV), (dict(n=(1 << 28) + 1, rows=1 << 30), UNS),
     (dict(rows=9), INV), (dict(per=1), INV), (dict(n=(1 << 63) - 1, per=2), UNS), (dict(qa=None), INV), (dict(a_scale=None), INV), (dict(w=None), INV),
     (dict(w_scale=None), INV), (dict(offsets=None), INV), (dict(order=None), INV), (dict(y=None), INV), (dict(lda=1008), INV), (dict(ldw=1008), INV),
     (dict(lda=(1 << 23) + 16), UNS), (dict(ldw=1 << 24, w_stride=1 << 40), UNS), (dict(w_stride=64 * 1024 - 16), INV), (dict(w_stride=-(1 << 40)), INV),
