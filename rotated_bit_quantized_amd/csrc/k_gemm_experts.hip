@@ -318,22 +318,28 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW / 4) gemm_experts_tile(const
   for (int i = threadIdx.x; i < C::BM; i += 64 * C::NW) s_mu[i] = 0.f;
   __syncthreads();
   const int tiles = __builtin_amdgcn_readfirstlane(s_sum[g.E - 1]), run = __builtin_amdgcn_readfirstlane(run_of(tiles, nt));
-  // tile `it` of this workgroup, in the order described at find_tile
+  // Tile `it` of this workgroup: as at find_tile an XCD takes a run of tiles, here those of an expert in
+  // bands of 8 row tiles, column by column, so that many columns share rows and weights as well
+  // (8192 rows of one expert, 4096 -> 14336: 509 us; row by row 590).
   auto find = [&](int it) {
     Place p{0, 0, 0, 0};
     const int in_run = (blockIdx.x >> 3) + it * (gridDim.x >> 3), id = (blockIdx.x & 7) * run + in_run;
     const int tile = __builtin_amdgcn_readfirstlane((int)((uint32_t)id / (uint32_t)nt));
     if (in_run >= run || tile >= tiles) return p;
-    p.tn = id - tile * nt;
     const int last = lane * each + each - 1;
     const uint64_t past = __ballot(s_sum[last < g.E ? last : g.E - 1] > tile);
     const int first = (__ffsll((long long)past) - 1) * each, mine = first + (lane < each ? lane : each - 1);
     const uint64_t in = __ballot(s_sum[mine < g.E ? mine : g.E - 1] > tile);
     p.e = __builtin_amdgcn_readfirstlane(first + __ffsll((long long)in) - 1);
-    const int left = __builtin_amdgcn_readfirstlane(tile - (p.e ? s_sum[p.e - 1] : 0));
+    const int before = __builtin_amdgcn_readfirstlane(p.e ? s_sum[p.e - 1] : 0), own = __builtin_amdgcn_readfirstlane(s_sum[p.e]) - before;
     const int start = __builtin_amdgcn_readfirstlane(s_off[p.e]), end = __builtin_amdgcn_readfirstlane(s_off[p.e + 1]);
-    const int64_t at = start + (int64_t)left * C::BM;
-    if (left < 0 || at >= end) return p;  // not with oq_route's lists
+    // bands of 8 row tiles, column by column
+    const uint32_t local = (uint32_t)(id - before * nt), wide = 8 * (uint32_t)nt;
+    const uint32_t band = __builtin_amdgcn_readfirstlane((int)(local / wide)), in_band = local - band * wide;
+    const uint32_t high = own - 8 * (int)band < 8 ? own - 8 * (int)band : 8;
+    p.tn = __builtin_amdgcn_readfirstlane((int)(in_band / (high ? high : 1)));
+    const int64_t at = start + ((int64_t)8 * band + in_band - p.tn * high) * C::BM;
+    if (at < start || at >= end || p.tn >= nt) return p;  // not with oq_route's lists
     p.p0 = (int)at;
     p.rows = end - p.p0 < C::BM ? end - p.p0 : C::BM;
     return p;
@@ -476,6 +482,7 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW / 4) gemm_experts_tile(const
   };
 
   const bool vec_ok = (reinterpret_cast<uintptr_t>(g.y) & 15) == 0 && g.ldy % 8 == 0;
+  constexpr int BLOCKS = ACT ? TJ / 2 : TJ;  // of 32 outputs a wavefront
   int slot = 0;
   for (int it = 1;; ++it) {
     nx = find(it);
@@ -521,7 +528,6 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW / 4) gemm_experts_tile(const
     // Epilogue, straight from the registers: of the four outputs that a lane has of
     // every eight, the wavefront's halves exchange two fours, so that each stores 16
     // bytes in a row.  Without a mean or bias their zeros are added.
-    constexpr int BLOCKS = ACT ? TJ / 2 : TJ;  // of 32 outputs a wavefront
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
       const int row = 32 * (wm * TI + i) + r;
@@ -564,9 +570,9 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW / 4) gemm_experts_tile(const
             o[y] = sw2[0];
             o[2 + y] = sw2[1];
           }
-          if (en < 0) continue;
           const int col = rt.tn * OUT + 32 * (wn * BLOCKS + k) + 16 * e8 + 8 * half;
           uint16_t *dst = g.y + en * g.ldy + col;
+          if (en < 0) continue;
           if (vec_ok && col + 8 <= outs) {
             *reinterpret_cast<u32x4 *>(dst) = o;
           } else {
@@ -618,11 +624,24 @@ hipError_t launch_rows(const ExpertArgs &g, hipStream_t stream) {
 
 template <bool ACT>
 hipError_t launch(const ExpertArgs &g, hipStream_t stream) {
-  if (g.n <= 8 * (int64_t)g.E) return launch_rows<1, 2, ACT>(g, stream);
-  if (g.n <= 32 * (int64_t)g.E) return launch_rows<4, 1, ACT>(g, stream);
   using Big = Tile<2, 2, 2, 4, 3>;
-  if (g.K <= 128 * (Big::MIN_STAGES - 1)) return launch_rows<4, 1, ACT>(g, stream);
-  return launch_tile<Big, ACT>(g, stream);
+  const int64_t cus = device_cus(), outs = ACT ? g.N / 2 : g.N, reached = g.E < g.n ? g.E : g.n;  // experts with entries, at most
+  const int64_t tiles = reached * ((g.N + Big::BN - 1) / Big::BN);
+  // The persistent tiles stream weights as well as anything (16 x 8 entries of 128 experts,
+  // 2048 -> 1536: 46.5 us, 5.6 TB/s, gemm_experts_rows 51; 64 x 8 71 and 76; 256 x 8 78 and 98),
+  // except where there are too few for half of the CUs: 1 x 8 19.3, rows 11.2; 2 x 2 of 8
+  // experts, 4096 -> 7168, 30 and 23; 4 x 2 42 and 50.
+  const bool small = g.K <= 128 * (Big::MIN_STAGES - 1);
+  if (!small && (tiles > cus / 2 || g.n > 32 * (int64_t)g.E)) return launch_tile<Big, ACT>(g, stream);
+  if (g.n > 16 * (int64_t)g.E && small) return launch_rows<4, 1, ACT>(g, stream);
+  // k is split over as many wavefronts as leave the CUs one workgroup each (1 x 4 of 60, 1408 ->
+  // 2048: 7.1 us with 8, 8.3 with 4, 15 with 1; 4 x 4: 18.6 with 8, 12.9 with 2)
+  const int64_t rows = reached + g.n / 16, blocks = (outs + (ACT ? 15 : 31)) / (ACT ? 16 : 32);
+  auto fits = [&](int64_t ks) { return rows * ((blocks * ks + 7) / 8) <= cus + cus / 8; };
+  if (fits(8)) return launch_rows<1, 8, ACT>(g, stream);
+  if (fits(4)) return launch_rows<1, 4, ACT>(g, stream);
+  if (fits(2)) return launch_rows<1, 2, ACT>(g, stream);
+  return launch_rows<1, 1, ACT>(g, stream);
 }
 
 }  // namespace
