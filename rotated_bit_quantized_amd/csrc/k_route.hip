@@ -10,7 +10,7 @@
 // (six cross-lane steps), one ballot and a shift of the winner's list.  The
 // groups' scores come from the same layout, which gives each group lanes of its
 // own.  The choices are to be those of the exact scores: float32 scores carry an
-// error of less than 2^-18 (1 + |c|), so wherever two neighbours among the
+// error of less than 2^-19 (1 + |c|), so wherever two neighbours among the
 // chosen, the first one left out and the groups at the border are nearer than
 // twice that, the token is done again in float64 (one token in some hundreds; a
 // choice by the logits themselves compares exactly and never does).
@@ -27,9 +27,12 @@
 namespace oq {
 namespace {
 
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
 constexpr int WAVES = 16, THREADS = 64 * WAVES;
-// Up to SOLO tokens one workgroup routes and lists; CHUNKS: most workgroups else.
-constexpr int SOLO = 32, CHUNKS = 512;
+// Up to SOLO tokens one workgroup routes and lists; CHUNKS, LISTS: most workgroups
+// of the two launches else.
+constexpr int SOLO = 32, CHUNKS = 512, LISTS = 256;
 
 struct Layout {
   int lanes;  // of a group
@@ -74,37 +77,57 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 __device__ __forceinline__ uint64_t wave_max(uint64_t v) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) {
-    const uint64_t w = (uint64_t)__shfl_xor((long long)v, o);
-    v = v > w ? v : w;
-  }
-  return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
-         (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+  const uint32_t hi = wave_max((uint32_t)(v >> 32));
+  return (uint64_t)hi << 32 | wave_max((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
 }
-template <class F>
-__device__ __forceinline__ F wave_sum(F v) {
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_other(float v, float none) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(none), __float_as_int(v), CTRL, ROWS, 0xF, false));
+}
+// the sum over the wavefront and the largest number, in every lane
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp_other<0xB1, 0xF>(v, 0.f);
+  v += dpp_other<0x4E, 0xF>(v, 0.f);
+  v += dpp_other<0x141, 0xF>(v, 0.f);
+  v += dpp_other<0x140, 0xF>(v, 0.f);
+  v += dpp_other<0x142, 0xA>(v, 0.f);
+  v += dpp_other<0x143, 0xC>(v, 0.f);
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ float wave_fmax(float v) {
+  v = fmaxf(v, dpp_other<0xB1, 0xF>(v, v));
+  v = fmaxf(v, dpp_other<0x4E, 0xF>(v, v));
+  v = fmaxf(v, dpp_other<0x141, 0xF>(v, v));
+  v = fmaxf(v, dpp_other<0x140, 0xF>(v, v));
+  v = fmaxf(v, dpp_other<0x142, 0xA>(v, v));
+  v = fmaxf(v, dpp_other<0x143, 0xC>(v, v));
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
   return v;
 }
-__device__ __forceinline__ float wave_fmax(float v) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
+__device__ __forceinline__ uint32_t read_lane(uint32_t v, int lane) { return (uint32_t)__builtin_amdgcn_readlane((int)v, lane); }
+__device__ __forceinline__ uint64_t read_lane(uint64_t v, int lane) {
+  return (uint64_t)read_lane((uint32_t)(v >> 32), lane) << 32 | read_lane((uint32_t)v, lane);
 }
 __device__ __forceinline__ float exp_(float v) { return expf(v); }
 __device__ __forceinline__ double exp_(double v) { return exp(v); }
-__device__ __forceinline__ bool near(float a, float b) { return !(a - b > 0x1p-17f * (1.f + fabsf(a) + fabsf(b))); }
+// Whether float32 scores (sums of n of them) may be in the wrong order: each is off by less than
+// 2^-19 (1 + |c|), softmax scores by the most, 28 units of 2^-24 (their sum goes over
+// at most 16 terms a lane and 6 steps, the exponential and the quotient are 6 more).
+__device__ __forceinline__ bool near(float a, float b, float n) { return !(a - b > 0x1p-18f * n * (1.f + fabsf(a) + fabsf(b))); }
 
-// The k choices of a token in F; lane j returns the j-th (others: -1).  x, bias:
-// the lane's logits and biases, experts first + i, i < n.
-template <int NPL, class F>
+// The k choices of a token in F; lane j returns the j-th (others: -1) and, where
+// the logits themselves are compared (PLAIN: no bias, no groups), its logit.  x,
+// bias: the lane's logits and biases, experts first + i, i < n.
+template <int NPL, bool PLAIN, class F>
 __device__ __forceinline__ int choose(const float (&x)[NPL], const float (&bias)[NPL], int first, int n, float xmax,
-                                      const Work &g, bool &sure) {
+                                      const Work &g, bool &sure, float &logit) {
   const oq_router &r = g.a.r;
   const int lane = threadIdx.x & 63;
-  const bool biased = r.bias != nullptr, grouped = g.l.groups > 1, sums = grouped && r.group_best == 2;
+  const bool biased = !PLAIN && r.bias != nullptr, grouped = !PLAIN && g.l.groups > 1, sums = grouped && r.group_best == 2;
   using K = decltype(key_of(F()));
   F sc[NPL];
 #pragma unroll
@@ -127,7 +150,7 @@ __device__ __forceinline__ int choose(const float (&x)[NPL], const float (&bias)
 #pragma unroll
     for (int i = 0; i < NPL; ++i) sc[i] = biased ? sc[i] + (F)bias[i] : sc[i];
   }
-  bool exact = sizeof(F) == 8 || !biased;
+  const bool exact = sizeof(F) == 8 || !biased;
   sure = true;
   bool open = n > 0;
   if (grouped) {
@@ -151,7 +174,7 @@ __device__ __forceinline__ int choose(const float (&x)[NPL], const float (&bias)
     const K mine = key_of(score);
     int rank = 0;
     for (int j = 0; j < g.l.groups; ++j) {
-      const K other = __shfl(mine, j * g.l.lanes);
+      const K other = read_lane(mine, j * g.l.lanes);
       rank += other > mine || (other == mine && j < group);
     }
     const bool head = sub == 0 && group < g.l.groups;
@@ -160,7 +183,7 @@ __device__ __forceinline__ int choose(const float (&x)[NPL], const float (&bias)
     if (sizeof(F) == 4 && (biased || sums)) {
       const int last = __ffsll((long long)__ballot(head && rank == r.top_groups - 1)) - 1;
       const int next = __ffsll((long long)__ballot(head && rank == r.top_groups)) - 1;
-      if (near((float)__shfl(score, last), (float)__shfl(score, next))) sure = false;
+      if (near((float)__shfl(score, last), (float)__shfl(score, next), 2.f)) sure = false;
     }
     if (!biased && sums) {
 #pragma unroll
@@ -188,12 +211,15 @@ __device__ __forceinline__ int choose(const float (&x)[NPL], const float (&bias)
   for (int j = 0; j <= r.k; ++j) {
     if (j == r.k && exact) break;  // the first one left out, to see how near it is
     const K m = wave_max(key[0]);
-    if (sizeof(F) == 4 && !exact && j && m && near(value_of((uint32_t)before), value_of((uint32_t)m))) sure = false;
+    if (sizeof(F) == 4 && !exact && j && m && near(value_of((uint32_t)before), value_of((uint32_t)m), 1.f)) sure = false;
     if (j == r.k) break;
     before = m;
     const int win = __ffsll((long long)__ballot(key[0] == m)) - 1;
     const int id = __builtin_amdgcn_readlane(at[0], win);
-    if (lane == j) chosen = id;
+    if (lane == j) {
+      chosen = id;
+      if constexpr (PLAIN) logit = value_of(m);
+    }
     if (lane == win) {
 #pragma unroll
       for (int i = 0; i + 1 < NPL; ++i) key[i] = key[i + 1], at[i] = at[i + 1];
@@ -221,7 +247,7 @@ __device__ __forceinline__ float weight(float x, bool mine, float xmax, float to
   return r.factor * (r.renorm ? s / wave_sum(s) : s);
 }
 
-template <int NPL, int W, class T>
+template <int NPL, int W, bool PLAIN, class T>
 __device__ __forceinline__ void route_tokens(const Work &g, int64_t t0, int64_t t1, int *hist) {
   const RouteArgs &a = g.a;
   const oq_router &r = a.r;
@@ -251,7 +277,8 @@ __device__ __forceinline__ void route_tokens(const Work &g, int64_t t0, int64_t 
     int id = -1;
     float w = 0.f;
     if (!a.mask || a.mask[t]) {
-      const bool softmax = r.score == OQ_SCORE_SOFTMAX, scores = r.bias || (g.l.groups > 1 && r.group_best == 2);
+      const bool softmax = r.score == OQ_SCORE_SOFTMAX;
+      const bool scores = !PLAIN && (r.bias || (g.l.groups > 1 && r.group_best == 2));
       float xmax = -INFINITY, total = 0.f;
       bool nan = false;
       if (softmax) {
@@ -266,14 +293,16 @@ __device__ __forceinline__ void route_tokens(const Work &g, int64_t t0, int64_t 
         }
       }
       bool sure;
-      id = choose<NPL, float>(x, bias, first, n, xmax, g, sure);
-      if (!sure) id = choose<NPL, double>(x, bias, first, n, xmax, g, sure);
-      const bool mine = lane < r.k;
       float chosen = 0.f;
-      if (mine) {
-        const T v = static_cast<const T *>(a.logits)[t * a.ld + id];
-        if constexpr (sizeof(T) == 2) chosen = __uint_as_float((uint32_t)v << 16);
-        else chosen = v;
+      id = choose<NPL, PLAIN, float>(x, bias, first, n, xmax, g, sure, chosen);
+      const bool mine = lane < r.k;
+      if constexpr (!PLAIN) {
+        if (!sure) id = choose<NPL, PLAIN, double>(x, bias, first, n, xmax, g, sure, chosen);
+        if (mine) {
+          const T v = static_cast<const T *>(a.logits)[t * a.ld + id];
+          if constexpr (sizeof(T) == 2) chosen = __uint_as_float((uint32_t)v << 16);
+          else chosen = v;
+        }
       }
       w = weight(chosen, mine, xmax, total, nan, r);
     }
@@ -349,7 +378,7 @@ __device__ __forceinline__ void fill_tail(const RouteArgs &a, int64_t i0, int64_
 }
 
 // W wavefronts: 16, or 8 where a lane's lists need the registers of two.
-template <int NPL, int W, class T>
+template <int NPL, int W, bool PLAIN, class T>
 __global__ void __launch_bounds__(64 * W) route_kernel(const Work g) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   int *hist = reinterpret_cast<int *>(smem);
@@ -361,7 +390,7 @@ __global__ void __launch_bounds__(64 * W) route_kernel(const Work g) {
     __syncthreads();
   }
   const int64_t t0 = blockIdx.x * g.tokens, t1 = t0 + g.tokens < a.T ? t0 + g.tokens : a.T;
-  route_tokens<NPL, W, T>(g, t0, t1, lists ? hist : nullptr);
+  route_tokens<NPL, W, PLAIN, T>(g, t0, t1, lists ? hist : nullptr);
   if (!lists) return;
   __syncthreads();
   if (W < WAVES || !g.solo) {
@@ -384,39 +413,54 @@ __global__ void __launch_bounds__(THREADS) route_lists_kernel(const Work g) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ int wave_sums[WAVES];
   const RouteArgs &a = g.a;
-  const int E = a.r.experts, chunk = blockIdx.x, chunks = g.chunks;
+  // this workgroup's chunks; every one of them before it costs a row of counts
+  const int E = a.r.experts, chunks = g.chunks, share = (chunks + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int chunk = blockIdx.x * share;
   int *base = reinterpret_cast<int *>(smem), *total = base + E;
   if (threadIdx.x < E) base[threadIdx.x] = total[threadIdx.x] = 0;
   __syncthreads();
-  // rows of counts in turn over the thread groups of E
-  const int rows = THREADS / E, row = threadIdx.x / E, e = threadIdx.x - row * E;
-  if (row < rows) {
-    int before = 0, sum = 0;
-#pragma unroll 8
+  // rows of counts in turn over groups of threads, four counts a load where they allow
+  auto add_rows = [&](auto load, int cols, int width) {
+    const int rows = THREADS / cols < 64 ? THREADS / cols : 64;  // more would meet in the same few sums
+    const int row = threadIdx.x / cols, col = threadIdx.x - row * cols;
+    if (row >= rows) return;
+    i32x4 before = {0, 0, 0, 0}, sum = {0, 0, 0, 0};
+#pragma unroll 16
     for (int c = row; c < chunks; c += rows) {
-      const int v = g.hist[(int64_t)c * E + e];
-      before += c < chunk ? v : 0;
+      const i32x4 v = load((int64_t)c * E + col * width);
+      before += c < chunk ? v : (i32x4){0, 0, 0, 0};
       sum += v;
     }
-    atomicAdd(base + e, before);
-    atomicAdd(total + e, sum);
-  }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j >= width) continue;
+      atomicAdd(base + col * width + j, before[j]);
+      atomicAdd(total + col * width + j, sum[j]);
+    }
+  };
+  if (E % 4 == 0) add_rows([&](int64_t i) { return *reinterpret_cast<const i32x4 *>(g.hist + i); }, E / 4, 4);
+  else add_rows([&](int64_t i) { return (i32x4){g.hist[i], 0, 0, 0}; }, E, 1);
   __syncthreads();
   int all;
   const int start = scan_block(threadIdx.x < E ? total[threadIdx.x] : 0, wave_sums, all);
   if (threadIdx.x < E) {
     base[threadIdx.x] += start;
-    if (chunk == 0) a.offsets[threadIdx.x] = start;
+    if (blockIdx.x == 0) a.offsets[threadIdx.x] = start;
   }
-  if (chunk == 0 && threadIdx.x == 0) a.offsets[E] = all;
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[E] = all;
   __syncthreads();
-  const int64_t t0 = chunk * g.tokens, t1 = t0 + g.tokens < a.T ? t0 + g.tokens : a.T;
+  const int64_t t0 = chunk * g.tokens < a.T ? chunk * g.tokens : a.T, t1 = t0 + share * g.tokens < a.T ? t0 + share * g.tokens : a.T;
   scatter(a, t0 * a.r.k, t1 * a.r.k, base, reinterpret_cast<uint16_t *>(total + E));
   fill_tail(a, t0 * a.r.k, t1 * a.r.k, all);
 }
 
-int64_t chunk_tokens(int64_t T) {
-  const int64_t each = (T + CHUNKS - 1) / CHUNKS;
+// Where logits alone are compared two workgroups fit a CU; with scores and their
+// float64 form one does, and half as many chunks are faster (16384 tokens of 256
+// experts in groups: 43 us, 50 with 512 chunks; logits of 32768 x 128: 32 and 30).
+bool plain(const oq_router &r) { return !r.bias && r.top_groups == r.groups; }
+
+int64_t chunk_tokens(int64_t T, const oq_router &r) {
+  const int64_t most = plain(r) ? CHUNKS : CHUNKS / 2, each = (T + most - 1) / most;
   return each < WAVES ? WAVES : (each + WAVES - 1) / WAVES * WAVES;
 }
 
@@ -432,11 +476,11 @@ Layout layout_of(const oq_router &r) {
 
 bool solo(int64_t T, const Layout &l) { return T <= SOLO && l.c <= 8; }
 
-template <class T>
+template <bool PLAIN, class T>
 hipError_t launch(const Work &g, unsigned chunks, hipStream_t stream) {
   const int E = g.a.r.experts;
   const size_t lds = g.a.offsets ? (size_t)E * 4 + (g.solo ? (size_t)E * 2 * WAVES : 0) : 0;
-#define ROUTE(NPL, W) hipLaunchKernelGGL((route_kernel<NPL, W, T>), dim3(chunks), dim3(64 * W), lds, stream, g)
+#define ROUTE(NPL, W) hipLaunchKernelGGL((route_kernel<NPL, W, PLAIN, T>), dim3(chunks), dim3(64 * W), lds, stream, g)
   if (g.l.c <= 1) ROUTE(1, 16);
   else if (g.l.c <= 2) ROUTE(2, 16);
   else if (g.l.c <= 4) ROUTE(4, 16);
@@ -450,22 +494,23 @@ hipError_t launch(const Work &g, unsigned chunks, hipStream_t stream) {
 
 size_t route_ws(int64_t T, const oq_router &r) {
   if (solo(T, layout_of(r))) return 0;
-  const int64_t tokens = chunk_tokens(T);
+  const int64_t tokens = chunk_tokens(T, r);
   return (size_t)((T + tokens - 1) / tokens) * r.experts * 4;
 }
 
 hipError_t launch_route(const RouteArgs &a, bool bf16, void *ws, hipStream_t stream) {
   Work g{a, layout_of(a.r), a.T, static_cast<int32_t *>(ws), 0, 0};
   g.solo = a.offsets && solo(a.T, g.l);
-  if (!g.solo) g.tokens = chunk_tokens(a.T);
+  if (!g.solo) g.tokens = chunk_tokens(a.T, a.r);
   g.chunks = g.solo ? 1 : (int)((a.T + g.tokens - 1) / g.tokens);
   if (g.chunks) {  // none: no token, whose empty lists come from the second launch
-    const hipError_t e = bf16 ? launch<uint16_t>(g, g.chunks, stream) : launch<float>(g, g.chunks, stream);
+    const hipError_t e = plain(a.r) ? bf16 ? launch<true, uint16_t>(g, g.chunks, stream) : launch<true, float>(g, g.chunks, stream)
+                         : bf16 ? launch<false, uint16_t>(g, g.chunks, stream) : launch<false, float>(g, g.chunks, stream);
     if (e != hipSuccess) return e;
   }
   if (!a.offsets || g.solo) return hipSuccess;
   const size_t lds = (size_t)a.r.experts * (8 + 2 * WAVES);
-  hipLaunchKernelGGL(route_lists_kernel, dim3(g.chunks ? g.chunks : 1), dim3(THREADS), lds, stream, g);
+  hipLaunchKernelGGL(route_lists_kernel, dim3(g.chunks < 1 ? 1 : g.chunks < LISTS ? g.chunks : LISTS), dim3(THREADS), lds, stream, g);
   return hipGetLastError();
 }
 
