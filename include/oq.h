@@ -784,7 +784,7 @@ int oq_residual_norm(const uint16_t *y, int64_t y_ld, int32_t k, const float *we
  * Sums are float32; values are off by about 1e-7 of lse - scale x, absolute.
  * Each output nullable but logprob and rank with n > 0, and the top pair with
  * top > 0.  Rows need the alignment of their element only.
- * 1 <= V <= 2^22, 0 <= n <= 64, 0 <= top <= 32, top <= V, scale > 0 and its
+ * 1 <= V <= 2^21, 0 <= n <= 64, 0 <= top <= 32, top <= V, scale > 0 and its
  * product with log2(e) finite.
  * ws: device scratch of oq_logprobs_ws_bytes(T, V, n, top) bytes, 16-byte
  * aligned (may be 0).

@@ -58,8 +58,8 @@ int check_rows(const char *fn, const char *name, const void *x, int64_t ld, int6
 
 int check_logprobs(const char *fn, int64_t T, int32_t V, int32_t n, int32_t top) {
   if (T < 0 || V < 1 || n < 0 || top < 0) return fail(OQ_ERR_INVALID_ARG, "%s: T=%lld, V=%d, n=%d, top=%d", fn, (long long)T, V, n, top);
-  if (V > (1 << 22) || n > 64 || top > 32)
-    return fail(OQ_ERR_UNSUPPORTED, "%s: V=%d exceeds 2^22, n=%d exceeds 64 or top=%d exceeds 32", fn, V, n, top);
+  if (V > (1 << 21) || n > 64 || top > 32)
+    return fail(OQ_ERR_UNSUPPORTED, "%s: V=%d exceeds 2^21, n=%d exceeds 64 or top=%d exceeds 32", fn, V, n, top);
   if (top > V) return fail(OQ_ERR_INVALID_ARG, "%s: top=%d of %d", fn, top, V);
   if (T > ((int64_t)1 << 24)) return fail(OQ_ERR_UNSUPPORTED, "%s: T=%lld exceeds 2^24", fn, (long long)T);
   return OQ_OK;

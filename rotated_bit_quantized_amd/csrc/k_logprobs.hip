@@ -20,7 +20,7 @@
 //
 // Rows of several parts leave statistics and sorted candidates for a second
 // launch, a wavefront a row.
-#include "oq_internal.h"
+#include "sparse_plan.h"
 
 namespace oq {
 namespace {
@@ -508,42 +508,16 @@ __global__ void __launch_bounds__(64) logprobs_join(const LogprobArgs a, const S
   }
 }
 
-// Wavefronts of a workgroup, pieces a thread and parts a row.  lead: elements by
-// which rows begin inside a piece.
-struct Plan {
-  int waves, nv, parts, each;  // each: pieces of a part
-};
-Plan plan_for(int64_t T, int V, int bytes, int lead) {
-  const int ve = 16 / bytes;
-  const int pieces = (V + lead + ve - 1) / ve;
-  // Few rows that 16 wavefronts can hold: one launch.  Else as many pieces a thread
-  // as there are, up to 8, while the parts of all rows still are two workgroups a CU.
-  if (T <= 2 * device_cus() && pieces <= 1024 * 8 && pieces > 512) return Plan{16, 8, 1, pieces};
-  Plan p{8, 8, 1, 0};
-  for (;; p.nv /= 2) {
-    p.parts = (pieces + 512 * p.nv - 1) / (512 * p.nv);
-    if (p.nv == 1 || T * p.parts >= 2 * device_cus()) break;
-  }
-  p.each = (pieces + p.parts - 1) / p.parts;
-  return p;
-}
-
-size_t round16(size_t n) { return (n + 15) & ~(size_t)15; }
-size_t scratch_bytes(int64_t T, int parts, int n, int top) {
-  if (parts == 1) return 0;
-  const size_t rows = (size_t)T * parts;
-  return rows * sizeof(Part) + round16(rows * top * 8) + round16(rows * n * 4);
-}
-
 template <class T>
 hipError_t launch(const LogprobArgs &a, void *ws, hipStream_t stream) {
   const int ve = 16 / sizeof(T), lead = (int)(reinterpret_cast<uintptr_t>(a.logits) & 15) / (int)sizeof(T);
-  const Plan p = plan_for(a.T, a.V, sizeof(T), a.T == 1 || a.ld % ve == 0 ? lead : ve - 1);
+  const LogprobPlan p = logprob_plan(a.T, a.V, sizeof(T), a.T == 1 || a.ld % ve == 0 ? lead : ve - 1);
   const size_t rows = (size_t)a.T * p.parts;
   if (rows > 0x7fffffff) return hipErrorInvalidConfiguration;
   char *base = static_cast<char *>(ws);
-  const Scratch w{reinterpret_cast<Part *>(base), reinterpret_cast<uint64_t *>(base + rows * sizeof(Part)),
-                  reinterpret_cast<int32_t *>(base + rows * sizeof(Part) + round16(rows * a.top * 8))};
+  const LogprobScratch at = logprob_scratch(a.T, p.parts, a.n, a.top);
+  static_assert(sizeof(Part) == 16, "scratch of a part");
+  const Scratch w{reinterpret_cast<Part *>(base), reinterpret_cast<uint64_t *>(base + at.keys), reinterpret_cast<int32_t *>(base + at.ranks)};
 #define PART(NV, WAVES) \
   hipLaunchKernelGGL((logprobs_part<T, NV, WAVES>), dim3((unsigned)rows), dim3(64 * WAVES), 0, stream, a, w, p.parts, p.each)
   if (p.waves == 16) PART(8, 16);
@@ -559,16 +533,6 @@ hipError_t launch(const LogprobArgs &a, void *ws, hipStream_t stream) {
 }
 
 }  // namespace
-
-size_t logprobs_ws(int64_t T, int V, int n, int top) {
-  size_t most = 0;
-  for (int bytes = 2; bytes <= 4; bytes += 2)
-    for (int lead = 0; lead < 16 / bytes; ++lead) {  // a piece more can choose another plan
-      const size_t b = scratch_bytes(T, plan_for(T, V, bytes, lead).parts, n, top);
-      most = b > most ? b : most;
-    }
-  return most;
-}
 
 hipError_t launch_logprobs(const LogprobArgs &a, bool bf16, void *ws, hipStream_t stream) {
   return bf16 ? launch<uint16_t>(a, ws, stream) : launch<float>(a, ws, stream);

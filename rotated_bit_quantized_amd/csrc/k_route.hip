@@ -22,28 +22,18 @@
 // launch) and writes the entries in order; equal ones of a wavefront find their
 // rank by ballots, so no order depends on the time.  Few tokens: one workgroup
 // does both.
-#include "oq_internal.h"
+#include "sparse_plan.h"
 
 namespace oq {
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int WAVES = 16, THREADS = 64 * WAVES;
-// Up to SOLO tokens one workgroup routes and lists; CHUNKS, LISTS: most workgroups
-// of the two launches else.
-constexpr int SOLO = 32, CHUNKS = 512, LISTS = 256;
-
-struct Layout {
-  int lanes;  // of a group
-  int each;   // experts of a group
-  int c;      // experts of a lane
-  int groups;
-};
+constexpr int WAVES = ROUTE_WAVES, THREADS = 64 * WAVES;
 
 struct Work {
   RouteArgs a;
-  Layout l;
+  RouteLayout l;
   int64_t tokens;  // of a chunk
   int32_t *hist;   // [chunks][experts]
   int chunks, solo;
@@ -454,28 +444,6 @@ __global__ void __launch_bounds__(THREADS) route_lists_kernel(const Work g) {
   fill_tail(a, t0 * a.r.k, t1 * a.r.k, all);
 }
 
-// Where logits alone are compared two workgroups fit a CU; with scores and their
-// float64 form one does, and half as many chunks are faster (16384 tokens of 256
-// experts in groups: 43 us, 50 with 512 chunks; logits of 32768 x 128: 32 and 30).
-bool plain(const oq_router &r) { return !r.bias && r.top_groups == r.groups; }
-
-int64_t chunk_tokens(int64_t T, const oq_router &r) {
-  const int64_t most = plain(r) ? CHUNKS : CHUNKS / 2, each = (T + most - 1) / most;
-  return each < WAVES ? WAVES : (each + WAVES - 1) / WAVES * WAVES;
-}
-
-// groups that are all open are none; each group has lanes of its own
-Layout layout_of(const oq_router &r) {
-  Layout l;
-  l.groups = r.top_groups == r.groups ? 1 : r.groups;
-  l.lanes = 64 / l.groups;
-  l.each = r.experts / l.groups;
-  l.c = (l.each + l.lanes - 1) / l.lanes;
-  return l;
-}
-
-bool solo(int64_t T, const Layout &l) { return T <= SOLO && l.c <= 8; }
-
 template <bool PLAIN, class T>
 hipError_t launch(const Work &g, unsigned chunks, hipStream_t stream) {
   const int E = g.a.r.experts;
@@ -492,25 +460,19 @@ hipError_t launch(const Work &g, unsigned chunks, hipStream_t stream) {
 
 }  // namespace
 
-size_t route_ws(int64_t T, const oq_router &r) {
-  if (solo(T, layout_of(r))) return 0;
-  const int64_t tokens = chunk_tokens(T, r);
-  return (size_t)((T + tokens - 1) / tokens) * r.experts * 4;
-}
-
 hipError_t launch_route(const RouteArgs &a, bool bf16, void *ws, hipStream_t stream) {
-  Work g{a, layout_of(a.r), a.T, static_cast<int32_t *>(ws), 0, 0};
-  g.solo = a.offsets && solo(a.T, g.l);
-  if (!g.solo) g.tokens = chunk_tokens(a.T, a.r);
-  g.chunks = g.solo ? 1 : (int)((a.T + g.tokens - 1) / g.tokens);
-  if (g.chunks) {  // none: no token, whose empty lists come from the second launch
-    const hipError_t e = plain(a.r) ? bf16 ? launch<true, uint16_t>(g, g.chunks, stream) : launch<true, float>(g, g.chunks, stream)
-                         : bf16 ? launch<false, uint16_t>(g, g.chunks, stream) : launch<false, float>(g, g.chunks, stream);
+  const RoutePlan p = route_plan(a.T, a.r);
+  const Work g{a, p.l, p.tokens, static_cast<int32_t *>(ws), p.chunks, p.solo && a.offsets};
+  if (a.T > 0 || g.solo) {
+    const hipError_t e = p.plain ? bf16 ? launch<true, uint16_t>(g, p.chunks, stream) : launch<true, float>(g, p.chunks, stream)
+                         : bf16  ? launch<false, uint16_t>(g, p.chunks, stream)
+                                 : launch<false, float>(g, p.chunks, stream);
     if (e != hipSuccess) return e;
   }
   if (!a.offsets || g.solo) return hipSuccess;
   const size_t lds = (size_t)a.r.experts * (8 + 2 * WAVES);
-  hipLaunchKernelGGL(route_lists_kernel, dim3(g.chunks < 1 ? 1 : g.chunks < LISTS ? g.chunks : LISTS), dim3(THREADS), lds, stream, g);
+  const int lists = p.chunks < 1 ? 1 : p.chunks < ROUTE_LISTS ? p.chunks : ROUTE_LISTS;  // without tokens the lists are empty
+  hipLaunchKernelGGL(route_lists_kernel, dim3(lists), dim3(THREADS), lds, stream, g);
   return hipGetLastError();
 }
 

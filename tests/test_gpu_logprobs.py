@@ -212,6 +212,13 @@ def test_tokens_outside_the_vocabulary():
         check(logits_of(T, V, 5), tok, top=2)
 
 
+def test_the_widest_rows():
+    """As many parts as there can be, one list a lane and several."""
+    for T, V in ((1, 1 << 21), (2, 1200003)):
+        check(logits_of(T, V, 1), tokens_of(T, V, 2, 1), top=32)
+        check(logits_of(T, V, 2, BF), tokens_of(T, V, 2, 1), top=32)
+
+
 def test_the_same_token_twice():
     tok = tokens_of(5, 3000, 1, 0).repeat(1, 6).contiguous()
     logprob, rank, *_ = check(logits_of(5, 3000, 0), tok)

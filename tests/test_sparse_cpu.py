@@ -108,7 +108,7 @@ LP = dict(logits=P, dtype=oq.OQ_BF16, ld=1000, T=10, V=1000, scale=f32(1), token
 
 
 @pytest.mark.parametrize("change,code", [
-    (dict(T=-1), INV), (dict(V=0), INV), (dict(V=-5), INV), (dict(n=-1), INV), (dict(top=-1), INV), (dict(V=(1 << 22) + 1, ld=1 << 23), UNS),
+    (dict(T=-1), INV), (dict(V=0), INV), (dict(V=-5), INV), (dict(n=-1), INV), (dict(top=-1), INV), (dict(V=(1 << 21) + 1, ld=1 << 23), UNS),
     (dict(n=65), UNS), (dict(top=33), UNS), (dict(V=4, top=5), INV), (dict(T=(1 << 24) + 1), UNS), (dict(T=(1 << 63) - 1), UNS), (dict(dtype=7), INV),
     (dict(scale=f32(0)), INV), (dict(scale=f32(-1)), INV), (dict(scale=NAN), INV), (dict(scale=INF), INV), (dict(scale=f32(3e38)), INV), (dict(ld=999), INV),
     (dict(ld=(1 << 63) - 1), UNS), (dict(logits=None), INV), (dict(tokens=None), INV), (dict(logprob=None), INV), (dict(rank=None), INV),
