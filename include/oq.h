@@ -761,6 +761,7 @@ typedef struct {
  * A row of y whose weight is 0 is not read (an entry that has no expert, say).
  * y, h bf16; r, r_out of type r_type (OQ_F32 or OQ_BF16).  r_out may be r (same
  * ld); other outputs must not overlap inputs or each other.
+ * Sums are float32, the norms' squares included (elements below 2^63).
  * d a multiple of 8, 8 <= d <= 16384; 1 <= k <= 64; T k < 2^31; every row
  * 16-byte aligned; y_scale, r_scale finite; eps finite, >= 0.
  */
@@ -778,10 +779,11 @@ int oq_residual_norm(const uint16_t *y, int64_t y_ld, int32_t k, const float *we
  *   top_id[t][j], top_logprob[t][j], j < top: the first `top` of the row
  * The order is that of falling logits, equal ones by rising index; NaN comes
  * behind all numbers.  A token outside [0, V) (padding) gives NaN and rank -1.
- * Masked logits (-inf) take no part and no time of their own; a row of nothing
- * else has lse -inf and NaN elsewhere, as has a row with NaN or +inf (whose lse
- * is NaN too); ranks and top_id are in order there as well.
- * Sums are float32; values are off by about 1e-7 of lse - scale x, absolute.
+ * Masked logits (-inf, or the type's lowest value) take no part.  A row of nothing
+ * but -inf has lse -inf and NaN for all other values; a row with NaN or +inf has NaN
+ * for all of them.  Ranks and top_id are in order in such rows as well.
+ * Sums are float32; a log probability is off by some units of 2^-24 of log V and of
+ * its own size.
  * Each output nullable but logprob and rank with n > 0, and the top pair with
  * top > 0.  Rows need the alignment of their element only.
  * 1 <= V <= 2^21, 0 <= n <= 64, 0 <= top <= 32, top <= V, scale > 0 and its

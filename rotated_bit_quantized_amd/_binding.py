@@ -1095,16 +1095,23 @@ def oq_logprobs(logits, tokens=None, top: int = 0, scale: float = 1.0, logprob=N
         n = tokens.shape[1]
     _small(V, n, top)
 
-    def out(t, *shape, dtype=_F):
-        return torch.empty(shape, dtype=dtype, device=logits.device) if t is None else t
+    new, device = torch.empty, logits.device
+
+    def out(t, shape, count, dtype, what):
+        """(tensor, address) of an output, allocated where none is given."""
+        if t is None:
+            t = new(shape, dtype=dtype, device=device)
+            return t, t.data_ptr()
+        return t, _vec(t, count, dtype, what, dev)
 
     top_n = max(top, 0)
-    logprob, rank, entropy, lse = out(logprob, T, n), out(rank, T, n, dtype=_I32), out(entropy, T), out(lse, T)
-    top_id, top_logprob = out(top_id, T, top_n, dtype=_I32), out(top_logprob, T, top_n)
-    ws, ws_at, ws_bytes = _scratch(ws, lambda: oq_logprobs_ws_bytes(T, V, n, top), dev, logits.device)
-    _check(_lib.oq_logprobs(at, dtype, ld, T, V, scale, _opt(tokens, T * n, _I32, "tokens", dev), n, top,
-                            _vec(logprob, T * n, _F, "logprob", dev), _vec(rank, T * n, _I32, "rank", dev),
-                            _vec(entropy, T, _F, "entropy", dev), _vec(lse, T, _F, "lse", dev),
-                            _vec(top_id, T * top_n, _I32, "top_id", dev), _vec(top_logprob, T * top_n, _F, "top_logprob", dev),
-                            ws_at, ws_bytes, stream))
+    logprob, logprob_at = out(logprob, (T, n), T * n, _F, "logprob")
+    rank, rank_at = out(rank, (T, n), T * n, _I32, "rank")
+    entropy, entropy_at = out(entropy, (T,), T, _F, "entropy")
+    lse, lse_at = out(lse, (T,), T, _F, "lse")
+    top_id, id_at = out(top_id, (T, top_n), T * top_n, _I32, "top_id")
+    top_logprob, top_at = out(top_logprob, (T, top_n), T * top_n, _F, "top_logprob")
+    ws, ws_at, ws_bytes = _scratch(ws, lambda: oq_logprobs_ws_bytes(T, V, n, top), dev, device)
+    _check(_lib.oq_logprobs(at, dtype, ld, T, V, scale, _opt(tokens, T * n, _I32, "tokens", dev), n, top, logprob_at, rank_at, entropy_at,
+                            lse_at, id_at, top_at, ws_at, ws_bytes, stream))
     return logprob, rank, entropy, lse, top_id, top_logprob

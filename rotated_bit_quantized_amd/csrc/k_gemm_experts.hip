@@ -4,14 +4,22 @@
 //   v[i][o] = a_scale w_scale[e] acc + mean w1[e] + bias[e],  acc exact in int32
 //   y[i][o] = bf16(v)   or   bf16(silu(v[gate]) v[up])
 //
-// The host does not know how many entries an expert has.  The grid covers the
-// most row tiles that n entries of E experts can make, n / TM + min(E, n); every
-// wavefront finds its tile's expert from the E offsets by a cross-lane sum, and
-// tiles that are not there end at once.  An entry's row is found through the
-// list when it is copied into LDS, and its output goes to the entry's own row,
-// so nothing is gathered or sorted in memory.  With SwiGLU a wavefront's two
-// blocks of weight rows are a gate's and the same outputs' up rows: both sums
-// are in the same lane and registers, and the intermediate never exists.
+// The host does not know how many entries an expert has: a wavefront finds its
+// tile's expert from the E offsets by a sum across its lanes, and tiles that are
+// not there end at once.  An entry's activation row is found through the list when
+// it is copied into LDS, and its output goes to the entry's own row, so nothing is
+// gathered or sorted in memory.  With SwiGLU a wavefront's two blocks of weight rows
+// are a gate's and the same outputs' up rows: both sums are in the same lane and
+// registers, and the projections' 2 f values never exist.
+//
+// What bounds it.  Few entries an expert: the weights, read once, at copy rate
+// (16 x 8 entries of 128 experts, 2048 -> 1536: 41 to 47 us, 260 MB; a copy of as
+// many bytes takes 50).  Many: the matrix unit at the clock that power allows, a stage
+// of 128 k of a 128 x 256 tile a CU in 1.0 us (2.15 POP/s, as the library's int8
+// products), and what is not product: 3 us between two tiles, 1.2 us of epilogue, 2 us
+// of stores, a sixteenth to an eighth of the rows empty in the experts' last tiles.
+// 8192 x 8 entries of 128 experts, 2048 -> 1536: 278 to 302 us of 191 for the products
+// alone; 4096 k, 64 experts: 478 of 382.
 #include "oq_internal.h"
 
 namespace oq {
@@ -604,7 +612,8 @@ hipError_t launch_tile(const ExpertArgs &g, hipStream_t stream) {
   const int64_t nt = ((ACT ? g.N / 2 : g.N) + (ACT ? C::BN / 2 : C::BN) - 1) / (ACT ? C::BN / 2 : C::BN);
   int64_t grid = most_tiles<C::BM>(g, nt);
   if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
-  if (grid > device_cus() / 8 * 8) grid = device_cus() / 8 * 8;
+  const int64_t cus = device_cus() < 8 ? 8 : device_cus() / 8 * 8;
+  if (grid > cus) grid = cus;
   hipLaunchKernelGGL((gemm_experts_tile<C, ACT>), dim3((unsigned)grid), dim3(64 * C::NW), C::LDS, stream, g, (int)nt, div_by((uint32_t)g.per));
   return hipGetLastError();
 }

@@ -7,7 +7,12 @@
 // pieces of 8 elements each (16-byte loads and stores), so that everything
 // between the loads and the stores happens in registers: the sums over the
 // row are cross-lane adds, and meet in LDS where L passes a wavefront.  A layer
-// norm takes its squares about the mean, a second sum over the same registers.
+// norm takes its squares about the mean, a second sum over the same registers.  One
+// piece a thread up to 2048 elements, two above.
+// Measured: 32768 x 4096, norms on both sides, 194 to 204 us, 5.3 to 5.5 TB/s (a large
+// copy: 5.2; four pieces a thread 199, one 203), 8192 x 8192 105 us (four 108, one 130);
+// 4100 x 1920 in float32 with gate and modulation 22 us (two pieces 22, four 26); 64 x 8
+// x 2048 5.0 us, two trips to memory and a launch (two pieces 6.4, four 8.7).
 #include "oq_internal.h"
 
 namespace oq {
