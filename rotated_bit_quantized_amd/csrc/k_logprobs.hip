@@ -29,7 +29,6 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int LIST = 512;
 constexpr float LN2 = 0.693147180559945309417f;
 
 // What is known of a row or a part of it: sums over 2^(z(x)).
@@ -146,12 +145,12 @@ __device__ __forceinline__ float largest(const u32x4 (&raw)[NV]) {
 }
 
 // Pieces part * each .. (part + 1) * each - 1 of a row, NV a thread at most, by WAVES
-// wavefronts.  Of 8 wavefronts three workgroups fit a CU, whose loads run under each
-// other's arithmetic (2048 x 131072: 133 us; four of them, with 64 registers a
-// thread, spill: 163).
+// wavefronts.  24 wavefronts fit a CU, three workgroups of 8 or six of 4, whose loads
+// run under each other's arithmetic (2048 x 131072: 133 us; 32 wavefronts, with 64
+// registers a thread, spill: 163).
 template <class T, int NV, int WAVES>
-__global__ void __launch_bounds__(64 * WAVES, WAVES == 8 ? 6 : 4) logprobs_part(const LogprobArgs a, const Scratch ws, const int parts, const int each) {
-  constexpr int THREADS = 64 * WAVES;
+__global__ void __launch_bounds__(64 * WAVES, WAVES <= 8 ? 6 : 4) logprobs_part(const LogprobArgs a, const Scratch ws, const int parts, const int each) {
+  constexpr int THREADS = 64 * WAVES, LIST = THREADS < 512 ? THREADS : 512;  // a thread for each listed candidate
   constexpr int VE = 16 / sizeof(T);  // elements of a piece
   constexpr int HELD = 64;            // threads whose pieces go to LDS for their candidates
   __shared__ u32x4 s_held[HELD * NV];
@@ -513,7 +512,7 @@ __global__ void __launch_bounds__(64) logprobs_join(const LogprobArgs a, const S
 template <class T>
 hipError_t launch(const LogprobArgs &a, void *ws, hipStream_t stream) {
   const int ve = 16 / sizeof(T), lead = (int)(reinterpret_cast<uintptr_t>(a.logits) & 15) / (int)sizeof(T);
-  const LogprobPlan p = logprob_plan(a.T, a.V, sizeof(T), a.T == 1 || a.ld % ve == 0 ? lead : ve - 1);
+  const LogprobPlan p = logprob_plan(a.T, a.V, sizeof(T), a.T == 1 || a.ld % ve == 0 ? lead : ve - 1, a.top);
   const size_t rows = (size_t)a.T * p.parts;
   if (rows > 0x7fffffff) return hipErrorInvalidConfiguration;
   char *base = static_cast<char *>(ws);
@@ -523,6 +522,7 @@ hipError_t launch(const LogprobArgs &a, void *ws, hipStream_t stream) {
 #define PART(NV, WAVES) \
   hipLaunchKernelGGL((logprobs_part<T, NV, WAVES>), dim3((unsigned)rows), dim3(64 * WAVES), 0, stream, a, w, p.parts, p.each)
   if (p.waves == 16) PART(8, 16);
+  else if (p.waves == 4) PART(8, 4);
   else if (p.nv == 8) PART(8, 8);
   else if (p.nv == 4) PART(4, 8);
   else if (p.nv == 2) PART(2, 8);

@@ -32,8 +32,8 @@ struct LogprobPlan {
   int waves, nv, parts;  // wavefronts of a workgroup, pieces of 16 bytes a thread, parts of a row
   int each;              // pieces of a part
 };
-// lead: elements by which rows begin inside a piece; bytes: of an element.
-LogprobPlan logprob_plan(int64_t T, int V, int bytes, int lead);
+// lead: elements by which rows begin inside a piece; bytes: of an element; top: alternatives.
+LogprobPlan logprob_plan(int64_t T, int V, int bytes, int lead, int top);
 
 // Scratch of rows in several parts, in this order, each 16-byte aligned: statistics, keys, ranks.
 struct LogprobScratch {

@@ -26,15 +26,23 @@ size_t route_ws(int64_t T, const oq_router &r) {
   return p.solo ? 0 : (size_t)p.chunks * r.experts * 4;
 }
 
-LogprobPlan logprob_plan(int64_t T, int V, int bytes, int lead) {
+LogprobPlan logprob_plan(int64_t T, int V, int bytes, int lead, int top) {
   const int ve = 16 / bytes;
   const int pieces = (V + lead + ve - 1) / ve;
   const int64_t cus = device_cus();
-  // Few rows that 16 wavefronts can hold: one launch (1 x 32000 float32 8.0 us; in 16
-  // parts 6.4 and 7.5 for the join).  Else as many pieces a thread as there are, up to
-  // 8, while the parts of all rows still are two workgroups a CU; not more than 256
-  // parts, whose keys the join has in 64 KiB of LDS.
-  if (T <= 2 * cus && pieces <= 1024 * 8 && pieces > 512) return LogprobPlan{16, 8, 1, pieces};
+  // Rows that 16 wavefronts can hold and 8 cannot, up to two a CU: one launch (1 x
+  // 32000 float32 8.3 us, in 16 parts 9.4; 256 rows 12.5 and 16.2; 256 x 50000 bfloat16 14.7
+  // and 18.6, but 32 rows 11.2 and 11.4, 8 11.0 and 10.3, one 10.9 and 9.8).
+  if (pieces > 512 * 8 && pieces <= 1024 * 8 && T <= 2 * cus && (bytes == 4 || T >= 32)) return LogprobPlan{16, 8, 1, pieces};
+  // Many parts of 4 wavefronts, six workgroups a CU, wait less for each other's threshold
+  // than of 8, three a CU (2048 x 131072 bfloat16 127 us and 135, 512 x 16000 10.5 and
+  // 12.1); many alternatives cost each part more (20: 153 and 145).
+  const int quarter = (pieces + 256 * 8 - 1) / (256 * 8);
+  if (top <= 8 && (quarter == 1 ? T >= cus : quarter <= 256 && T * quarter >= 6 * cus))
+    return LogprobPlan{4, 8, quarter, (pieces + quarter - 1) / quarter};
+  // As many pieces a thread as there are, up to 8, while the parts of all rows still
+  // are two workgroups a CU; not more than 256 parts, whose keys the join has in 64 KiB
+  // of LDS.
   LogprobPlan p{8, 8, 1, 0};
   for (;; p.nv /= 2) {
     p.parts = (pieces + 512 * p.nv - 1) / (512 * p.nv);
@@ -59,7 +67,7 @@ size_t logprobs_ws(int64_t T, int V, int n, int top) {
   size_t most = 0;
   for (int bytes = 2; bytes <= 4; bytes += 2)
     for (int lead = 0; lead < 16 / bytes; ++lead) {  // a piece more can choose another plan
-      const size_t b = logprob_scratch(T, logprob_plan(T, V, bytes, lead).parts, n, top).bytes;
+      const size_t b = logprob_scratch(T, logprob_plan(T, V, bytes, lead, top).parts, n, top).bytes;
       most = b > most ? b : most;
     }
   return most;

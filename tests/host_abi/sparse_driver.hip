@@ -168,10 +168,10 @@ void logprob_plans() {
             const size_t ws = oq_logprobs_ws_bytes(T, V, n, top);
             for (int bytes : {2, 4})
               for (int lead = 0; lead < 16 / bytes; ++lead) {
-                const oq::LogprobPlan p = oq::logprob_plan(T, V, bytes, lead);
+                const oq::LogprobPlan p = oq::logprob_plan(T, V, bytes, lead, top);
                 const int ve = 16 / bytes, pieces = (V + lead + ve - 1) / ve;
                 bool ok = p.parts >= 1 && p.each >= 1 && (int64_t)p.parts * p.each >= pieces && (p.parts - 1) * p.each < pieces;
-                ok = ok && p.each <= 64 * p.waves * p.nv && p.nv >= 1 && p.nv <= 8 && (p.waves == 8 || (p.waves == 16 && p.nv == 8));
+                ok = ok && p.each <= 64 * p.waves * p.nv && p.nv >= 1 && p.nv <= 8 && (p.waves == 8 || ((p.waves == 16 || p.waves == 4) && p.nv == 8));
                 ok = ok && (int64_t)p.parts * top * 8 <= 65536;  // the join's keys in LDS
                 const oq::LogprobScratch s = oq::logprob_scratch(T, p.parts, n, top);
                 ok = ok && s.bytes <= ws && s.keys % 16 == 0 && s.ranks % 16 == 0;

@@ -91,7 +91,7 @@ def test_widths(V, T, dtype):
     check(logits_of(T, V, V, dtype), tokens_of(T, V, 2, V), top=min(V, 7), scale=1.25)
 
 
-@pytest.mark.parametrize("T,V", [(600, 5000), (600, 20000), (530, 33000), (260, 70000), (2000, 300), (130, 131072)])
+@pytest.mark.parametrize("T,V", [(600, 5000), (600, 20000), (530, 33000), (260, 70000), (2000, 300), (130, 131072), (1700, 20000), (800, 33001)])
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_many_rows(T, V, dtype):
     """Every number of pieces a thread, one part a row and several."""
@@ -127,6 +127,7 @@ def test_equal_logits(V, T):
     tok[0] = torch.tensor([0, 1, V - 1, V // 2])
     check(x, tok, top=32)
     check(x.bfloat16(), tok, top=20)
+    check(x.bfloat16(), tok, top=8)
 
 
 @pytest.mark.parametrize("V", [300, 9000, 40000])
@@ -142,6 +143,7 @@ def test_masked_vocabulary(V, T, kept):
             x.scatter_(1, keep, logits_of(T, kept, kept, dtype))
             tok = torch.cat((keep[:, :2].int(), torch.zeros(T, 1, dtype=torch.int32, device=DEV), torch.full((T, 1), V - 1, dtype=torch.int32, device=DEV)), 1)
             check(x, tok, top=20)
+            check(x, tok, top=5)
 
 
 @pytest.mark.parametrize("kind", ["rising", "falling", "one lane", "two values", "block"])
@@ -164,6 +166,7 @@ def test_orders_that_fill_the_list(kind, T, V):
             y[:, (i // ve) % 64 == 3] += 40
         y = y.to(dtype)
         check(y, tokens_of(T, V, 2, 3), top=20)
+        check(y, tokens_of(T, V, 2, 3), top=6)  # parts of another size
 
 
 @pytest.mark.parametrize("V", [200, 5000, 40000])
@@ -184,6 +187,7 @@ def test_values_that_are_not_finite(V, T):
     tok[:, 0], tok[:, 1] = V // 3, 3
     tok[7, 2] = 11
     for dtype in (F32, BF):
+        check(x.to(dtype), tok, top=8, plain_rows=plain)
         logprob, rank, entropy, lse, top_id, top_logprob = check(x.to(dtype), tok, top=20, plain_rows=plain)
         assert float(lse[1]) == -INF and torch.isnan(lse[2:7]).all()
         assert torch.isnan(logprob[1:7]).all() and torch.isnan(entropy[1:7]).all() and torch.isnan(top_logprob[1:7]).all()
