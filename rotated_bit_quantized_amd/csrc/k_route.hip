@@ -222,6 +222,36 @@ __device__ __forceinline__ int choose(const float (&x)[NPL], const float (&bias)
   return chosen;
 }
 
+// choose() where 16-bit logits alone are compared: value and index share a word, the
+// index falling, so no two keys are equal and the largest one says everything.
+template <int NPL>
+__device__ __forceinline__ int choose_packed(const float (&x)[NPL], int first, int n, int k, float &logit) {
+  const int lane = threadIdx.x & 63;
+  uint32_t key[NPL];
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) key[i] = i < n ? (key_of(x[i]) & 0xFFFF0000u) | (uint32_t)(0xFFFF - first - i) : 0u;
+#pragma unroll
+  for (int p = 0; p < NPL; ++p) {
+#pragma unroll
+    for (int i = p & 1; i + 1 < NPL; i += 2) {
+      const uint32_t a = key[i], b = key[i + 1];
+      key[i] = a > b ? a : b, key[i + 1] = a > b ? b : a;
+    }
+  }
+  uint32_t mine = 0;
+  for (int j = 0; j < k; ++j) {
+    const uint32_t m = wave_max(key[0]);
+    mine = lane == j ? m : mine;
+    if (key[0] == m) {
+#pragma unroll
+      for (int i = 0; i + 1 < NPL; ++i) key[i] = key[i + 1];
+      key[NPL - 1] = 0;
+    }
+  }
+  logit = __uint_as_float((mine >> 31) ? mine & 0x7FFF0000u : ~mine & 0xFFFF0000u);  // NaN, whose value is 0, is one again
+  return 0xFFFF - (int)(mine & 0xFFFFu);
+}
+
 // The weight of the lane's chosen expert (lanes below k).
 __device__ __forceinline__ float weight(float x, bool mine, float xmax, float total, bool nan, const oq_router &r) {
   float s = 0.f;
@@ -287,8 +317,9 @@ __device__ __forceinline__ void route_tokens(const Work &g, int64_t t0, int64_t 
       }
       bool sure;
       float chosen = 0.f;
-      id = choose<NPL, PLAIN, float>(x, bias, first, n, xmax, g, sure, chosen);
       const bool mine = lane < r.k;
+      if constexpr (PLAIN && sizeof(T) == 2) id = choose_packed<NPL>(x, first, n, r.k, chosen);
+      else id = choose<NPL, PLAIN, float>(x, bias, first, n, xmax, g, sure, chosen);
       if constexpr (!PLAIN) {
         if (!sure) id = choose<NPL, PLAIN, double>(x, bias, first, n, xmax, g, sure, chosen);
         if (mine) {
