@@ -274,7 +274,7 @@ template <int NPL, int W, bool PLAIN, class T>
 __device__ __forceinline__ void route_tokens(const Work &g, int64_t t0, int64_t t1, int *hist) {
   const RouteArgs &a = g.a;
   const oq_router &r = a.r;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // a token's addresses are scalar
   const int group = lane / g.l.lanes, sub = lane - group * g.l.lanes;
   const int first = group * g.l.each + sub * g.l.c;
   int n = g.l.each - sub * g.l.c;
