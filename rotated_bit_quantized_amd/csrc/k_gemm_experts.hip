@@ -18,7 +18,7 @@
 // of 128 k of a 128 x 256 tile a CU in 1.0 us (2.15 POP/s, as the library's int8
 // products), and what is not product: 3 us between two tiles, 1.2 us of epilogue, 2 us
 // of stores, a sixteenth to an eighth of the rows empty in the experts' last tiles.
-// 8192 x 8 entries of 128 experts, 2048 -> 1536: 278 to 302 us of 191 for the products
+// 8192 x 8 entries of 128 experts, 2048 -> 1536: 274 to 302 us of 191 for the products
 // alone; 4096 k, 64 experts: 478 of 382.
 #include "oq_internal.h"
 

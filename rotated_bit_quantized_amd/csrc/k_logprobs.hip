@@ -9,8 +9,8 @@
 // pieces of 16 bytes all in flight at once and held in registers as they came: the
 // maximum is known before the first exponential, so nothing is rescaled, and what comes
 // after it (ranks, best alternatives) reads registers.  Measured: 2048 x 131072
-// bfloat16 115 to 135 us by cards and 7 for the join (4.1 to 4.7 TB/s; with values unpacked once
-// and kept, one workgroup a CU, 550); 77 x 100003 11 and 5; 1 x 32000 float32 8, a launch.
+// bfloat16 114 to 127 us by cards, 7 of them the join (4.2 to 4.7 TB/s; with values unpacked
+// once and kept, one workgroup a CU, 550); 77 x 100003 11 and 5; 1 x 32000 float32 8, a launch.
 //
 // Alternatives: the `top`-th largest of 64 maxima (over the threads of one lane
 // number) is a threshold that at least `top` elements reach and hardly more do.  The

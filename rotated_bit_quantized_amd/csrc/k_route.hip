@@ -15,10 +15,10 @@
 // twice that, the token is done again in float64 (one token in some hundreds; a
 // choice by the logits themselves compares exactly and never does).
 //
-// Bound: instructions, some 350 issue slots a token of 128 experts and 8 choices, of
-// which the cross-lane maxima are half: 32768 tokens in 20 us (their bytes take 2);
-// for few tokens launches and the length of one token's chain (1 token 5.4 us, 333 in
-// groups, one a wavefront, 11).
+// Bound: instructions, some 230 vector and 80 scalar ones a token of 128 experts and 8
+// choices, of which the cross-lane maxima are a third: 32768 bfloat16 tokens in 17 us
+// (their bytes take 2); for few tokens launches and the length of one token's chain (1
+// token 5.4 us, 333 in groups, one a wavefront, 11).
 // Lists: a counting sort over at most 512 chunks of tokens.  The routing launch leaves
 // each chunk's count of every expert, the second one adds them up (every workgroup
 // for itself, four counts a load: that costs less than a third launch; 32768 tokens
