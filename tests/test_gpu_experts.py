@@ -3,9 +3,11 @@
 Bound on an output before SwiGLU, as for the plain product: 2^-8 |exact| (the
 bfloat16 rounding) + 2^-21 (|a s acc| + |mean w1| + |bias|) = 2^-8 |v| + e(v).
 SwiGLU: y = silu(g) u with |silu'| <= 1.1, so float32 values off by e(g), e(u)
-move y by at most 1.1 e(g) |u| + |silu(g)| e(u) + e(g) e(u); the exponential,
-sum, quotient and product add less than 8 units of 2^-24 of |y|, the result's
-rounding 2^-8 |y|.  The bound takes 2 e(g) |u| and 2^-7.9 |y|."""
+move y by at most 1.1 e(g) |u| + |silu(g)| e(u) + e(g) e(u).  The exponential's
+argument g log2(e) is off by 1.5 |g log2(e)| units of 2^-24, which moves y by 1.5
+|g| units at most; the exponential, sum, reciprocal and products add 8; the result's
+rounding 2^-8 |y|.  The bound takes 2 e(g) |u| and 2^-7.9 |y|, which leaves 4700
+units for |g| (below 10 here, unless a test says otherwise)."""
 import pytest
 import torch
 
