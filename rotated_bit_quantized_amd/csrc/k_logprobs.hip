@@ -90,7 +90,8 @@ __device__ __forceinline__ float logit(const T *row, int i) {
 // What a row's statistics say of a logit and of the row.
 __device__ __forceinline__ float log_prob(float x, float scale, const Part &r) {
   const float z = z_of(x, scale * ATTN_LOG2E, r), log_s = log2f(r.s);
-  if (z == -INFINITY && x > -INFINITY && r.top < INFINITY) return (x - r.top) * scale;  // in units of log 2 it passes float32
+  // in units of log 2 it passes float32; of a row with NaN (s is NaN) nothing is known
+  if (z == -INFINITY && x > -INFINITY && r.top < INFINITY && r.s == r.s) return (x - r.top) * scale;
   return (z - log_s) * LN2;
 }
 __device__ __forceinline__ void row_outputs(const LogprobArgs &a, int64_t t, const Part &r) {
