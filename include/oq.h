@@ -782,8 +782,10 @@ int oq_residual_norm(const uint16_t *y, int64_t y_ld, int32_t k, const float *we
  * Masked logits (-inf, or the type's lowest value) take no part.  A row of nothing
  * but -inf has lse -inf and NaN for all other values; a row with NaN or +inf has NaN
  * for all of them.  Ranks and top_id are in order in such rows as well.
- * Sums are float32; a log probability is off by some units of 2^-24 of log V and of
- * its own size.
+ * Sums are float32, of the others beside the largest logit alone: a log probability is off
+ * by at most some 100 units of 2^-24 (3 more for each unit of scale x that the others lie
+ * below the largest logit on average) of itself, however near 0 it is, and never above 0;
+ * an entropy likewise, and never below 0.  (Terms below 2^-126 of the largest may count as 0.)
  * Each output nullable but logprob and rank with n > 0, and the top pair with
  * top > 0.  Rows need the alignment of their element only.
  * 1 <= V <= 2^21, 0 <= n <= 64, 0 <= top <= 32, top <= V, scale > 0 and its

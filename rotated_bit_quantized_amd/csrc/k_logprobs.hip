@@ -1,8 +1,12 @@
 // Log probabilities, ranks, entropy and best alternatives of rows of logits
 // (oq_logprobs).
 //
-//   z = scale log2(e) x - M,  s = sum 2^z,  t = sum 2^z z     (M: the largest)
-//   lse = ln2 (M + log2 s),  log p = ln2 (z - log2 s),  entropy = ln2 (log2 s - t / s)
+//   z = scale log2(e) (x - M),  r = sum 2^z - 1,  t = sum 2^z z     (M: the largest)
+//   lse = scale M + log1p(r),  log p = scale (x - M) - log1p(r),  entropy = log1p(r) - ln2 t / (1 + r)
+//
+// The 1 of r is the largest logit's own term, which is left out of the sum: of a
+// nearly certain token all digits of log p are those of r.  Both parts of log p are
+// <= 0 and both of the entropy >= 0, so nothing cancels and no sign is ever wrong.
 //
 // Bound: HBM, one pass over the logits; some 11 vector instructions an element
 // (the exponential counts four) are near that.  A workgroup takes a part of a row, its
@@ -31,22 +35,16 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float LN2 = 0.693147180559945309417f;
 
-// What is known of a row or a part of it: sums over 2^(z(x)).
+// What is known of a row or a part of it.
 struct Part {
-  float top, m, s, t;  // the largest logit, m = RN(top scale log2(e))
+  float top;      // the largest logit; 0 where there is nothing but -inf
+  float rest, t;  // r and t of above; r is -1 where there is nothing but -inf
+  float unused;
 };
+constexpr float NOTHING = -1.f;  // as rest
 
-// z of a logit.  Where m passes float32 (logits next to the type's ends: a mask of
-// the lowest value) the difference is formed first; else in one step, whose only
-// rounding is that of z.
-__device__ __forceinline__ float z_of(float x, float c, const Part &r) {
-  return fabsf(r.m) < INFINITY ? __builtin_fmaf(x, c, -r.m) : (x - r.top) * c;
-}
 // The reference of logits of which `top` is the largest; of nothing but -inf any does.
-__device__ __forceinline__ Part about(float top, float c) {
-  const float ref = top == -INFINITY ? 0.f : top;
-  return Part{ref, ref * c, 0.f, 0.f};
-}
+__device__ __forceinline__ float about(float top) { return top == -INFINITY ? 0.f : top; }
 
 struct Scratch {
   Part *part;      // [T][parts]
@@ -87,23 +85,31 @@ __device__ __forceinline__ float logit(const T *row, int i) {
   else return row[i];
 }
 
-// What a row's statistics say of a logit and of the row.
-__device__ __forceinline__ float log_prob(float x, float scale, const Part &r) {
-  const float z = z_of(x, scale * ATTN_LOG2E, r), log_s = log2f(r.s);
-  // in units of log 2 it passes float32; of a row with NaN (s is NaN) nothing is known
-  if (z == -INFINITY && x > -INFINITY && r.top < INFINITY && r.s == r.s) return (x - r.top) * scale;
-  return (z - log_s) * LN2;
+// log(1 + r) for r >= 0 within 2.7 units of 2^-24 of itself, and -inf of NOTHING: the
+// logarithm of the rounded sum and what the rounding left out of it, or three terms of
+// the series (log1pf takes 2048 x 131072 another 9 us).
+__device__ __forceinline__ float log_sum(float r) {
+  const float u = 1.f + r;
+  const float far = __builtin_fmaf(__builtin_amdgcn_logf(u), LN2, (r - (u - 1.f)) * __builtin_amdgcn_rcpf(u));
+  const float near = r * __builtin_fmaf(r, __builtin_fmaf(r, 1.f / 3.f, -0.5f), 1.f);
+  return r == NOTHING ? -INFINITY : r < 0x1p-8f ? near : far;
 }
-__device__ __forceinline__ void row_outputs(const LogprobArgs &a, int64_t t, const Part &r) {
-  const float log_s = log2f(r.s);
-  if (a.lse) a.lse[t] = fabsf(r.m) < INFINITY ? (r.m + log_s) * LN2 : __builtin_fmaf(r.top, a.scale, log_s * LN2);
-  if (a.entropy) a.entropy[t] = (log_s - r.t / r.s) * LN2;
+// What a row's statistics, log_s = log_sum(rest) among them, say of a logit and of the row.
+__device__ __forceinline__ float log_prob(float x, float scale, const Part &r, float log_s) {
+  const float d = x - r.top;
+  // a distance past float32 may have a product that is not (if scale < 1; else both are -inf)
+  const float z = fabsf(d) < INFINITY || !(fabsf(x) < INFINITY) ? d * scale : __builtin_fmaf(x, scale, -(r.top * scale));
+  return z - log_s;
+}
+__device__ __forceinline__ void row_outputs(const LogprobArgs &a, int64_t t, const Part &r, float log_s) {
+  if (a.lse) a.lse[t] = __builtin_fmaf(r.top, a.scale, log_s);
+  if (a.entropy) a.entropy[t] = log_s - r.t / (1.f + r.rest) * LN2;
 }
 template <class T>
-__device__ __forceinline__ void token_outputs(const LogprobArgs &a, const T *row, int64_t t, int i, const Part &r, int rank) {
+__device__ __forceinline__ void token_outputs(const LogprobArgs &a, const T *row, int64_t t, int i, const Part &r, float log_s, int rank) {
   const int tok = a.tokens[t * a.n + i];
   const bool in = tok >= 0 && tok < a.V;
-  a.logprob[t * a.n + i] = in ? log_prob(logit(row, tok), a.scale, r) : NAN;
+  a.logprob[t * a.n + i] = in ? log_prob(logit(row, tok), a.scale, r, log_s) : NAN;
   a.rank[t * a.n + i] = in ? rank : -1;
 }
 
@@ -157,7 +163,7 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES <= 8 ? 6 : 4) logprobs_part(
   __shared__ u32x4 s_held[HELD * NV];
   __shared__ int s_first[HELD];
   __shared__ uint32_t s_max[WAVES * 64];
-  __shared__ float s_sum[2 * WAVES];
+  __shared__ float s_sum[3 * WAVES];
   __shared__ uint64_t s_list[LIST];
   __shared__ int s_rank[64];
   __shared__ int s_count[3];  // listed candidates, a count, threads held
@@ -221,8 +227,7 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES <= 8 ? 6 : 4) logprobs_part(
     const uint32_t o = s_max[64 * w + lane];
     group = o > group ? o : group;
   }
-  const float top = value_of(wave_max(group)), c = a.scale * ATTN_LOG2E;
-  Part stat = about(top, c);
+  const float top = value_of(wave_max(group)), ref = about(top), c = a.scale * ATTN_LOG2E;
 
   // the threshold: the top-th largest of the 64 group maxima
   if (a.top > 0 && wave == 0) {
@@ -235,24 +240,59 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES <= 8 ? 6 : 4) logprobs_part(
     if (lane == 0) s_limit = limit;
   }
 
+  // s and t over all but the largest ones, which are counted.  z is taken about m =
+  // RN(ref c) in one step, whose only rounding is z's, and m's error off the sums
+  // afterwards: up to |m| = 2^20, where it is below 2^-4.  The elements of a thread that
+  // holds a largest one are then summed again, a lane each; of many such threads, and
+  // beyond 2^20, every element is looked at (2048 x 131072: 130 us; 140 where every
+  // wavefront with a largest one looks at all of its elements).
   float s = 0.f, sum_t = 0.f;
-  auto sums = [&](auto z_at) {
+  int largest_ones = 0;
+  auto sums = [&](auto add) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       forget(v);
 #pragma unroll
-      for (int j = 0; j < VE; ++j) {
-        const float z = z_at(at(v, j)), e = __builtin_amdgcn_exp2f(z);
-        s += e;
-        sum_t = __builtin_fmaf(e, fmaxf(z, -1024.f), sum_t);  // 2^-inf takes no part
-      }
+      for (int j = 0; j < VE; ++j) add(at(v, j));
     }
   };
-  if (fabsf(stat.m) < INFINITY) sums([&](float x) { return __builtin_fmaf(x, c, -stat.m); });
-  else sums([&](float x) { return (x - stat.top) * c; });
+  auto add = [&](float z) {
+    const float e = __builtin_amdgcn_exp2f(z);
+    s += e;
+    sum_t = __builtin_fmaf(e, fmaxf(z, -1024.f), sum_t);  // 2^-inf takes no part
+  };
+  const float m = ref * c;
+  uint64_t owners = __ballot(mine == ref);
+  if (fabsf(m) < 0x1p20f && __popcll(owners) <= 8) {
+    sums([&](float x) { add(__builtin_fmaf(x, c, -m)); });
+    if (mine == ref) s = sum_t = 0.f;
+    u32x4 *own = s_held + wave * NV;  // nobody else's until the next barrier
+    for (; owners; owners &= owners - 1) {
+      if (lane == __ffsll((long long)owners) - 1) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) own[v] = raw[v];
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      const bool in = lane < NV * VE;
+      const float x = in ? logit(reinterpret_cast<const T *>(own), lane) : -INFINITY;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      add(x == ref ? -INFINITY : __builtin_fmaf(x, c, -m));
+      largest_ones += __popcll(__ballot(x == ref));
+    }
+    const float off = __builtin_fmaf(ref, c, -m), back = __builtin_amdgcn_exp2f(-off);
+    sum_t = back * __builtin_fmaf(-off, s, sum_t);
+    s *= back;
+  } else {
+    sums([&](float x) {
+      add(x == ref ? -INFINITY : (x - ref) * c);
+      largest_ones += __popcll(__ballot(x == ref));
+    });
+  }
   s = wave_sum(s);
   sum_t = wave_sum(sum_t);
-  if (lane == 0) s_sum[wave] = s, s_sum[WAVES + wave] = sum_t;
+  if (lane == 0) s_sum[wave] = s, s_sum[WAVES + wave] = sum_t, s_sum[2 * WAVES + wave] = (float)largest_ones;
 
   // ranks: elements above the token's, and equal ones before it.  A piece before
   // the token's counts from its value on, that one and those behind it from the
@@ -290,8 +330,12 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES <= 8 ? 6 : 4) logprobs_part(
     if (lane == 0 && count) atomicAdd(s_rank + i, count);
   }
   __syncthreads();
+  Part stat{ref, 0.f, 0.f, 0.f};
+  float ones = 0.f;
 #pragma unroll
-  for (int w = 0; w < WAVES; ++w) stat.s += s_sum[w], stat.t += s_sum[WAVES + w];
+  for (int w = 0; w < WAVES; ++w) stat.rest += s_sum[w], stat.t += s_sum[WAVES + w], ones += s_sum[2 * WAVES + w];
+  stat.rest = top == INFINITY ? NAN : stat.rest + (ones - 1.f);
+  const float log_s = log_sum(stat.rest);
 
   if (a.top > 0) {
     const uint32_t lowest = order_of(-INFINITY);
@@ -393,7 +437,7 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES <= 8 ? 6 : 4) logprobs_part(
     if (parts == 1) {
       if ((int)threadIdx.x < n && rank < a.top) {
         a.top_id[t * a.top + rank] = (int32_t)~(uint32_t)key;
-        a.top_logprob[t * a.top + rank] = log_prob(value_of((uint32_t)(key >> 32)), a.scale, stat);
+        a.top_logprob[t * a.top + rank] = log_prob(value_of((uint32_t)(key >> 32)), a.scale, stat, log_s);
       }
     } else {
       uint64_t *keys = ws.keys + ((int64_t)t * parts + part) * a.top;
@@ -402,8 +446,8 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES <= 8 ? 6 : 4) logprobs_part(
     }
   }
   if (parts == 1) {
-    if (threadIdx.x == 0) row_outputs(a, t, stat);
-    if ((int)threadIdx.x < a.n) token_outputs(a, row, t, threadIdx.x, stat, s_rank[threadIdx.x]);
+    if (threadIdx.x == 0) row_outputs(a, t, stat, log_s);
+    if ((int)threadIdx.x < a.n) token_outputs(a, row, t, threadIdx.x, stat, log_s, s_rank[threadIdx.x]);
   } else {
     if (threadIdx.x == 0) ws.part[t * parts + part] = stat;
     if ((int)threadIdx.x < a.n) ws.ranks[(t * parts + part) * a.n + threadIdx.x] = s_rank[threadIdx.x];
@@ -429,30 +473,36 @@ __global__ void __launch_bounds__(64) logprobs_join(const LogprobArgs a, const S
   }
 #pragma unroll 4
   for (int i = lane; i < total; i += 64) s_keys[i] = ws.keys[t * total + i];
-  // parts of nothing but -inf (s = 0) have no maximum
-  Part mine = lane < parts ? ws.part[t * parts + lane] : Part{0.f, 0.f, 0.f, 0.f};
-  float top = mine.s != 0.f ? mine.top : -INFINITY;
+  Part mine = lane < parts ? ws.part[t * parts + lane] : Part{0.f, NOTHING, 0.f, 0.f};
+  float top = mine.rest != NOTHING ? mine.top : -INFINITY;
   for (int p = lane + 64; p < parts; p += 64) {
     const Part q = ws.part[t * parts + p];
-    if (q.s != 0.f) top = fmaxf(top, q.top);
+    if (q.rest != NOTHING) top = fmaxf(top, q.top);
   }
 #pragma unroll
   for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
   const float c = a.scale * ATTN_LOG2E;
-  Part stat = about(top, c);
+  Part stat{about(top), 0.f, 0.f, 0.f};
+  float largest_ones = 0.f;  // parts whose own 1 is one of the row's largest
   for (int p = lane; p < parts; p += 64) {
     const Part q = p == lane ? mine : ws.part[t * parts + p];
-    if (q.s == 0.f) continue;
-    const bool far = !(fabsf(q.m) < INFINITY && fabsf(stat.m) < INFINITY);
-    const float down = fmaxf(far ? (q.top - stat.top) * c : q.m - stat.m, -1024.f), f = __builtin_amdgcn_exp2f(down);
-    stat.s = __builtin_fmaf(f, q.s, stat.s);
-    stat.t = __builtin_fmaf(f, __builtin_fmaf(q.s, down, q.t), stat.t);
+    if (q.rest == NOTHING) continue;
+    if (q.top == stat.top) {
+      stat.rest += q.rest;
+      stat.t += q.t;
+      largest_ones += 1.f;
+    } else {
+      const float down = fmaxf((q.top - stat.top) * c, -1024.f), f = __builtin_amdgcn_exp2f(down);
+      stat.rest += __builtin_fmaf(f, q.rest, f);
+      stat.t = __builtin_fmaf(f, __builtin_fmaf(1.f + q.rest, down, q.t), stat.t);
+    }
   }
-  stat.s = wave_sum(stat.s);
+  stat.rest = wave_sum(stat.rest) + (wave_sum(largest_ones) - 1.f);
   stat.t = wave_sum(stat.t);
-  if (lane == 0) row_outputs(a, t, stat);
+  const float log_s = log_sum(stat.rest);
+  if (lane == 0) row_outputs(a, t, stat, log_s);
   if (lane < a.n) {
-    a.logprob[t * a.n + lane] = in ? log_prob(xt, a.scale, stat) : NAN;
+    a.logprob[t * a.n + lane] = in ? log_prob(xt, a.scale, stat, log_s) : NAN;
     a.rank[t * a.n + lane] = in ? rank : -1;
   }
   if (a.top == 0) return;
@@ -506,7 +556,7 @@ __global__ void __launch_bounds__(64) logprobs_join(const LogprobArgs a, const S
   }
   if (lane < a.top && best_key) {
     a.top_id[t * a.top + lane] = (int32_t)~(uint32_t)best_key;
-    a.top_logprob[t * a.top + lane] = log_prob(value_of((uint32_t)(best_key >> 32)), a.scale, stat);
+    a.top_logprob[t * a.top + lane] = log_prob(value_of((uint32_t)(best_key >> 32)), a.scale, stat, log_s);
   }
 }
 
