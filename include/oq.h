@@ -659,7 +659,8 @@ enum { OQ_SCORE_SOFTMAX = 1, OQ_SCORE_SIGMOID = 2 };
  * Equal ones go to the lowest index, runs and experts alike.  Choices are those
  * of the exact values: where float32 cannot tell neighbours apart, float64
  * decides.  A NaN ranks below all numbers (in a run's score it counts as -inf);
- * ids are valid whatever the logits hold, weights follow the formula.
+ * ids are valid whatever the logits hold, weights follow the formula (a softmax over
+ * NaN or +inf is NaN throughout, whoever is chosen).
  * 1 <= experts <= 1024 (512 with groups); groups <= 64 divides experts; group_best <= experts /
  * groups; 1 <= k <= 32, k <= top_groups experts / groups; factor finite.
  */

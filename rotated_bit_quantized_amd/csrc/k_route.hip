@@ -306,7 +306,10 @@ __device__ __forceinline__ void route_tokens(const Work &g, int64_t t0, int64_t 
       bool nan = false;
       if (softmax) {
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) xmax = fmaxf(xmax, x[i]), nan = nan || x[i] != x[i];
+        for (int i = 0; i < NPL; ++i) {
+          xmax = fmaxf(xmax, x[i]);
+          nan = nan || (PLAIN ? x[i] != x[i] : !(x[i] < INFINITY));  // a plain choice takes an infinity itself
+        }
         nan = __any(nan);
         if (scores || !r.renorm) xmax = wave_fmax(xmax);
         if (!r.renorm) {
