@@ -703,7 +703,8 @@ enum { OQ_ACT_NONE = 0, OQ_ACT_SWIGLU = 1 };
  *   v[o] = a_scale[row] * w_scale[e][o] * acc + mean[row] * w1[e][o] + bias[e][o]
  *   y[i][o] = bf16_RNE(v[o])                                  OQ_ACT_NONE, N outputs
  *   y[i][o] = bf16_RNE(v[o] / (1 + exp(-v[o])) * v[N/2 + o])  OQ_ACT_SWIGLU, N/2 outputs
- * (N even; the first half of the weight rows is the gate).
+ * (N even; the first half of the weight rows is the gate; below a gate of -174 the product
+ * may be 0, and NaN with an infinite v[N/2 + o]).
  * per = k: entries of a token share its activation row (up projections); per =
  * 1: every entry has a row of its own (down projections).
  * qa int8 [rows][lda], a_scale and mean float32 [rows]; w int8 [E][N][ldw], an
