@@ -151,12 +151,12 @@ __device__ __forceinline__ float largest(const u32x4 (&raw)[NV]) {
   return m;
 }
 
-// Pieces part * each .. (part + 1) * each - 1 of a row, NV a thread at most, by WAVES
-// wavefronts.  24 wavefronts fit a CU, three workgroups of 8 or six of 4, whose loads
+// Pieces part * each .. (part + 1) * each - 1 of a row (from row t0 on), NV a thread at most, by
+// WAVES wavefronts.  24 wavefronts fit a CU, three workgroups of 8 or six of 4, whose loads
 // run under each other's arithmetic (2048 x 131072: 133 us; 32 wavefronts, with 64
 // registers a thread, spill: 163).
 template <class T, int NV, int WAVES>
-__global__ void __launch_bounds__(64 * WAVES, WAVES <= 8 ? 6 : 4) logprobs_part(const LogprobArgs a, const Scratch ws, const int parts, const int each) {
+__global__ void __launch_bounds__(64 * WAVES, WAVES <= 8 ? 6 : 4) logprobs_part(const LogprobArgs a, const Scratch ws, const int64_t t0, const int parts, const int each) {
   constexpr int THREADS = 64 * WAVES, LIST = THREADS < 512 ? THREADS : 512;  // a thread for each listed candidate
   constexpr int VE = 16 / sizeof(T);  // elements of a piece
   constexpr int HELD = 64;            // threads whose pieces go to LDS for their candidates
@@ -169,8 +169,9 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES <= 8 ? 6 : 4) logprobs_part(
   __shared__ int s_count[3];  // listed candidates, a count, threads held
   __shared__ uint32_t s_limit;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = blockIdx.x / parts;
-  const int part = blockIdx.x - (int)(t * parts);
+  const uint32_t in_launch = blockIdx.x / parts;
+  const int64_t t = t0 + in_launch;
+  const int part = blockIdx.x - in_launch * parts;
   const T *row = static_cast<const T *>(a.logits) + t * a.ld;
   // pieces lie on 16-byte boundaries: the first one may begin before the row
   const int lead = (int)(reinterpret_cast<uintptr_t>(row) & 15) / (int)sizeof(T);
@@ -564,23 +565,25 @@ template <class T>
 hipError_t launch(const LogprobArgs &a, void *ws, hipStream_t stream) {
   const int ve = 16 / sizeof(T), lead = (int)(reinterpret_cast<uintptr_t>(a.logits) & 15) / (int)sizeof(T);
   const LogprobPlan p = logprob_plan(a.T, a.V, sizeof(T), a.T == 1 || a.ld % ve == 0 ? lead : ve - 1, a.top);
-  const size_t rows = (size_t)a.T * p.parts;
-  if (rows > 0x7fffffff) return hipErrorInvalidConfiguration;
   char *base = static_cast<char *>(ws);
   const LogprobScratch at = logprob_scratch(a.T, p.parts, a.n, a.top);
   static_assert(sizeof(Part) == 16, "scratch of a part");
   const Scratch w{reinterpret_cast<Part *>(base), reinterpret_cast<uint64_t *>(base + at.keys), reinterpret_cast<int32_t *>(base + at.ranks)};
-#define PART(NV, WAVES) \
-  hipLaunchKernelGGL((logprobs_part<T, NV, WAVES>), dim3((unsigned)rows), dim3(64 * WAVES), 0, stream, a, w, p.parts, p.each)
-  if (p.waves == 16) PART(8, 16);
-  else if (p.waves == 4) PART(8, 4);
-  else if (p.nv == 8) PART(8, 8);
-  else if (p.nv == 4) PART(4, 8);
-  else if (p.nv == 2) PART(2, 8);
-  else PART(1, 8);
+  const int64_t most = launch_rows(64 * p.waves * p.parts);
+  for (int64_t t0 = 0; t0 < a.T; t0 += most) {
+    const unsigned groups = (unsigned)((a.T - t0 < most ? a.T - t0 : most) * p.parts);
+#define PART(NV, WAVES) hipLaunchKernelGGL((logprobs_part<T, NV, WAVES>), dim3(groups), dim3(64 * WAVES), 0, stream, a, w, t0, p.parts, p.each)
+    if (p.waves == 16) PART(8, 16);
+    else if (p.waves == 4) PART(8, 4);
+    else if (p.nv == 8) PART(8, 8);
+    else if (p.nv == 4) PART(4, 8);
+    else if (p.nv == 2) PART(2, 8);
+    else PART(1, 8);
 #undef PART
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.parts == 1) return e;
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (p.parts == 1) return hipSuccess;
   hipLaunchKernelGGL(logprobs_join<T>, dim3((unsigned)a.T), dim3(64), (size_t)p.parts * a.top * 8, stream, a, w, p.parts);
   return hipGetLastError();
 }
