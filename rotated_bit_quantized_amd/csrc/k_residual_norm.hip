@@ -13,7 +13,7 @@
 // copy: 5.2; four pieces a thread 199, one 203), 8192 x 8192 105 us (four 108, one 130);
 // 4100 x 1920 in float32 with gate and modulation 22 us (two pieces 22, four 26); 64 x 8
 // x 2048 5.0 us, two trips to memory and a launch (two pieces 6.4, four 8.7).
-#include "oq_internal.h"
+#include "sparse_plan.h"
 
 namespace oq {
 namespace {
@@ -102,11 +102,11 @@ __device__ __forceinline__ void norm(float (&x)[NV][8], const oq_norm &n, const 
 }
 
 template <int L, int NV, bool RBF>
-__global__ void __launch_bounds__(L > 256 ? L : 256) residual_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(L > 256 ? L : 256) residual_norm_kernel(const NormArgs a, const int64_t t0) {
   constexpr int ROWS = L > 256 ? 1 : 256 / L;
   __shared__ float slots[L > 64 ? 4 * 16 : 1];
   const int gl = threadIdx.x % L;
-  const int64_t t = (int64_t)blockIdx.x * ROWS + threadIdx.x / L;
+  const int64_t t = t0 + (int64_t)blockIdx.x * ROWS + threadIdx.x / L;
   if (L <= 64 && t >= a.T) return;
   const bool row_live = t < a.T;
   const int d = a.d;
@@ -228,10 +228,15 @@ __global__ void __launch_bounds__(L > 256 ? L : 256) residual_norm_kernel(const 
 template <int L, int NV>
 hipError_t launch(const NormArgs &a, bool r_bf16, hipStream_t stream) {
   constexpr int THREADS = L > 256 ? L : 256, ROWS = THREADS / L;
-  const dim3 grid((unsigned)((a.T + ROWS - 1) / ROWS)), block(THREADS);
-  if (r_bf16) hipLaunchKernelGGL((residual_norm_kernel<L, NV, true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((residual_norm_kernel<L, NV, false>), grid, block, 0, stream, a);
-  return hipGetLastError();
+  constexpr int64_t MOST = launch_rows(THREADS) * ROWS;
+  for (int64_t t0 = 0; t0 < a.T; t0 += MOST) {
+    const dim3 grid((unsigned)(((a.T - t0 < MOST ? a.T - t0 : MOST) + ROWS - 1) / ROWS)), block(THREADS);
+    if (r_bf16) hipLaunchKernelGGL((residual_norm_kernel<L, NV, true>), grid, block, 0, stream, a, t0);
+    else hipLaunchKernelGGL((residual_norm_kernel<L, NV, false>), grid, block, 0, stream, a, t0);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
