@@ -20,7 +20,7 @@
 // of stores, a sixteenth to an eighth of the rows empty in the experts' last tiles.
 // 8192 x 8 entries of 128 experts, 2048 -> 1536: 274 to 302 us of 191 for the products
 // alone; 4096 k, 64 experts: 478 of 382.
-#include "oq_internal.h"
+#include "sparse_plan.h"
 
 namespace oq {
 namespace {
@@ -83,12 +83,12 @@ __device__ __forceinline__ int run_of(int rows, int nt) {
   return run < 1 << 28 ? (int)run : 1 << 28;
 }
 
-// Tile of this workgroup, TM entries a row tile, nt column tiles.  Workgroups go to
-// the 8 XCDs in turn; each XCD takes a run of tiles, the columns of a row tile one
+// Tile of this workgroup, `block` of all launches, TM entries a row tile, nt column tiles.
+// Workgroups go to the 8 XCDs in turn; each XCD takes a run of tiles, the columns of a row tile one
 // after the other, so that what it has in flight are the tiles of one expert or two,
 // whose rows and weights its L2 holds.  The same in every lane.
 template <int TM>
-__device__ __forceinline__ Place find_tile(const ExpertArgs &g, int nt) {
+__device__ __forceinline__ Place find_tile(const ExpertArgs &g, int nt, uint32_t block) {
   const int lane = threadIdx.x & 63, n = (int)g.n, each = (g.E + 63) / 64;
   auto cut = [&](int v) { return v < 0 ? 0 : v < n ? v : n; };
   const int e0 = lane * each, e1 = e0 + each < g.E ? e0 + each : g.E;
@@ -104,7 +104,7 @@ __device__ __forceinline__ Place find_tile(const ExpertArgs &g, int nt) {
   const int sum = tiles_below<TM>(g, tiles);  // up to and with this lane
   Place r{0, 0, 0, 0};
   const int rows = __builtin_amdgcn_readlane(sum, 63), run = run_of(rows, nt);
-  const int in_run = blockIdx.x >> 3, id = (blockIdx.x & 7) * run + in_run;
+  const int in_run = block >> 3, id = (block & 7) * run + in_run;
   const int tile = __builtin_amdgcn_readfirstlane((int)((uint32_t)id / (uint32_t)nt));
   if (in_run >= run || tile >= rows) return r;
   r.tn = id - tile * nt;
@@ -160,11 +160,11 @@ __device__ __forceinline__ void silu_mul(float (&v)[N], const float (&up)[N]) {
 // of CH bytes, each row's 16-byte pieces permuted by the row against bank
 // conflicts.
 template <int MT, int KS, bool ACT>
-__global__ void __launch_bounds__(512) gemm_experts_rows(const ExpertArgs g, const int CH, const int nt, const Div per) {
+__global__ void __launch_bounds__(512) gemm_experts_rows(const ExpertArgs g, const uint32_t first, const int CH, const int nt, const Div per) {
   constexpr int NW = 8, TM = 16 * MT, GROUPS = NW / KS, DEPTH = 2;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Place rt = find_tile<TM>(g, nt);
+  const Place rt = find_tile<TM>(g, nt, first + blockIdx.x);
   if (rt.rows == 0) return;
   const uint32_t lds0 = lds_addr_of(smem);
   const int r16 = lane & 15, kq = lane >> 4, ks = wave % KS;
@@ -645,9 +645,14 @@ hipError_t launch_rows(const ExpertArgs &g, hipStream_t stream) {
   int ch = 65536 / TM / 1024 * 1024;
   if (ch > (g.K + 1023) / 1024 * 1024) ch = (g.K + 1023) / 1024 * 1024;
   const size_t lds = (size_t)TM * ch > PART || KS == 1 ? (size_t)TM * ch : PART;
-  hipLaunchKernelGGL((gemm_experts_rows<MT, KS, ACT>), dim3((unsigned)grid), dim3(512), lds, stream, g, ch, (int)nt,
-                     div_by((uint32_t)g.per));
-  return hipGetLastError();
+  constexpr int64_t MOST = rows_of_launch(512) / 8 * 8;  // workgroups, whole turns of the XCDs
+  for (int64_t first = 0; first < grid; first += MOST) {
+    hipLaunchKernelGGL((gemm_experts_rows<MT, KS, ACT>), dim3((unsigned)(grid - first < MOST ? grid - first : MOST)), dim3(512), lds, stream, g,
+                       (uint32_t)first, ch, (int)nt, div_by((uint32_t)g.per));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <bool ACT>

@@ -569,7 +569,7 @@ hipError_t launch(const LogprobArgs &a, void *ws, hipStream_t stream) {
   const LogprobScratch at = logprob_scratch(a.T, p.parts, a.n, a.top);
   static_assert(sizeof(Part) == 16, "scratch of a part");
   const Scratch w{reinterpret_cast<Part *>(base), reinterpret_cast<uint64_t *>(base + at.keys), reinterpret_cast<int32_t *>(base + at.ranks)};
-  const int64_t most = launch_rows(64 * p.waves * p.parts);
+  const int64_t most = rows_of_launch(64 * p.waves * p.parts);
   for (int64_t t0 = 0; t0 < a.T; t0 += most) {
     const unsigned groups = (unsigned)((a.T - t0 < most ? a.T - t0 : most) * p.parts);
 #define PART(NV, WAVES) hipLaunchKernelGGL((logprobs_part<T, NV, WAVES>), dim3(groups), dim3(64 * WAVES), 0, stream, a, w, t0, p.parts, p.each)

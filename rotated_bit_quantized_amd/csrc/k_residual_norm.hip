@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(L > 256 ? L : 256) residual_norm_kernel(const 
 template <int L, int NV>
 hipError_t launch(const NormArgs &a, bool r_bf16, hipStream_t stream) {
   constexpr int THREADS = L > 256 ? L : 256, ROWS = THREADS / L;
-  constexpr int64_t MOST = launch_rows(THREADS) * ROWS;
+  constexpr int64_t MOST = rows_of_launch(THREADS) * ROWS;
   for (int64_t t0 = 0; t0 < a.T; t0 += MOST) {
     const dim3 grid((unsigned)(((a.T - t0 < MOST ? a.T - t0 : MOST) + ROWS - 1) / ROWS)), block(THREADS);
     if (r_bf16) hipLaunchKernelGGL((residual_norm_kernel<L, NV, true>), grid, block, 0, stream, a, t0);
