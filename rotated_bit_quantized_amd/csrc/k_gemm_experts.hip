@@ -615,40 +615,29 @@ __global__ void __launch_bounds__(64 * C::NW, C::NW / 4) gemm_experts_tile(const
   wait_vm<0>();  // copies into LDS that nobody waited for
 }
 
-// Most workgroups that n entries of E experts can need: row tiles times column
-// tiles, in 8 runs.
-template <int TM>
-int64_t most_tiles(const ExpertArgs &g, int64_t nt) {
-  return (nt * (g.n / TM + (g.E < g.n ? g.E : g.n)) + 7) / 8 * 8;
-}
-
 // Tiles need more than NSLOT stages.
 template <class C, bool ACT>
-hipError_t launch_tile(const ExpertArgs &g, hipStream_t stream) {
+hipError_t launch_tile(const ExpertArgs &g, const ExpertPlan &p, hipStream_t stream) {
+  static_assert(C::BM == EXPERT_BM && C::BN == EXPERT_BN && C::MIN_STAGES == EXPERT_STAGES, "the plan's tiles");
   static std::atomic<bool> attr_set[64];
   const hipError_t e = lds_limit_once((const void *)gemm_experts_tile<C, ACT>, C::LDS, attr_set);
   if (e != hipSuccess) return e;
-  const int64_t nt = ((ACT ? g.N / 2 : g.N) + (ACT ? C::BN / 2 : C::BN) - 1) / (ACT ? C::BN / 2 : C::BN);
-  int64_t grid = most_tiles<C::BM>(g, nt);
-  if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
-  const int64_t cus = device_cus() < 8 ? 8 : device_cus() / 8 * 8;
-  if (grid > cus) grid = cus;
-  hipLaunchKernelGGL((gemm_experts_tile<C, ACT>), dim3((unsigned)grid), dim3(64 * C::NW), C::LDS, stream, g, (int)nt, div_by((uint32_t)g.per));
+  const int64_t cus = device_cus() < 8 ? 8 : device_cus() / 8 * 8, grid = p.grid < cus ? p.grid : cus;
+  hipLaunchKernelGGL((gemm_experts_tile<C, ACT>), dim3((unsigned)grid), dim3(64 * C::NW), C::LDS, stream, g, (int)p.columns,
+                     div_by((uint32_t)g.per));
   return hipGetLastError();
 }
 
 template <int MT, int KS, bool ACT>
-hipError_t launch_rows(const ExpertArgs &g, hipStream_t stream) {
-  constexpr int TM = 16 * MT, OUT = (ACT ? 16 : 32) * (8 / KS), PART = 8 * MT * 2 * 1024;
-  const int64_t nt = ((ACT ? g.N / 2 : g.N) + OUT - 1) / OUT, grid = most_tiles<TM>(g, nt);
-  if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
+hipError_t launch_rows(const ExpertArgs &g, const ExpertPlan &p, hipStream_t stream) {
+  constexpr int TM = 16 * MT, PART = 8 * MT * 2 * 1024;
   int ch = 65536 / TM / 1024 * 1024;
   if (ch > (g.K + 1023) / 1024 * 1024) ch = (g.K + 1023) / 1024 * 1024;
   const size_t lds = (size_t)TM * ch > PART || KS == 1 ? (size_t)TM * ch : PART;
   constexpr int64_t MOST = rows_of_launch(512) / 8 * 8;  // workgroups, whole turns of the XCDs
-  for (int64_t first = 0; first < grid; first += MOST) {
-    hipLaunchKernelGGL((gemm_experts_rows<MT, KS, ACT>), dim3((unsigned)(grid - first < MOST ? grid - first : MOST)), dim3(512), lds, stream, g,
-                       (uint32_t)first, ch, (int)nt, div_by((uint32_t)g.per));
+  for (int64_t first = 0; first < p.grid; first += MOST) {
+    hipLaunchKernelGGL((gemm_experts_rows<MT, KS, ACT>), dim3((unsigned)(p.grid - first < MOST ? p.grid - first : MOST)), dim3(512), lds, stream, g,
+                       (uint32_t)first, ch, (int)p.columns, div_by((uint32_t)g.per));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -657,24 +646,14 @@ hipError_t launch_rows(const ExpertArgs &g, hipStream_t stream) {
 
 template <bool ACT>
 hipError_t launch(const ExpertArgs &g, hipStream_t stream) {
-  using Big = Tile<2, 2, 2, 4, 3>;
-  const int64_t cus = device_cus(), outs = ACT ? g.N / 2 : g.N, reached = g.E < g.n ? g.E : g.n;  // experts with entries, at most
-  const int64_t tiles = reached * ((g.N + Big::BN - 1) / Big::BN);
-  // The persistent tiles stream weights as well as anything (16 x 8 entries of 128 experts,
-  // 2048 -> 1536: 46.5 us, 5.6 TB/s, gemm_experts_rows 51; 64 x 8 71 and 76; 256 x 8 78 and 98),
-  // except where there are too few for half of the CUs: 1 x 8 19.3, rows 11.2; 2 x 2 of 8
-  // experts, 4096 -> 7168, 30 and 23; 4 x 2 42 and 50.
-  const bool small = g.K <= 128 * (Big::MIN_STAGES - 1);
-  if (!small && (tiles > cus / 2 || g.n > 32 * (int64_t)g.E)) return launch_tile<Big, ACT>(g, stream);
-  if (g.n > 16 * (int64_t)g.E && small) return launch_rows<4, 1, ACT>(g, stream);
-  // k is split over as many wavefronts as leave the CUs one workgroup each (1 x 4 of 60, 1408 ->
-  // 2048: 7.1 us with 8, 8.3 with 4, 15 with 1; 4 x 4: 18.6 with 8, 12.9 with 2)
-  const int64_t rows = reached + g.n / 16, blocks = (outs + (ACT ? 15 : 31)) / (ACT ? 16 : 32);
-  auto fits = [&](int64_t ks) { return rows * ((blocks * ks + 7) / 8) <= cus + cus / 8; };
-  if (fits(8)) return launch_rows<1, 8, ACT>(g, stream);
-  if (fits(4)) return launch_rows<1, 4, ACT>(g, stream);
-  if (fits(2)) return launch_rows<1, 2, ACT>(g, stream);
-  return launch_rows<1, 1, ACT>(g, stream);
+  const ExpertPlan p = expert_plan(g.n, g.K, g.N, g.E, ACT);
+  if (p.grid > 0x7fffffff) return hipErrorInvalidConfiguration;
+  if (p.mt == 0) return launch_tile<Tile<2, 2, 2, 4, 3>, ACT>(g, p, stream);
+  if (p.mt == 4) return launch_rows<4, 1, ACT>(g, p, stream);
+  if (p.ks == 8) return launch_rows<1, 8, ACT>(g, p, stream);
+  if (p.ks == 4) return launch_rows<1, 4, ACT>(g, p, stream);
+  if (p.ks == 2) return launch_rows<1, 2, ACT>(g, p, stream);
+  return launch_rows<1, 1, ACT>(g, p, stream);
 }
 
 }  // namespace

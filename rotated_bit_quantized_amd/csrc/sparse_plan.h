@@ -1,5 +1,5 @@
-// How routing and log probabilities divide their work: host code of its own, for
-// the launchers, the workspace queries and tests on the CPU.
+// How routing, the experts' products and log probabilities divide their work: host code
+// of its own, for the launchers, the workspace queries and tests on the CPU.
 #pragma once
 #include "oq_internal.h"
 
@@ -29,6 +29,17 @@ struct RoutePlan {
   int chunks;
 };
 RoutePlan route_plan(int64_t T, const oq_router &r);
+
+// ----------------------------------------------------- experts' products --
+// The persistent kernel's tiles: entries x weight rows, and the fewest stages of 128 k of one.
+constexpr int EXPERT_BM = 128, EXPERT_BN = 256, EXPERT_STAGES = 4;
+
+struct ExpertPlan {
+  int mt, ks;      // 16 mt entries a workgroup, k over ks of its 8 wavefronts; mt 0: persistent tiles
+  int64_t columns; // column tiles
+  int64_t grid;    // most tiles that n entries of E experts can need, in 8 runs
+};
+ExpertPlan expert_plan(int64_t n, int K, int N, int E, bool act);
 
 // -------------------------------------------------------- log probabilities --
 struct LogprobPlan {

@@ -26,6 +26,28 @@ size_t route_ws(int64_t T, const oq_router &r) {
   return p.solo ? 0 : (size_t)p.chunks * r.experts * 4;
 }
 
+ExpertPlan expert_plan(int64_t n, int K, int N, int E, bool act) {
+  const int64_t cus = device_cus(), outs = act ? N / 2 : N, reached = E < n ? E : n;  // experts with entries, at most
+  auto plan = [&](int mt, int ks) {
+    const int rows = mt ? 16 * mt : EXPERT_BM, wide = (mt ? 32 * (8 / ks) : EXPERT_BN) / (act ? 2 : 1);
+    const int64_t columns = (outs + wide - 1) / wide;
+    return ExpertPlan{mt, ks, columns, (columns * (n / rows + reached) + 7) / 8 * 8};
+  };
+  const int64_t tiles = reached * ((N + EXPERT_BN - 1) / EXPERT_BN);
+  // The persistent tiles stream weights as well as anything (16 x 8 entries of 128 experts,
+  // 2048 -> 1536: 46.5 us, 5.6 TB/s, gemm_experts_rows 51; 64 x 8 71 and 76; 256 x 8 78 and 98),
+  // except where there are too few for half of the CUs: 1 x 8 19.3, rows 11.2; 2 x 2 of 8
+  // experts, 4096 -> 7168, 30 and 23; 4 x 2 42 and 50.
+  const bool small = K <= 128 * (EXPERT_STAGES - 1);
+  if (!small && (tiles > cus / 2 || n > 32 * (int64_t)E)) return plan(0, 1);
+  if (n > 16 * (int64_t)E && small) return plan(4, 1);
+  // k is split over as many wavefronts as leave the CUs one workgroup each (1 x 4 of 60, 1408 ->
+  // 2048: 7.1 us with 8, 8.3 with 4, 15 with 1; 4 x 4: 18.6 with 8, 12.9 with 2)
+  const int64_t rows = reached + n / 16, blocks = (outs + (act ? 15 : 31)) / (act ? 16 : 32);
+  auto fits = [&](int64_t ks) { return rows * ((blocks * ks + 7) / 8) <= cus + cus / 8; };
+  return plan(1, fits(8) ? 8 : fits(4) ? 4 : fits(2) ? 2 : 1);
+}
+
 LogprobPlan logprob_plan(int64_t T, int V, int bytes, int lead, int top) {
   const int ve = 16 / bytes;
   const int pieces = (V + lead + ve - 1) / ve;
