@@ -58,12 +58,12 @@ __device__ __forceinline__ void unpack8(float (&x)[8], const u32x4 raw) {
 
 // HPG heads of one token per lane group of L lanes.
 template <int L, int KIND, int HPG>
-__global__ void __launch_bounds__(256) heads_kernel(const HeadArgs a, const int chunks0, const int chunks) {
+__global__ void __launch_bounds__(256) heads_kernel(const HeadArgs a, const int64_t t0, const int chunks0, const int chunks) {
   __shared__ float stage[KIND == ROPE_ANY ? 256 * 8 : 1];
   const int lane = threadIdx.x & 63;
   const int g = threadIdx.x / L, gl = threadIdx.x % L;  // lane group of the workgroup, lane of the group
   const int c = blockIdx.x % chunks;
-  const int64_t t = (int64_t)(blockIdx.x / chunks) * (256 / L) + g;
+  const int64_t t = t0 + (int64_t)(blockIdx.x / chunks) * (256 / L) + g;
   if (KIND != ROPE_ANY && t >= a.T) return;
   const bool live = t < a.T;
   const int pi = c >= chunks0 ? 1 : 0;
@@ -214,11 +214,14 @@ __global__ void __launch_bounds__(256) heads_kernel(const HeadArgs a, const int 
 template <int L, int KIND, int HPG>
 hipError_t launch_l(const HeadArgs &a, hipStream_t stream) {
   const int c0 = (a.part[0].heads + HPG - 1) / HPG, c1 = (a.part[1].heads + HPG - 1) / HPG;
-  const int64_t per = 256 / L;
-  const int64_t blocks = (a.T + per - 1) / per * (c0 + c1);
-  if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((heads_kernel<L, KIND, HPG>), dim3((unsigned)blocks), dim3(256), 0, stream, a, c0, c0 + c1);
-  return hipGetLastError();
+  const int64_t per = 256 / L, most = rows_of_launch(256 * (c0 + c1)) * per;  // tokens of a launch
+  for (int64_t t0 = 0; t0 < a.T; t0 += most) {
+    const int64_t blocks = ((a.T - t0 < most ? a.T - t0 : most) + per - 1) / per * (c0 + c1);
+    hipLaunchKernelGGL((heads_kernel<L, KIND, HPG>), dim3((unsigned)blocks), dim3(256), 0, stream, a, t0, c0, c0 + c1);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <int KIND, int HPG>

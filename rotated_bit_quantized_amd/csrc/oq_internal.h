@@ -442,6 +442,9 @@ hipError_t launch_logprobs(const LogprobArgs &a, bool bf16, void *ws, hipStream_
 
 // Compute units of the current device (cached per device).
 int device_cus();
+// Rows of `threads` threads each that one launch takes: HIP takes fewer than 2^32 threads
+// (at 2^32 it returns an error, beyond it runs what is left of them).
+constexpr int64_t rows_of_launch(int64_t threads) { return 0xFFFFFFFFll / threads; }
 // Matrix-core rate probe (oq_probe_mfma): launches it and returns the number
 // of operations (2 M N K per instruction) one launch performs in *ops.
 hipError_t launch_mfma_probe(int kind, int iters, float *sink, hipStream_t stream, double *ops);

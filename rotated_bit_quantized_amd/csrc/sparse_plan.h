@@ -5,9 +5,6 @@
 
 namespace oq {
 
-// Rows of `threads` threads each that one launch takes: HIP refuses 2^32 threads and more.
-constexpr int64_t rows_of_launch(int64_t threads) { return 0xFFFFFFFFll / threads; }
-
 // ------------------------------------------------------------------ routing --
 constexpr int ROUTE_WAVES = 16;  // of a workgroup; chunks are whole rounds of them
 // Up to SOLO tokens one workgroup routes and lists; CHUNKS, LISTS: most workgroups
