@@ -626,13 +626,13 @@ __device__ __forceinline__ float wave_all(float v, F f) {
 // 9.7 us, 11.4 with early loads.
 template <int D, int WAVES>
 __global__ void __launch_bounds__(256)
-attn_join_kernel(const AttnArgs a, int rows, int parts, const float *__restrict__ part_o, const float2 *__restrict__ part_ml) {
+attn_join_kernel(const AttnArgs a, int64_t first, int rows, int parts, const float *__restrict__ part_o, const float2 *__restrict__ part_ml) {
   constexpr int L = D / 4, AT = 64 / L, STEP = WAVES == 4 ? 4 * AT : AT;
   constexpr int BATCH = WAVES == 0 ? 0 : 64 / STEP < 8 ? 64 / STEP : 8;
   __shared__ float4 sum[WAVES == 4 ? 4 : 1][L];
   const int64_t all = (int64_t)rows * a.kv.heads;
   const int wave = threadIdx.x >> 6;
-  const int64_t id = WAVES == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
+  const int64_t id = WAVES == 4 ? (int64_t)blockIdx.x : (first + blockIdx.x) * 4 + wave;
   const int lane = threadIdx.x & 63, gl = lane % L, sub = (WAVES == 4 ? wave * AT : 0) + lane / L;
   if (id >= all) return;
   float m = -INFINITY, l = 0.f;
@@ -709,7 +709,7 @@ hipError_t launch_d(const AttnArgs &a, Plan &p, float *po, float2 *pm, hipStream
   Launch &lp = p.launch;
   int64_t wide = 0, narrow = 0;
   for (PartPlan &q : lp.part) (q.wide ? wide : narrow) += q.items;
-  if (wide + narrow > 0x7fffffff || (p.rows_all + 3) / 4 > 0x7fffffff) return hipErrorInvalidConfiguration;
+  if (wide + narrow > 0x7fffffff) return hipErrorInvalidConfiguration;
   lp.wide_items = (int)wide;
   lp.narrow_items = (int)narrow;
   lp.waves = wide ? 8 : 1;
@@ -726,6 +726,7 @@ hipError_t launch_d(const AttnArgs &a, Plan &p, float *po, float2 *pm, hipStream
     if (e != hipSuccess) return e;
     const int lds = wide ? MOST : ONE + 1024;
     const int64_t blocks = wide + (narrow + lp.waves - 1) / lp.waves;
+    if (blocks > rows_of_launch(64 * lp.waves)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(attn_part_kernel<D>, dim3((unsigned)blocks), dim3(64 * lp.waves), lds, stream, a, lp, po, pm);
     const hipError_t r = hipGetLastError();
     if (r != hipSuccess) return r;
@@ -736,8 +737,13 @@ hipError_t launch_d(const AttnArgs &a, Plan &p, float *po, float2 *pm, hipStream
   const auto join = shared                ? attn_join_kernel<D, 4>
                     : p.rows_all <= 4096 ? attn_join_kernel<D, 1>
                                           : attn_join_kernel<D, 0>;
-  hipLaunchKernelGGL(join, dim3((unsigned)blocks), dim3(256), 0, stream, a, p.rows, p.parts, po, pm);
-  return hipGetLastError();
+  constexpr int64_t MOST = rows_of_launch(256);
+  for (int64_t first = 0; first < blocks; first += MOST) {
+    hipLaunchKernelGGL(join, dim3((unsigned)(blocks - first < MOST ? blocks - first : MOST)), dim3(256), 0, stream, a, first, p.rows, p.parts, po, pm);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
