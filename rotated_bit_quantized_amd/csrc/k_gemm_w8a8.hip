@@ -403,16 +403,27 @@ __global__ void __launch_bounds__(512) gemm_w8a8_rows(const GemmArgs g, const in
 }
 
 template <class C>
-hipError_t launch_tile(const GemmArgs &g, hipStream_t stream) {
+hipError_t launch_tile(const GemmArgs &all, hipStream_t stream) {
   static std::atomic<bool> attr_set[64];
   const hipError_t e = lds_limit_once((const void *)gemm_w8a8_tile<C>, C::LDS, attr_set);
   if (e != hipSuccess) return e;
-  const int64_t mt = (g.M + C::BM - 1) / C::BM, nt = (g.N + C::BN - 1) / C::BN;
-  if (mt * nt > 0x7fffffff || 8 * nt > 0x7fffffff) return hipErrorInvalidConfiguration;
-  const int tiles = (int)(mt * nt);
-  const TileMap t{(int)mt, (int)nt, tiles / 8, tiles % 8, div_by((uint32_t)(8 * nt)), div_by(8), div_by(mt % 8 ? (uint32_t)(mt % 8) : 8)};
-  hipLaunchKernelGGL(gemm_w8a8_tile<C>, dim3((unsigned)tiles), dim3(64 * C::NW), C::LDS, stream, g, t);
-  return hipGetLastError();
+  const int64_t nt = (all.N + (int64_t)C::BN - 1) / C::BN, most = rows_of_launch(64 * C::NW) / nt * C::BM;  // tokens of a launch
+  if (most == 0) return hipErrorInvalidConfiguration;
+  for (int64_t m = 0; m < all.M; m += most) {
+    GemmArgs g = all;
+    g.qa += m * g.lda;
+    g.a_scale += m;
+    if (g.mean) g.mean += m;
+    g.y += m * g.ldy;
+    g.M = all.M - m < most ? all.M - m : most;
+    const int64_t mt = (g.M + C::BM - 1) / C::BM;
+    const int tiles = (int)(mt * nt);
+    const TileMap t{(int)mt, (int)nt, tiles / 8, tiles % 8, div_by((uint32_t)(8 * nt)), div_by(8), div_by(mt % 8 ? (uint32_t)(mt % 8) : 8)};
+    hipLaunchKernelGGL(gemm_w8a8_tile<C>, dim3((unsigned)tiles), dim3(64 * C::NW), C::LDS, stream, g, t);
+    const hipError_t r = hipGetLastError();
+    if (r != hipSuccess) return r;
+  }
+  return hipSuccess;
 }
 
 template <int MT>
