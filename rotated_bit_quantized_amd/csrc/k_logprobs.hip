@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES <= 8 ? 6 : 4) logprobs_part(
   // RN(ref c) in one step, whose only rounding is z's, and m's error off the sums
   // afterwards: up to |m| = 2^20, where it is below 2^-4.  The elements of a thread that
   // holds a largest one are then summed again, a lane each; of many such threads, and
-  // beyond 2^20, every element is looked at (2048 x 131072: 130 us; 140 where every
+  // beyond 2^20, every element is looked at (2048 x 131072: 128 us; 140 where every
   // wavefront with a largest one looks at all of its elements).
   float s = 0.f, sum_t = 0.f;
   int largest_ones = 0;
@@ -263,22 +263,20 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES <= 8 ? 6 : 4) logprobs_part(
     sum_t = __builtin_fmaf(e, fmaxf(z, -1024.f), sum_t);  // 2^-inf takes no part
   };
   const float m = ref * c;
-  uint64_t owners = __ballot(mine == ref);
-  if (fabsf(m) < 0x1p20f && __popcll(owners) <= 8) {
+  const uint64_t owners = __ballot(mine == ref);
+  if (fabsf(m) < 0x1p20f && __popcll(owners) <= HELD / WAVES) {
+    u32x4 *own = s_held + wave * (HELD / WAVES * NV);  // nobody else's until the next barrier
+    if (mine == ref) {
+      u32x4 *to = own + NV * __popcll(owners & ((1ull << lane) - 1));
+#pragma unroll
+      for (int v = 0; v < NV; ++v) to[v] = raw[v];
+    }
     sums([&](float x) { add(__builtin_fmaf(x, c, -m)); });
     if (mine == ref) s = sum_t = 0.f;
-    u32x4 *own = s_held + wave * NV;  // nobody else's until the next barrier
-    for (; owners; owners &= owners - 1) {
-      if (lane == __ffsll((long long)owners) - 1) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v) own[v] = raw[v];
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      const bool in = lane < NV * VE;
-      const float x = in ? logit(reinterpret_cast<const T *>(own), lane) : -INFINITY;
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    for (int h = 0; h < __popcll(owners); ++h) {
+      const float x = lane < NV * VE ? logit(reinterpret_cast<const T *>(own + h * NV), lane) : -INFINITY;
       add(x == ref ? -INFINITY : __builtin_fmaf(x, c, -m));
       largest_ones += __popcll(__ballot(x == ref));
     }
@@ -331,13 +329,8 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES <= 8 ? 6 : 4) logprobs_part(
     if (lane == 0 && count) atomicAdd(s_rank + i, count);
   }
   __syncthreads();
-  Part stat{ref, 0.f, 0.f, 0.f};
-  float ones = 0.f;
-#pragma unroll
-  for (int w = 0; w < WAVES; ++w) stat.rest += s_sum[w], stat.t += s_sum[WAVES + w], ones += s_sum[2 * WAVES + w];
-  stat.rest = top == INFINITY ? NAN : stat.rest + (ones - 1.f);
-  const float log_s = log_sum(stat.rest);
-
+  int n_list = 0, rank = 0;  // of the listed candidates, a thread each
+  uint64_t key = 0;
   if (a.top > 0) {
     const uint32_t lowest = order_of(-INFINITY);
     uint32_t limit = s_limit;
@@ -431,22 +424,30 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES <= 8 ? 6 : 4) logprobs_part(
       if (have < a.top) collect_first(1, a.top - have);
       __syncthreads();
     }
-    const int n = s_count[0];
-    const uint64_t key = (int)threadIdx.x < n ? s_list[threadIdx.x] : 0;
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += s_list[j] > key;
-    if (parts == 1) {
-      if ((int)threadIdx.x < n && rank < a.top) {
-        a.top_id[t * a.top + rank] = (int32_t)~(uint32_t)key;
-        a.top_logprob[t * a.top + rank] = log_prob(value_of((uint32_t)(key >> 32)), a.scale, stat, log_s);
-      }
-    } else {
+    n_list = s_count[0];
+    if (64 * wave < n_list) {
+      key = (int)threadIdx.x < n_list ? s_list[threadIdx.x] : 0;
+      for (int j = 0; j < n_list; ++j) rank += s_list[j] > key;
+    }
+    if (parts > 1) {
       uint64_t *keys = ws.keys + ((int64_t)t * parts + part) * a.top;
-      if ((int)threadIdx.x < n && rank < a.top) keys[rank] = key;
-      if ((int)threadIdx.x >= n && (int)threadIdx.x < a.top) keys[threadIdx.x] = 0;
+      if ((int)threadIdx.x < n_list && rank < a.top) keys[rank] = key;
+      if ((int)threadIdx.x >= n_list && (int)threadIdx.x < a.top) keys[threadIdx.x] = 0;
     }
   }
+  // the first wavefront's threads have the row's or part's values, those of the list alternatives
+  if (wave > 0 && (parts > 1 || 64 * wave >= n_list)) return;
+  Part stat{ref, 0.f, 0.f, 0.f};
+  float ones = 0.f;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) stat.rest += s_sum[w], stat.t += s_sum[WAVES + w], ones += s_sum[2 * WAVES + w];
+  stat.rest = top == INFINITY ? NAN : stat.rest + (ones - 1.f);
+  const float log_s = log_sum(stat.rest);
   if (parts == 1) {
+    if ((int)threadIdx.x < n_list && rank < a.top) {
+      a.top_id[t * a.top + rank] = (int32_t)~(uint32_t)key;
+      a.top_logprob[t * a.top + rank] = log_prob(value_of((uint32_t)(key >> 32)), a.scale, stat, log_s);
+    }
     if (threadIdx.x == 0) row_outputs(a, t, stat, log_s);
     if ((int)threadIdx.x < a.n) token_outputs(a, row, t, threadIdx.x, stat, log_s, s_rank[threadIdx.x]);
   } else {
