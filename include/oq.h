@@ -790,7 +790,7 @@ int oq_residual_norm(const uint16_t *y, int64_t y_ld, int32_t k, const float *we
  * an entropy likewise, and never below 0.  (Terms below 2^-126 of the largest may count as 0.)
  * Each output nullable but logprob and rank with n > 0, and the top pair with
  * top > 0.  Rows need the alignment of their element only.
- * 1 <= V <= 2^21, 0 <= n <= 64, 0 <= top <= 32, top <= V, scale > 0 and its
+ * T <= 2^24, 1 <= V <= 2^21, 0 <= n <= 64, 0 <= top <= 32, top <= V, scale > 0 and its
  * product with log2(e) finite.
  * ws: device scratch of oq_logprobs_ws_bytes(T, V, n, top) bytes, 16-byte
  * aligned (may be 0).

@@ -15,11 +15,12 @@
 // What bounds it.  Few entries an expert: the weights, read once, at copy rate
 // (16 x 8 entries of 128 experts, 2048 -> 1536: 41 to 47 us, 260 MB; a copy of as
 // many bytes takes 50).  Many: the matrix unit at the clock that power allows, a stage
-// of 128 k of a 128 x 256 tile a CU in 1.0 us (2.15 POP/s, as the library's int8
-// products), and what is not product: 3 us between two tiles, 1.2 us of epilogue, 2 us
-// of stores, a sixteenth to an eighth of the rows empty in the experts' last tiles.
-// 8192 x 8 entries of 128 experts, 2048 -> 1536: 274 to 302 us of 191 for the products
-// alone; 4096 k, 64 experts: 478 of 382.
+// of 128 k of a 128 x 256 tile a CU in 1.0 us (2.15 POP/s; the library's largest int8
+// product reaches 2.4), and what is not product: 3 us between two tiles, 1.2 us of
+// epilogue, 2 us of stores, a sixteenth to an eighth of the rows empty in the experts' last
+// tiles.  8192 x 8 entries of 128 experts, 2048 -> 1536: 274 to 302 us of 172 for the
+// products alone at the library's rate; 4096 k, 64 experts: 465 of 344; 768 -> 2048: 207 of 100.
+// Outputs that 16-byte stores do not fit (N or ldy no multiple of 8) go two bytes at a time.
 #include "sparse_plan.h"
 
 namespace oq {

@@ -13,8 +13,10 @@
 // pieces of 16 bytes all in flight at once and held in registers as they came: the
 // maximum is known before the first exponential, so nothing is rescaled, and what comes
 // after it (ranks, best alternatives) reads registers.  Measured: 2048 x 131072
-// bfloat16 114 to 127 us by cards, 7 of them the join (4.2 to 4.7 TB/s; with values unpacked
-// once and kept, one workgroup a CU, 550); 77 x 100003 11 and 5; 1 x 32000 float32 8, a launch.
+// bfloat16 119 to 135 us by cards and by what ran before, 7 of them the join (4.0 to 4.5
+// TB/s; with values unpacked once and kept, one workgroup a CU, 550); 77 x 100003 12 and
+// 5; 1 x 32000 float32 8, a launch.  Comparisons below and at the plan are of ten calls in
+// a graph on one card, where the first takes 127 to 130.
 //
 // Alternatives: the `top`-th largest of 64 maxima (over the threads of one lane
 // number) is a threshold that at least `top` elements reach and hardly more do.  The
@@ -153,8 +155,8 @@ __device__ __forceinline__ float largest(const u32x4 (&raw)[NV]) {
 
 // Pieces part * each .. (part + 1) * each - 1 of a row (from row t0 on), NV a thread at most, by
 // WAVES wavefronts.  24 wavefronts fit a CU, three workgroups of 8 or six of 4, whose loads
-// run under each other's arithmetic (2048 x 131072: 133 us; 32 wavefronts, with 64
-// registers a thread, spill: 163).
+// run under each other's arithmetic (2048 x 131072 with 32 wavefronts, whose 64
+// registers a thread spill: a fifth more).
 template <class T, int NV, int WAVES>
 __global__ void __launch_bounds__(64 * WAVES, WAVES <= 8 ? 6 : 4) logprobs_part(const LogprobArgs a, const Scratch ws, const int64_t t0, const int parts, const int each) {
   constexpr int THREADS = 64 * WAVES, LIST = THREADS < 512 ? THREADS : 512;  // a thread for each listed candidate
