@@ -726,10 +726,20 @@ hipError_t launch_d(const AttnArgs &a, Plan &p, float *po, float2 *pm, hipStream
     if (e != hipSuccess) return e;
     const int lds = wide ? MOST : ONE + 1024;
     const int64_t blocks = wide + (narrow + lp.waves - 1) / lp.waves;
-    if (blocks > rows_of_launch(64 * lp.waves)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(attn_part_kernel<D>, dim3((unsigned)blocks), dim3(64 * lp.waves), lds, stream, a, lp, po, pm);
-    const hipError_t r = hipGetLastError();
-    if (r != hipSuccess) return r;
+    const int64_t most = rows_of_launch(64 * lp.waves);
+    if (wide > most) return hipErrorInvalidConfiguration;
+    if (lp.lead > most - wide) lp.lead = 0;  // the first launch holds all wide items
+    for (int64_t first = 0; first < blocks; first += most) {
+      Launch some = lp;
+      if (first > 0) {  // single wavefronts' workgroups alone, counted on from the first launch's
+        some.lead = 0;
+        some.wide_items = (int)(wide - first);
+      }
+      hipLaunchKernelGGL(attn_part_kernel<D>, dim3((unsigned)(blocks - first < most ? blocks - first : most)), dim3(64 * lp.waves), lds, stream, a,
+                         some, po, pm);
+      const hipError_t r = hipGetLastError();
+      if (r != hipSuccess) return r;
+    }
   }
   if (lp.direct) return hipSuccess;
   const bool shared = p.rows_all <= 512;
