@@ -435,10 +435,16 @@ hipError_t launch_prepack_w16(const uint8_t *w, const float *ws, int N, int K, i
 hipError_t launch_lm_expand(const uint8_t *codes, int64_t ldc, int nibbles, const uint16_t *levels, int nlev,
                             int64_t M, int K, uint8_t *out, hipStream_t stream) {
   if (M == 0) return hipSuccess;
-  const int64_t total = (M + 31) / 32 * (K / 16) * 64;
-  hipLaunchKernelGGL(lm_expand_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, stream, codes, ldc,
-                     nibbles, levels, nlev, M, K, out);
-  return hipGetLastError();
+  const int64_t block = (int64_t)(K / 16) * 64, most = rows_of_launch(256) * 256 / block * 32;  // threads of 32 rows, rows of a launch
+  if (most == 0) return hipErrorInvalidConfiguration;
+  for (int64_t m = 0; m < M; m += most) {
+    const int64_t rows = M - m < most ? M - m : most, total = (rows + 31) / 32 * block;
+    hipLaunchKernelGGL(lm_expand_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, stream, codes + m * ldc, ldc,
+                       nibbles, levels, nlev, rows, K, out + m / 32 * block * 16);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace oq
